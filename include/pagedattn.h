@@ -59,6 +59,7 @@ typedef enum { PA_OUT_F32 = 0, PA_OUT_BF16 = 1 } pa_out_dtype;
 #define PA_DEV_BAD_PAGE 2    /* a block_table entry that is read lies outside [0, num_pages) */
 #define PA_DEV_BAD_SLOT 4    /* reshape_and_cache: slot >= num_pages * block_size */
 #define PA_DEV_TIMEOUT 8     /* a bounded wait inside a kernel gave up (never expected) */
+#define PA_DEV_NO_PAGES 16   /* extend_block_tables: the pool ran out before a request's new pages */
 
 /* Shape and launch description of one attention call.
  *   num_seqs          B, number of sequences (>= 0; 0 is a no-op)
@@ -298,6 +299,149 @@ pa_status pa_paged_attention_verify_fp8(const void *q, const void *k_cache, cons
                                         const int32_t *block_table, const int32_t *seq_lens,
                                         const pa_attn_desc *desc, void *out, void *workspace,
                                         size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* ---- fp4 KV cache -----------------------------------------------------------
+ * A cache in 4.5 bits per element, for contexts whose e4m3 cache would not fit
+ * or whose decode time is KV bytes (the RTX 3090 page keeps its 128K context in
+ * a 4-bit format for both reasons).  An element x of KV head h is held as an
+ * e2m1 code (values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one
+ * e4m3 scale S per 16 consecutive dims of its row and one binary32 scale g =
+ * k_scale[h] or v_scale[h], chosen by the caller (finite and > 0; for example
+ * max |x| / 2688 over a calibration set, 2688 = 6 * 448):
+ *     S    = e4m3(max |x of the 16| / (6 g))
+ *     code = e2m1(x * (1 / (S g)))
+ *     x   ~= code * S * g
+ * Every product and quotient is rounded to binary32, the conversions round to
+ * nearest even and saturate (at 448 and at 6).  A block whose S is 0 has codes
+ * 0; a NaN anywhere in a block gives S = NaN (0x7F) and codes 0.
+ *
+ * A cache tensor is uint8 [num_pages, num_kv_heads, block_size / 16, 9 * D]:
+ * the 16 tokens of a (page, KV head) chunk form one record of 8 D code bytes
+ * and D scale bytes.  Inside a record (low nibble = the even dim of a pair;
+ * / and % on integers):
+ *   K code of token t, dims d, d + 1 (d even), blk = d / 16:
+ *       (blk / 8 * 2 + t / 8) * 512 + t % 8 * 64 + d % 16 / 4 * 16 + blk % 8 * 2 + d % 4 / 2
+ *   K scale of (t, blk):   8 D + t * D / 16 + blk
+ *   V code of token t, dims d, d + 1, u = t / 8 * 2 + t % 2:
+ *       u * 2 D + (d % 16 / 2 * 4 + t % 8 / 2) * D / 16 + blk
+ *   V scale of (t, blk):   8 D + blk / 4 * 64 + t % 8 / 2 * 16 + blk % 4 * 4 + u
+ * A page is contiguous, so pages can be copied, swapped and shared as those of
+ * the other caches.  head_dim is 128 or 256, block_size a multiple of 16
+ * (PA_ERR_UNSUPPORTED otherwise). */
+
+/* reshape_and_cache into an fp4 cache: the slot rules of pa_reshape_and_cache,
+ * each row quantised as above (bit for bit).  The non-negative slots of a call
+ * are distinct (two tokens with one slot leave a mixture of both rows).
+ *   k_new, v_new     device bf16 [num_tokens, num_kv_heads, head_dim]
+ *   k_cache, v_cache device uint8 records, written in place
+ *   k_scale, v_scale device float [num_kv_heads] */
+pa_status pa_reshape_and_cache_fp4(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                   const int64_t *slot_mapping, const float *k_scale, const float *v_scale,
+                                   int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_pages, int32_t *device_status, void *stream);
+
+/* gather_cache_fp4 -- the rows at the given slots read back as values (to move
+ * a request into another cache or to another worker, or to look at what was
+ * stored): k_out[i, h, :] = code * S * g, rounded to binary32 and, for bf16
+ * rows, once more to bf16.  A negative slot gives a row of zeros, as does one
+ * >= num_pages * block_size, which also sets PA_DEV_BAD_SLOT.
+ *   k_out, v_out     device [num_tokens, num_kv_heads, head_dim] of out_dtype */
+pa_status pa_gather_cache_fp4(const void *k_cache, const void *v_cache, const int64_t *slot_mapping,
+                              const float *k_scale, const float *v_scale, void *k_out, void *v_out,
+                              int32_t out_dtype, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t block_size, int64_t num_pages, int32_t *device_status, void *stream);
+
+/* paged_attention_decode over an fp4 cache: out as pa_paged_attention_decode
+ * with K_t = code * S * k_scale[kv head], V_t likewise.  Same plan, workspace,
+ * limits, window and flags as pa_paged_attention_decode.  The products run on
+ * code * S in f16 (exact; q enters scaled by a power of two, softmax weights as
+ * an f16 head and residual) with binary32 sums.  Slots past a sequence's end or
+ * before its window may hold any bytes.  A NaN in a visible row (a NaN scale)
+ * or in q makes the outputs that depend on it NaN. */
+pa_status pa_paged_attention_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scale, const float *v_scale,
+                                        const int32_t *block_table, const int32_t *seq_lens,
+                                        const pa_attn_desc *desc, void *out, void *workspace,
+                                        size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* paged_attention_decode_append over an fp4 cache: the new rows quantised as
+ * pa_reshape_and_cache_fp4 does (bit-exact), then the decode of
+ * pa_paged_attention_decode_fp4.  Arguments as for
+ * pa_paged_attention_decode_append_fp8. */
+pa_status pa_paged_attention_decode_append_fp4(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                               void *v_cache, const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const pa_attn_desc *desc, void *out, void *workspace,
+                                               size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* paged_attention_verify over an fp4 cache: out as pa_paged_attention_verify
+ * with K and V as for pa_paged_attention_decode_fp4.  Same plan, workspace,
+ * limits and errors as pa_paged_attention_verify. */
+pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scale, const float *v_scale,
+                                        const int32_t *block_table, const int32_t *seq_lens,
+                                        const pa_attn_desc *desc, void *out, void *workspace,
+                                        size_t workspace_bytes, int32_t *device_status, void *stream);
+
+/* ---- block tables and slot maps ---------------------------------------------
+ * The block table, seq_lens and slot_mapping that every call above takes, built
+ * on the device from request lengths, so that a serving step needs no copy of
+ * lengths to the host and can be captured into a graph.  The pool of free pages
+ * is a stack: free_pages[0 .. num_free) lists them.  A page belongs to one
+ * request.  Inputs and outputs are separate buffers (PA_ERR_INVALID_ARG where
+ * seq_lens or num_free_out is an input's address): a step hands the outputs of
+ * one call to the next, and a replayed call gives the same result again.
+ *
+ * Both calls write the block table, which PA_FLAG_EARLY_KV_READ reads ahead of
+ * the stream order: the attention calls of a step that runs them on the same
+ * stream are given no such flag, unless work of another kind (not a kernel of
+ * this library) lies between. */
+
+/* extend_block_tables -- request b holds context_lens[b] tokens and gets
+ * num_new[b] more.  It takes the pages that context_lens[b] + num_new[b] tokens
+ * need beyond those of context_lens[b] from the top of the stack, requests in
+ * order, pages in order of position (the first page taken is
+ * free_pages[num_free - 1]), and they are entered in its block-table row.  The
+ * new tokens are packed request by request (row i of k_new is the i-th of
+ * them); slot_mapping[i] is token i's slot, -1 for i past the last one.
+ * A request is refused -- seq_lens[b] = context_lens[b], slots -1, no pages --
+ * if its lengths are negative or exceed max_pages_per_seq * block_size
+ * (PA_DEV_BAD_SEQLEN), if the packed rows up to its last one exceed num_tokens
+ * (PA_DEV_BAD_SLOT), or if the pages wanted by all requests up to and including
+ * it exceed num_free (PA_DEV_NO_PAGES; it must want at least one itself).
+ *   context_lens, num_new  device int32 [num_seqs]
+ *   block_table            device int32 [num_seqs, max_pages_per_seq]; the entries of
+ *                          the pages taken are written, the others left as they are
+ *   free_pages             device int32 [num_pages], read; entries outside [0, num_pages)
+ *                          set PA_DEV_BAD_PAGE and give slots -1
+ *   num_free               device int32 [1]; outside [0, num_pages]: clamped, PA_DEV_BAD_PAGE
+ *   num_tokens             rows of slot_mapping
+ *   seq_lens               device int32 [num_seqs], out
+ *   slot_mapping           device int64 [num_tokens], out (every entry is written)
+ *   num_free_out           device int32 [1], out
+ * num_seqs <= 65535 and max_pages_per_seq * block_size < 2^31
+ * (PA_ERR_UNSUPPORTED otherwise). */
+pa_status pa_extend_block_tables(const int32_t *context_lens, const int32_t *num_new, int32_t *block_table,
+                                 const int32_t *free_pages, const int32_t *num_free, int32_t num_seqs,
+                                 int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
+                                 int32_t num_tokens, int32_t *seq_lens, int64_t *slot_mapping,
+                                 int32_t *num_free_out, int32_t *device_status, void *stream);
+
+/* release_block_tables -- the pages of every request with finished[b] != 0
+ * (those of its seq_lens[b] tokens) go back to the pool, requests in order,
+ * pages in order of position, above free_pages[num_free - 1];
+ * seq_lens_out[b] = 0 for them and seq_lens[b] for the others.  The block
+ * table is not written (entries of an empty request are never read).  A
+ * request whose pages would not fit under num_pages keeps them
+ * (PA_DEV_BAD_PAGE: more pages than the pool has; the same status reports an
+ * entry outside [0, num_pages), which is returned as it is).
+ *   free_pages  device int32 [num_pages], written from num_free on
+ * Other arguments and limits as for pa_extend_block_tables. */
+pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,
+                                  int32_t *free_pages, const int32_t *num_free, int32_t num_seqs,
+                                  int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
+                                  int32_t *seq_lens_out, int32_t *num_free_out, int32_t *device_status,
+                                  void *stream);
 
 /* Size of the scratch array that pa_paged_attention_decode_noalloc keeps in
  * device memory (8 MiB per GPU that loads the library, held until exit). */

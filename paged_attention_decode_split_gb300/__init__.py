@@ -12,7 +12,9 @@ missing or cannot be loaded, every call raises -- there is no fallback.
 
 Names follow the C ABI: ``reshape_and_cache``, ``paged_attention_decode``,
 ``paged_attention_decode_append``, ``paged_attention_verify``,
-``workspace_bytes``, ``last_plan``.
+``workspace_bytes``, ``last_plan``; ``_fp8`` and ``_fp4`` forms for quantised
+caches, ``gather_cache_fp4``, ``extend_block_tables``,
+``release_block_tables``.
 """
 from __future__ import annotations
 
@@ -29,11 +31,14 @@ __all__ = [
     "PA_ERR_CUDA", "PA_OUT_F32", "PA_OUT_BF16", "PA_DEV_BAD_SEQLEN", "PA_DEV_BAD_PAGE",
     "PA_DEV_BAD_SLOT", "PA_DEV_TIMEOUT", "PA_PATH_DECODE_CUDA_CORE", "PA_PATH_DECODE_MMA",
     "PA_PATH_VERIFY_TCGEN05", "PA_FLAG_EARLY_KV_READ", "PA_NOALLOC_SCRATCH_BYTES", "paged_attention_decode_noalloc",
+    "fp4_cache_shape", "reshape_and_cache_fp4", "gather_cache_fp4", "paged_attention_decode_fp4",
+    "paged_attention_decode_append_fp4", "paged_attention_verify_fp4", "extend_block_tables",
+    "release_block_tables", "PA_DEV_NO_PAGES",
 ]
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, 1, 2, 3, 4
 PA_OUT_F32, PA_OUT_BF16 = 0, 1
-PA_DEV_BAD_SEQLEN, PA_DEV_BAD_PAGE, PA_DEV_BAD_SLOT, PA_DEV_TIMEOUT = 1, 2, 4, 8
+PA_DEV_BAD_SEQLEN, PA_DEV_BAD_PAGE, PA_DEV_BAD_SLOT, PA_DEV_TIMEOUT, PA_DEV_NO_PAGES = 1, 2, 4, 8, 16
 PA_PATH_DECODE_CUDA_CORE, PA_PATH_DECODE_MMA, PA_PATH_VERIFY_TCGEN05 = 1, 2, 3
 PA_FLAG_EARLY_KV_READ = 1
 PA_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -78,7 +83,9 @@ _vp = ctypes.c_void_p
 _BOUND_ENTRIES = ("pa_paged_attention_decode", "pa_paged_attention_verify", "pa_paged_attention_decode_fp8",
                   "pa_paged_attention_verify_fp8", "pa_paged_attention_decode_append",
                   "pa_paged_attention_decode_append_fp8", "pa_paged_attention_decode_noalloc", "pa_reshape_and_cache",
-                  "pa_reshape_and_cache_fp8")
+                  "pa_reshape_and_cache_fp8", "pa_reshape_and_cache_fp4", "pa_gather_cache_fp4",
+                  "pa_paged_attention_decode_fp4", "pa_paged_attention_decode_append_fp4",
+                  "pa_paged_attention_verify_fp4", "pa_extend_block_tables", "pa_release_block_tables")
 
 
 def _load_binding(lib):
@@ -129,7 +136,17 @@ def load_library(path: str | None = None):
         lib.pa_reshape_and_cache_fp8.restype = ctypes.c_int
         lib.pa_reshape_and_cache_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32,
                                                  ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, _vp, _vp]
-        for name in ("pa_paged_attention_decode_fp8", "pa_paged_attention_verify_fp8"):
+        lib.pa_reshape_and_cache_fp4.restype = ctypes.c_int
+        lib.pa_reshape_and_cache_fp4.argtypes = lib.pa_reshape_and_cache_fp8.argtypes
+        lib.pa_gather_cache_fp4.restype = ctypes.c_int
+        lib.pa_gather_cache_fp4.argtypes = [_vp] * 7 + [ctypes.c_int32] * 5 + [ctypes.c_int64, _vp, _vp]
+        lib.pa_extend_block_tables.restype = ctypes.c_int
+        lib.pa_extend_block_tables.argtypes = ([_vp] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_int64, ctypes.c_int32]
+                                               + [_vp] * 5)
+        lib.pa_release_block_tables.restype = ctypes.c_int
+        lib.pa_release_block_tables.argtypes = [_vp] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_int64] + [_vp] * 4
+        for name in ("pa_paged_attention_decode_fp8", "pa_paged_attention_verify_fp8",
+                     "pa_paged_attention_decode_fp4", "pa_paged_attention_verify_fp4"):
             fn = getattr(lib, name)
             fn.restype = ctypes.c_int
             fn.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnDesc), _vp, _vp, ctypes.c_size_t,
@@ -137,10 +154,11 @@ def load_library(path: str | None = None):
         lib.pa_paged_attention_decode_append.restype = ctypes.c_int
         lib.pa_paged_attention_decode_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnDesc),
                                                          _vp, _vp, ctypes.c_size_t, _vp, _vp]
-        lib.pa_paged_attention_decode_append_fp8.restype = ctypes.c_int
-        lib.pa_paged_attention_decode_append_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                                             ctypes.POINTER(AttnDesc), _vp, _vp, ctypes.c_size_t,
-                                                             _vp, _vp]
+        for name in ("pa_paged_attention_decode_append_fp8", "pa_paged_attention_decode_append_fp4"):
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnDesc), _vp, _vp,
+                           ctypes.c_size_t, _vp, _vp]
         lib.pa_paged_attention_decode_noalloc.restype = ctypes.c_int
         lib.pa_paged_attention_decode_noalloc.argtypes = [_vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnDesc), _vp,
                                                           _vp, _vp]
@@ -196,7 +214,8 @@ def _check(status: int, what: str) -> None:
 
 
 # Call kinds of the compiled binding's attention(); each maps to one C entry point.
-_DECODE, _DECODE_APPEND, _VERIFY, _DECODE_FP8, _DECODE_APPEND_FP8, _VERIFY_FP8, _DECODE_NOALLOC = range(7)
+(_DECODE, _DECODE_APPEND, _VERIFY, _DECODE_FP8, _DECODE_APPEND_FP8, _VERIFY_FP8, _DECODE_NOALLOC, _DECODE_FP4,
+ _DECODE_APPEND_FP4, _VERIFY_FP4) = range(10)
 
 
 def _bound():
@@ -275,6 +294,73 @@ def paged_attention_verify_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     _check(_bound().attention(_VERIFY_FP8, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
                               ctypes.addressof(desc), out, workspace, status, _stream(stream)),
            "pa_paged_attention_verify_fp8")
+
+
+def fp4_cache_shape(num_pages: int, block_size: int, num_kv_heads: int, head_dim: int) -> tuple:
+    """Shape of the uint8 tensor that holds an fp4 K or V cache: one record of
+    9 * head_dim bytes per 16 tokens of a (page, KV head)."""
+    if block_size % 16 or head_dim not in (128, 256):
+        raise ValueError("fp4 cache: block_size is a multiple of 16, head_dim 128 or 256")
+    return (num_pages, num_kv_heads, block_size // 16, 9 * head_dim)
+
+
+def reshape_and_cache_fp4(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale, status=None,
+                          stream=None) -> None:
+    """Quantise new K/V rows ([N, Hkv, D] bf16) into fp4 cache slots (uint8
+    caches of fp4_cache_shape; float32 scales [Hkv]; distinct slots)."""
+    _check(_bound().reshape_fp4(k_new, v_new, k_cache, v_cache, slot_mapping, k_scale, v_scale, status,
+                                _stream(stream)), "pa_reshape_and_cache_fp4")
+
+
+def gather_cache_fp4(k_cache, v_cache, slot_mapping, k_scale, v_scale, k_out, v_out, status=None,
+                     stream=None) -> None:
+    """The rows at the given slots of an fp4 cache as values: k_out, v_out
+    [N, Hkv, D] bf16 or float32; zeros for a negative slot."""
+    _check(_bound().gather_fp4(k_cache, v_cache, slot_mapping, k_scale, v_scale, k_out, v_out, status,
+                               _stream(stream)), "pa_gather_cache_fp4")
+
+
+def paged_attention_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, desc: AttnDesc, out,
+                               workspace=None, status=None, stream=None) -> None:
+    """Decode over an fp4 cache: K = code x block scale x k_scale[kv head], V likewise."""
+    _check(_bound().attention(_DECODE_FP4, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
+                              ctypes.addressof(desc), out, workspace, status, _stream(stream)),
+           "pa_paged_attention_decode_fp4")
+
+
+def paged_attention_decode_append_fp4(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                                      desc: AttnDesc, out, workspace=None, status=None, stream=None) -> None:
+    """The fused append and decode over an fp4 cache (the new rows quantised
+    as reshape_and_cache_fp4 does)."""
+    _check(_bound().attention(_DECODE_APPEND_FP4, q, k_cache, v_cache, k_scale, v_scale, k_new, v_new, block_table,
+                              seq_lens, ctypes.addressof(desc), out, workspace, status, _stream(stream)),
+           "pa_paged_attention_decode_append_fp4")
+
+
+def paged_attention_verify_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, desc: AttnDesc, out,
+                               workspace=None, status=None, stream=None) -> None:
+    """Verify (q_len > 1) over an fp4 cache: K = code x block scale x k_scale[kv head], V likewise."""
+    _check(_bound().attention(_VERIFY_FP4, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
+                              ctypes.addressof(desc), out, workspace, status, _stream(stream)),
+           "pa_paged_attention_verify_fp4")
+
+
+def extend_block_tables(context_lens, num_new, block_table, free_pages, num_free, block_size: int, seq_lens,
+                        slot_mapping, num_free_out, status=None, stream=None) -> None:
+    """Give each request the pages its new tokens need and every new token its
+    slot: int32 context_lens, num_new and seq_lens (out) [B], block_table
+    [B, max_pages] (the new entries are written), free_pages [P] (the stack of
+    free pages), num_free and num_free_out [1]; int64 slot_mapping (out) [N]."""
+    _check(_bound().extend_tables(context_lens, num_new, block_table, free_pages, num_free, block_size, seq_lens,
+                                  slot_mapping, num_free_out, status, _stream(stream)), "pa_extend_block_tables")
+
+
+def release_block_tables(seq_lens, finished, block_table, free_pages, num_free, block_size: int, seq_lens_out,
+                         num_free_out, status=None, stream=None) -> None:
+    """Return the pages of the requests with finished[b] != 0 to the pool
+    (free_pages is written from num_free on) and set their lengths to 0."""
+    _check(_bound().release_tables(seq_lens, finished, block_table, free_pages, num_free, block_size, seq_lens_out,
+                                   num_free_out, status, _stream(stream)), "pa_release_block_tables")
 
 
 def last_plan() -> dict:

@@ -1,0 +1,43 @@
+// decode_launch_fp4.cu -- launches the split-KV decode over the fp4 cache.
+#include "decode_fp4.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+template <int D, int NT, int NW, int SPW>
+cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
+    using C = Fp4DecodeCfg<D, NT, NW, SPW>;
+    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW>;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
+    if (e != cudaSuccess) return e;
+    // programmatic dependent launch, as for the other decode kernels
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, group);
+}
+
+}  // namespace
+
+// One kernel per head_dim and 8-head n-tile count; the group and the window
+// are run-time values (they change a handful of instructions per chunk).
+cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream) {
+    if (head_dim == 256)
+        return group <= 8 ? launch_t<256, 1, 8, 6>(group, p, grid, stream, 140)
+                          : launch_t<256, 2, 8, 6>(group, p, grid, stream, 141);
+    if (head_dim == 128)
+        return group <= 8 ? launch_t<128, 1, 8, 12>(group, p, grid, stream, 142)
+                          : launch_t<128, 2, 8, 12>(group, p, grid, stream, 143);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -359,11 +359,17 @@ pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, c
                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
                       const pa_attn_desc *desc, void *out, void *workspace, size_t workspace_bytes,
                       int32_t *device_status, void *stream, const void *k_new = nullptr,
-                      const void *v_new = nullptr);
+                      const void *v_new = nullptr, bool fp4 = false);
 pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
                       const pa_attn_desc *desc, void *out, void *workspace, size_t workspace_bytes,
-                      int32_t *device_status, void *stream);
+                      int32_t *device_status, void *stream, bool fp4 = false);
+
+// The head scales of a quantised cache: both present, aligned floats.
+inline bool scales_ok(const float *k_scale, const float *v_scale) {
+    return k_scale && v_scale && !(reinterpret_cast<uintptr_t>(k_scale) & 3u) &&
+           !(reinterpret_cast<uintptr_t>(v_scale) & 3u);
+}
 
 }  // namespace pa
 
@@ -529,17 +535,48 @@ pa_status pa_paged_attention_verify_fp8(const void *q, const void *k_cache, cons
                        workspace_bytes, device_status, stream);
 }
 
+pa_status pa_paged_attention_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                        const int32_t *seq_lens, const pa_attn_desc *desc, void *out,
+                                        void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                        void *stream) {
+    if (!scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+    return decode_call(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, desc, out, workspace,
+                       workspace_bytes, device_status, stream, nullptr, nullptr, true);
+}
+
+pa_status pa_paged_attention_decode_append_fp4(const void *q, const void *k_new, const void *v_new, void *k_cache,
+                                               void *v_cache, const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const pa_attn_desc *desc, void *out, void *workspace,
+                                               size_t workspace_bytes, int32_t *device_status, void *stream) {
+    if (!k_new || !v_new || !scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+    return decode_call(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, desc, out, workspace,
+                       workspace_bytes, device_status, stream, k_new, v_new, true);
+}
+
+pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                        const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                        const int32_t *seq_lens, const pa_attn_desc *desc, void *out,
+                                        void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                        void *stream) {
+    if (!scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+    return verify_call(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, desc, out, workspace,
+                       workspace_bytes, device_status, stream, true);
+}
+
 }  // extern "C"
 
 namespace pa {
 
-// Decode over a bf16 cache (k_scale == nullptr) or an fp8 e4m3 cache; with
-// k_new / v_new, the fused append of each sequence's new token first.
+// Decode over a bf16 cache (k_scale == nullptr), an fp8 e4m3 cache or an fp4
+// cache; with k_new / v_new, the fused append of each sequence's new token
+// first.
 pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
                       const pa_attn_desc *desc, void *out, void *workspace, size_t workspace_bytes,
-                      int32_t *device_status, void *stream, const void *k_new, const void *v_new) {
-    const bool fp8 = k_scale != nullptr;
+                      int32_t *device_status, void *stream, const void *k_new, const void *v_new, bool fp4) {
+    const bool fp8 = k_scale != nullptr && !fp4;
     pa_status st = check_desc(desc, false);
     if (st != PA_OK) return st;
     if (desc->num_seqs == 0) return PA_OK;
@@ -555,8 +592,8 @@ pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, c
 
     // 16-token chunks as [column blocks][16 tokens][128 B], 128-byte swizzle
     CUtensorMap tk, tv;
-    if (!encode_cache_map_blocks(&tk, k_cache, desc, fp8, kChunk) ||
-        !encode_cache_map_blocks(&tv, v_cache, desc, fp8, kChunk))
+    if (!fp4 && (!encode_cache_map_blocks(&tk, k_cache, desc, fp8, kChunk) ||
+                 !encode_cache_map_blocks(&tv, v_cache, desc, fp8, kChunk)))
         return PA_ERR_CUDA;
 
     const int group = desc->num_q_heads / desc->num_kv_heads;
@@ -588,8 +625,9 @@ pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, c
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid(pl.num_splits, desc->num_kv_heads, desc->num_seqs);
-    const cudaError_t e = fp8 ? launch_decode_fp8(desc->head_dim, group, tk, tv, p, grid, s)
-                              : launch_decode(desc->head_dim, group, tk, tv, p, grid, s);
+    const cudaError_t e = fp4   ? launch_decode_fp4(desc->head_dim, group, p, grid, s)
+                          : fp8 ? launch_decode_fp8(desc->head_dim, group, tk, tv, p, grid, s)
+                                : launch_decode(desc->head_dim, group, tk, tv, p, grid, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (pl.num_splits > 1) {
         ReduceParams r;
@@ -606,12 +644,12 @@ pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, c
     return PA_OK;
 }
 
-// Verify over a bf16 cache (k_scale == nullptr) or an fp8 e4m3 cache.
+// Verify over a bf16 cache (k_scale == nullptr), an fp8 e4m3 cache or an fp4 cache.
 pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
                       const pa_attn_desc *desc, void *out, void *workspace, size_t workspace_bytes,
-                      int32_t *device_status, void *stream) {
-    const bool fp8 = k_scale != nullptr;
+                      int32_t *device_status, void *stream, bool fp4) {
+    const bool fp8 = k_scale != nullptr && !fp4;
     pa_status st = check_desc(desc, true);
     if (st != PA_OK) return st;
     if (desc->num_seqs == 0) return PA_OK;
@@ -625,7 +663,9 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
 
     CUtensorMap tk, tv;
     CUtensorMap tk64, tv64;  // whole-tile copies; only used where a 64-token tile fits in a page
-    if (fp8) {
+    if (fp4) {
+        // records: no tensor maps
+    } else if (fp8) {
         // e4m3 in 128-code column blocks, 128-byte swizzle: a 16-token chunk
         // per block, or a whole 64-token tile in one 5-D box
         if (!encode_cache_map(&tk, k_cache, desc, 128, true, true) ||
@@ -650,7 +690,7 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
     const int group = desc->num_q_heads / desc->num_kv_heads;
     // 128-token K tiles of one page, for the verify shapes that run 128-key score tiles
     CUtensorMap tk128 = tk64;
-    if (!fp8 && desc->block_size >= 128 && verify_wide_score_tiles(desc->head_dim, desc->q_len * group) &&
+    if (!fp8 && !fp4 && desc->block_size >= 128 && verify_wide_score_tiles(desc->head_dim, desc->q_len * group) &&
         !encode_cache_map_blocks(&tk128, k_cache, desc, false, 128))
         return PA_ERR_CUDA;
 
@@ -678,12 +718,15 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
     p.num_kv_heads = desc->num_kv_heads;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int row_blocks = (desc->q_len * group + 127) / 128;
     const dim3 grid(pl.num_splits, desc->num_kv_heads * row_blocks, desc->num_seqs);
-    const cudaError_t e = fp8 ? launch_verify_fp8(desc->head_dim, tk, tv, tk64, tv64, p, grid, s)
-                              : launch_verify(desc->head_dim, desc->q_len * group, tk, tv, tk64, tv64, tk128, p,
+    const cudaError_t e = fp4   ? launch_verify_fp4(desc->head_dim, p, grid, s)
+                          : fp8 ? launch_verify_fp8(desc->head_dim, tk, tv, tk64, tv64, p, grid, s)
+                                : launch_verify(desc->head_dim, desc->q_len * group, tk, tv, tk64, tv64, tk128, p,
                                               grid, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (pl.num_splits > 1) {

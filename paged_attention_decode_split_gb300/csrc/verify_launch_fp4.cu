@@ -1,0 +1,39 @@
+// verify_launch_fp4.cu -- the tensor-core verify over the fp4 cache, in a
+// translation unit of its own so it compiles in parallel with the rest.
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+template <int D, int NK, int NV, int NSG>
+cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
+    using C = VerifyTcCfg<D, NK, NV, NSG, 2, 64, true>;
+    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true>;
+    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const CUtensorMap none = {};  // the records are copied without tensor maps
+    return cudaLaunchKernelEx(&cfg, kern, none, none, none, none, p);
+}
+
+}  // namespace
+
+// The f16 rings of the fp8 form, and as many staging slots (9 KiB per tensor
+// and tile at D = 256, 4.5 KiB at D = 128) as fit beside them.
+cudaError_t launch_verify_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (head_dim == 256) return launch_t<256, 2, 3, 3>(p, grid, stream, 144);
+    if (head_dim == 128) return launch_t<128, 5, 5, 6>(p, grid, stream, 145);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

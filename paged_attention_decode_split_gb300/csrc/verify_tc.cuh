@@ -51,9 +51,20 @@
 // normaliser.  A q row enters scaled by a power of two that brings its
 // largest element into [2^14, 2^15), so any finite bf16 q fits f16; the
 // inverse power joins the softmax scale.
+//
+// fp4 cache (F4; fp4_cache.cuh): as over an e4m3 cache, but the staging slots
+// hold the tile's four records per tensor, copied by untiled bulk copies (one
+// per run of chunks in a page), and the widening applies each 16-dim block's
+// scale: code * S in f16 (exact).  The dims of a row are left in an order that
+// makes every ring write a whole 16-byte chunk of what one lane holds: K chunk
+// 4 g + c holds dims 4 c .. 4 c + 3 of blocks 2 g and 2 g + 1 (Q is stored in
+// the same order, a renaming of registers), V chunk 8 w + r of a row holds dims
+// 2 r, 2 r + 1 of blocks 4 w .. 4 w + 3 (so O's columns stand in that order,
+// undone by a renaming of registers in the epilogue).
 #pragma once
 
 #include "decode_split.cuh"
+#include "fp4_cache.cuh"
 
 namespace pa {
 
@@ -79,8 +90,10 @@ struct VerifyParams {
     int early_kv;  // stream the context before the new rows ahead of the dependency wait
     int num_kv_heads;  // grid y = num_kv_heads x 128-row blocks
     int window;        // 0: full attention; W > 0: each row sees only its last W keys
-    const float *k_scale;  // fp8 cache: [Hkv] dequantisation scales of K and V
+    const float *k_scale;  // fp8 / fp4 cache: [Hkv] dequantisation scales of K and V
     const float *v_scale;
+    const uint8_t *k_cache;  // fp4 cache: the records (copied without a tensor map)
+    const uint8_t *v_cache;
 };
 
 // Byte offset of 16-byte column chunk c of row t in a [D/64][rows][128 B]
@@ -227,9 +240,9 @@ __device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
 // V tiles per score tile.  At D = 256 two 128-column S/P buffers and O fill
 // tensor memory, so Q moves to shared memory as the product's A operand (QSM)
 // and the K ring holds one 128-key tile; at D = 128 Q stays in tensor memory.
-template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64>
+template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64, bool F4 = false>
 struct VerifyTcCfg {
-    static constexpr bool F8 = NSG > 0;                // fp8 cache: e4m3 staging ring of NSG slots per tensor
+    static constexpr bool F8 = NSG > 0;                // fp8 or fp4 cache: staging ring of NSG slots per tensor
     static constexpr bool QSM = TK == 128 && D == 256;  // Q in shared memory
     static constexpr int M = 128;                      // MMA rows (query rows, zero padded)
     static constexpr int TT = 64;                      // tokens per V tile (4 TMA chunks)
@@ -241,7 +254,8 @@ struct VerifyTcCfg {
     static constexpr int KTILE_BYTES = TK * D * 2;     // K of one score tile
     static constexpr int KVB = F8 ? 1 : 2;             // bytes per cached element
     static constexpr int CHUNK_BYTES = kChunk * D * KVB;  // one TMA chunk as copied
-    static constexpr int STG_BYTES = TT * D;           // one e4m3 tile, [D/128][64 tokens][128 B] swizzled
+    static constexpr int STG_BYTES = F4 ? CPT * fp4::rec_bytes(D)  // the tile's records
+                                        : TT * D;  // one e4m3 tile, [D/128][64 tokens][128 B] swizzled
     static constexpr int OFF_V = NK * KTILE_BYTES;      // K ring, then V ring
     static constexpr int OFF_STG = OFF_V + NV * TILE_BYTES;  // K staging, then V staging
     static constexpr int OFF_Q = OFF_STG + 2 * NSG * STG_BYTES;  // QSM: Q as [D/64][M rows][128 B], swizzled
@@ -269,6 +283,7 @@ struct VerifyTcCfg {
     static_assert(D == 256 || D == 128, "head_dim 256 or 128");
     static_assert(Q_COL + Q_TCOLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(TK == 64 || (TK == 128 && !F8), "128-key score tiles: bf16 cache only");
+    static_assert(!F4 || F8, "an fp4 cache is staged and widened");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -276,12 +291,12 @@ struct VerifyTcCfg {
 // tm_k64 / tm_v64: 5-D boxes of a whole 64-token tile, both with the 128-byte
 // swizzle).
 // tm_k64: 5-D boxes of a whole K tile of TK keys (64, or 128 with TK = 128).
-template <int D, int NK, int NV, int NSG, int NSB, int TK = 64>
-__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS, 1)
+template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false>
+__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
                         const VerifyParams p) {
-    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK>;
+    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>;
     constexpr bool F8 = C::F8, QSM = C::QSM;
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
@@ -343,7 +358,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
         flags[1] = 0;
         fence_mbar_init();
     }
-    if (warp == 5 && lane == 0) {
+    if (!F4 && warp == 5 && lane == 0) {  // (the fp4 records are copied without tensor maps)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
         prefetch_tensormap(&tm_k64);
@@ -428,7 +443,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
         const CUtensorMap *m5 = tensor == 0 ? &tm_k64 : &tm_v64;
         const int cpt = tensor == 0 ? CPK : CPT, tt = cpt * kChunk;  // chunks and tokens per tile
         const int nc = min(cpt, n_my - i * cpt);  // chunks in this tile
-        if (lane == 0) mbar_arrive_expect_tx(bar, nc * C::CHUNK_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(bar, nc * (F4 ? fp4::rec_bytes(D) : C::CHUNK_BYTES));
         __syncwarp();
         auto page_of = [&](int lp) {
             const int page = staged ? page_tab[lp - lp_first] : bt[lp];
@@ -440,6 +455,23 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
         };
         const int t00 = (c_begin + i * cpt) * kChunk;
         const int lp0 = t00 / p.block_size, off0 = t00 - lp0 * p.block_size;
+        if constexpr (F4) {
+            // the chunks of a page are contiguous: one copy for a tile inside one page, else one per chunk
+            constexpr int REC = fp4::rec_bytes(D);
+            const bool whole = off0 + nc * kChunk <= p.block_size;
+            const int n_copies = whole ? 1 : nc;
+            if (lane < n_copies) {
+                const int t0 = t00 + lane * kChunk, lp = t0 / p.block_size;
+                int page = page_of(lp);
+                if (page < 0 || (int64_t)page >= p.num_pages) page = 0;  // (flagged: the rows are zeroed)
+                const size_t rec = (((size_t)page * p.num_kv_heads + kvh) * (p.block_size / kChunk) +
+                                    (t0 - lp * p.block_size) / kChunk) * REC;
+                fp4::bulk_load(dst0 + lane * REC, (tensor == 0 ? p.k_cache : p.v_cache) + rec,
+                               (whole ? nc : 1) * REC, bar, policy);
+            }
+            __syncwarp();
+            return;
+        }
         if (nc == cpt && off0 + tt <= p.block_size) {
             // the whole tile lies in one page: one copy lands it as [blocks][tt tokens][128 B]
             if (lane == 0) tma_load_5d(dst0, m5, bar, 0, off0, 0, kvh, page_of(lp0), policy);
@@ -516,6 +548,16 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
             for (int v = 0; v < NQ; ++v)
                 qv[v] = make_uint4(bf16x2_to_f16x2_scaled(qv[v].x, q_pre), bf16x2_to_f16x2_scaled(qv[v].y, q_pre),
                                    bf16x2_to_f16x2_scaled(qv[v].z, q_pre), bf16x2_to_f16x2_scaled(qv[v].w, q_pre));
+        }
+        if constexpr (F4) {  // the dim order of the widened K tiles
+#pragma unroll
+            for (int v = 0; v < NQ; v += 4) {
+                const uint4 a = qv[v], b2 = qv[v + 1], c2 = qv[v + 2], d2 = qv[v + 3];
+                qv[v] = make_uint4(a.x, a.y, c2.x, c2.y);
+                qv[v + 1] = make_uint4(a.z, a.w, c2.z, c2.w);
+                qv[v + 2] = make_uint4(b2.x, b2.y, d2.x, d2.y);
+                qv[v + 3] = make_uint4(b2.z, b2.w, d2.z, d2.w);
+            }
         }
         if constexpr (QSM) {
             // row rho of the block at [D/64 column blocks][M rows][128 B], 16-byte unit u of a
@@ -692,7 +734,118 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
             }
         }
     } else if (warp >= 6) {
-        if constexpr (F8) {
+        if constexpr (F4) {
+            // ---------------- fp4: widen staged records into the K (warps 6, 7) / V (8, 9) ring ----------------
+            // A warp takes the tokens 8 part .. 8 part + 7 of every record.
+            const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
+            const int NR = tensor == 0 ? NK : NV;
+            uint64_t *ring_full = tensor == 0 ? k_full : v_full;
+            uint64_t *ring_empty = tensor == 0 ? k_empty : v_empty;
+            uint64_t *stg_full = tensor == 0 ? kst_full : vst_full;
+            uint64_t *stg_empty = tensor == 0 ? kst_empty : vst_empty;
+            uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V);
+            const uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES;
+            constexpr int REC = fp4::rec_bytes(D), NBL = D / 16;
+            const int t_end = min(L, (c_begin + n_my) * kChunk);
+            for (int i = 0; i < n_tiles; ++i) {
+                // the staged records have landed, and the ring slot's previous tile has been consumed
+                bool ok = __all_sync(0xffffffffu, mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]));
+                if (ok && i >= NR)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]));
+                if (!ok) {
+                    flags[0] = 1;
+                    break;
+                }
+                const uint8_t *stg_tile = stg + (i % NSG) * C::STG_BYTES;
+                uint8_t *ring_tile = ring + (i % NR) * C::TILE_BYTES;
+                const int t0 = (c_begin + i * CPT) * kChunk;
+                if (tensor == 0) {
+                    // lane: token r, quarter c of every block; r and r + 4 in the same quarter-warp, so that its
+                    // eight 16-byte ring writes fall in eight bank groups (rows past the tile's end may hold
+                    // anything: their scores are masked)
+                    const int c = lane & 3, r = ((lane >> 3) & 3) | (lane & 4);
+#pragma unroll 2
+                    for (int rc = 0; rc < CPT; ++rc) {
+                        const uint8_t *rec = stg_tile + rc * REC;
+                        uint8_t *dst = ring_tile + (rc * kChunk + 8 * part + r) * 128;
+                        uint32_t sc[NBL / 4];
+#pragma unroll
+                        for (int q = 0; q < NBL / 4; q += 2) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * part + r) * NBL + 4 * q);
+                            sc[q] = w.x;
+                            sc[q + 1] = w.y;
+                        }
+#pragma unroll
+                        for (int j = 0; j < NBL / 8; ++j) {
+                            const uint4 kw = *reinterpret_cast<const uint4 *>(rec + (2 * j + part) * 512 + (4 * r + c) * 16);
+                            const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1
+                                const int g = 4 * j + q;
+                                uint32_t a[4], s2[2];
+                                fp4::e2m1x8_f16(wd[q], a);
+                                fp4::e4m3x4_f16(sc[g / 2], s2[0], s2[1]);
+                                const uint32_t sv2 = s2[g & 1];
+                                const uint4 o = make_uint4(fp4::hmul2_lo(a[0], sv2), fp4::hmul2_lo(a[1], sv2),
+                                                           fp4::hmul2_hi(a[2], sv2), fp4::hmul2_hi(a[3], sv2));
+                                const int ch = 4 * g + c;
+                                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (TT * 128) + (((ch & 7) ^ r) << 4)) = o;
+                            }
+                        }
+                    }
+                } else {
+                    const int c = lane & 3, r = lane >> 2;
+#pragma unroll 2
+                    for (int rc = 0; rc < CPT; ++rc) {
+                        const uint8_t *rec = stg_tile + rc * REC;
+                        const int ta = 8 * part + 2 * c;  // the lane's tokens ta, ta + 1 of the record
+                        // rows outside the block's visible keys may hold anything: their scales become 0
+                        const int tg = t0 + rc * kChunk + ta;
+                        const uint32_t vm = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
+                                            (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
+                        uint32_t wd[2][NBL / 4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int q = 0; q < NBL / 4; q += 2) {
+                                const uint2 w = *reinterpret_cast<const uint2 *>(rec + (2 * part + e) * 2 * D + lane * NBL + 4 * q);
+                                wd[e][q] = w.x;
+                                wd[e][q + 1] = w.y;
+                            }
+                        }
+                        uint8_t *dst = ring_tile + (rc * kChunk + ta) * 128;
+                        const int p0 = (r ^ (2 * c)) << 4, p1 = (r ^ (2 * c + 1)) << 4;
+#pragma unroll
+                        for (int w = 0; w < NBL / 4; ++w) {
+                            uint32_t s2[4];  // scale pairs (tokens ta, ta + 1) of blocks 4 w .. 4 w + 3
+                            const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
+                            const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t lo2, hi2;
+                                fp4::e4m3x4_f16(sb[q], lo2, hi2);
+                                s2[q] = (part == 0 ? lo2 : hi2) & vm;
+                            }
+                            uint32_t a[4];
+                            fp4::e2m1x8_f16(wd[0][w], a);
+                            *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + p0) =
+                                make_uint4(fp4::hmul2_lo(a[0], s2[0]), fp4::hmul2_lo(a[1], s2[1]),
+                                           fp4::hmul2_lo(a[2], s2[2]), fp4::hmul2_lo(a[3], s2[3]));
+                            fp4::e2m1x8_f16(wd[1][w], a);
+                            *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + 128 + p1) =
+                                make_uint4(fp4::hmul2_hi(a[0], s2[0]), fp4::hmul2_hi(a[1], s2[1]),
+                                           fp4::hmul2_hi(a[2], s2[2]), fp4::hmul2_hi(a[3], s2[3]));
+                        }
+                    }
+                }
+                tc::fence_async_smem();  // the tensor core reads the widened tile
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ring_full[i % NR]);
+                    mbar_arrive(&stg_empty[i % NSG]);
+                }
+            }
+        } else if constexpr (F8) {
             // ---------------- fp8: widen staged e4m3 tiles into the K (warps 6, 7) / V (8, 9) ring ----------------
             const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
             constexpr int NR0 = NK, NR1 = NV;
@@ -1027,7 +1180,15 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
                     const int c0 = c1 + 16 * k;
                     float ov[16];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) ov[c] = __uint_as_float(r[k][c]) * inv;
+                    for (int c = 0; c < 16; ++c) {
+                        if constexpr (F4) {  // column 8 r' + 2 q + e of a 64-dim group holds dim 16 q + 2 r' + e
+                            const int col = (c >> 1) * 8 + 2 * k + (c & 1);
+                            // (a bad page's stand-in may hold NaN)
+                            ov[c] = poisoned ? 0.f : __uint_as_float(r[col >> 4][col & 15]) * inv;
+                        } else {
+                            ov[c] = __uint_as_float(r[k][c]) * inv;
+                        }
+                    }
                     if (bf) {
                         uint32_t w[8];
 #pragma unroll
@@ -1061,7 +1222,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK>::THREADS,
             }
         }
         if (live && !direct)
-            p.part_ml[orow * p.num_splits + split] = make_float2(m_ref, poisoned ? -1.f : l_sum);
+            // (F4: a NaN sum goes on as a NaN row with a weight, which the reduce does not take for an empty split)
+            p.part_ml[orow * p.num_splits + split] =
+                make_float2(m_ref, poisoned ? -1.f : F4 && l_sum != l_sum ? 1.f : l_sum);
     }
 
     tc::fence_before();
