@@ -10,14 +10,20 @@
 // k_scale[h] joined to the softmax scale and v_scale[h] to the normaliser.
 // q enters as f16 scaled by a power of two per head (f16_prescale), P as an
 // f16 head plus an f16 residual (22 significant bits): what is rounded to
-// fewer than 32 bits is rounded below the sums' own error.
+// fewer than 32 bits is rounded below the sums' own error.  For bf16 outputs
+// the residual is left out and the V scales are multiplied to P rather than to
+// V: two roundings of a weight by 2^-12 each, together a quarter of the half
+// step that the output itself is rounded by, and the errors of many keys
+// average out.
 //
 // Layout on sm_103a:
-//  * A chunk is two records (K, V) of 9 D contiguous bytes.  Every warp owns a
-//    ring of SPW stages of one chunk and fills it itself: lane k issues the
-//    copies of the warp's k-th chunk up front, lane 0 refills a stage when the
-//    warp has read it.  No producer warp and no empty barriers; all of a
-//    split's first NW * SPW chunks are in flight at once.
+//  * A chunk is two records (K, V) of 9 D contiguous bytes; a warp works on two
+//    chunks (32 tokens) at a time.  Every warp owns a ring of SPW stages of one
+//    chunk pair and fills it itself: lane k issues the copies of the warp's
+//    k-th pair up front, lane 0 refills a stage when the warp has read it.  No
+//    producer warp and no empty barriers; the first NW * SPW pairs of a split
+//    are in flight at once.  The chunks left after the last whole round of NW
+//    pairs are spread over the warps one by one.
 //  * Fragments come from shared memory by 16-byte loads at lane * 16 (the
 //    record is laid out for them).  K: a lane's 16 bytes are the codes of one
 //    token, dims 16 blk + 4 c .. + 3 of eight blocks; cvt widens a byte to a
@@ -27,6 +33,13 @@
 //    nibble by nibble (two bit selects per four bytes) before cvt, and one
 //    multiply by the tokens' scale pair finishes it (one m16 tile is one scale
 //    block).
+//  * Q^T's fragments stand in shared memory, one 16-byte load per two k-steps,
+//    used for both chunks; a pair's scales are widened to f16 once, into shared
+//    memory (each is used by four lanes of K, by eight of V).
+// In the loop HBM and the instruction issue are about even (a chunk pair takes
+// 400 clocks either way); 8 warps of 230 registers measured faster than 10 or 12
+// of 168 (which spill) and than 16 of 128 whose pairs share the work on a chunk
+// and exchange P (32 x 1K-32K batch: 141 us against 163, 150 and 151).
 #pragma once
 
 #include "decode_mma.cuh"
@@ -34,25 +47,37 @@
 
 namespace pa {
 
+// What the fp4 decode needs beyond DecodeParams: the group and the division of
+// a chunk index by the chunks of a page (a multiply by floor(2^32 / cpp), one
+// correction step).
+struct Fp4Params {
+    int group;
+    int chunks_per_page;
+    uint32_t page_mul;
+};
+
 template <int D, int NT, int NW, int SPW>
 struct Fp4DecodeCfg {
     static constexpr int REC = fp4::rec_bytes(D);
-    static constexpr int STAGE_BYTES = 2 * REC;  // K record, then V record
+    static constexpr int STAGE_BYTES = 4 * REC;  // K records of a chunk pair, then its V records
     static constexpr int THREADS = NW * 32;
     static constexpr int NB = D / 16;            // scale blocks = k16 steps = m16 tiles of d
     static constexpr int GMAX = 8 * NT;
     static constexpr int HS = D + 4;             // merge row stride in floats (bank spread)
     static constexpr int RING_BYTES = NW * SPW * STAGE_BYTES;
     static constexpr int MERGE_BYTES = NW * GMAX * HS * 4;
-    static constexpr int OFF_BAR = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
-    static constexpr int OFF_FLAGS = OFF_BAR + NW * SPW * 8;
+    static constexpr int OFF_Q = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;  // [NT][NB / 2][32] uint4
+    static constexpr int OFF_QSC = OFF_Q + NT * NB / 2 * 512;  // [GMAX] score multipliers
+    static constexpr int SC_BYTES = 2 * 2 * 16 * NB * 2;       // per warp: a pair's K, then V scales in f16
+    static constexpr int OFF_SC = OFF_QSC + GMAX * 4;
+    static constexpr int OFF_BAR = OFF_SC + NW * SC_BYTES;
+    static constexpr int OFF_FLAGS = OFF_BAR + (NW * SPW + 1) * 8;  // full[NW * SPW], q_full
     static constexpr int OFF_ML = OFF_FLAGS + 16;           // [NW][GMAX] (m, l)
-    static constexpr int OFF_W = OFF_ML + NW * GMAX * 8;    // [NW][GMAX] merge weights
-    static constexpr int OFF_PT = OFF_W + NW * GMAX * 4;
+    static constexpr int OFF_PT = OFF_ML + NW * GMAX * 8;
     static constexpr int SMEM_BYTES = OFF_PT + kPageTab * 4 + 128;  // + slack to align the base
     static_assert(D == 128 || D == 256, "head_dim 128 or 256");
     static_assert(NT == 1 || NT == 2, "up to 16 heads per KV head");
-    static_assert(SPW <= 32, "a lane per stage issues the first copies");
+    static_assert(SPW <= 32 && NT <= NW, "a lane per stage issues the first copies; a warp per n-tile lays Q out");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -79,40 +104,81 @@ __device__ __forceinline__ void append_new_row_fp4(const DecodeParams &p, int b,
     __syncwarp();
 }
 
-template <int D, int NT, int NW, int SPW>
-__global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const int G) {
+// NW warps, SPW stages per warp, RES: the P residual is multiplied too.
+template <int D, int NT, int NW, int SPW, bool RES>
+__global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const Fp4Params fp) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
-    constexpr int NB = C::NB, HS = C::HS, GMAX = C::GMAX;
+    constexpr int NB = C::NB, HS = C::HS, GMAX = C::GMAX, REC = C::REC;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 127) & ~uintptr_t(127));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page
     float2 *merge_ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
-    float *merge_w = reinterpret_cast<float *>(smem + C::OFF_W);
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
+    uint4 *q_frag = reinterpret_cast<uint4 *>(smem + C::OFF_Q);
+    float *q_mul = reinterpret_cast<float *>(smem + C::OFF_QSC);
+
+    // The reference max of a head is kept kAbove over the largest score it was
+    // raised for, and raised again when a score passes it by kRaise: without
+    // the residual P is multiplied by the V scales (up to 448) in f16, so it
+    // stays below 2^6.
+    constexpr float kAbove = RES ? 0.f : 2.f, kRaise = kLazyLog2 - kAbove;
 
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int hq0 = kvh * G, hkv = gridDim.y;
+    const int G = fp.group, hq0 = kvh * G, hkv = gridDim.y;
 
     pdl_launch_dependents();
-    if (threadIdx.x < NW * SPW) mbar_init(&full[threadIdx.x], 1);
+    uint64_t *q_full = full + NW * SPW;
+    if (threadIdx.x <= NW * SPW) {
+        mbar_init(&full[threadIdx.x], threadIdx.x < NW * SPW ? 1 : NT);
+        fence_mbar_init();
+    }
     if (threadIdx.x == 0) {
         flags[0] = 0;
         flags[1] = 0;
     }
-    if (threadIdx.x < NW * SPW) fence_mbar_init();
     // Every global access waits for the work before this call, except that
     // early_kv lets the block table, seq_lens and the chunks wholly before the
     // new row go first.
     if (!p.early_kv) pdl_wait_primary();
 
+    // Q^T as B fragments, in f16: n-tile nt, k-step ks -> dims 16 ks + 4c (+1)
+    // and 16 ks + 4c + 2 (+3) of head 8 nt + r; warp nt lays its tile out.  Its
+    // loads go out first: behind the CTAs' copies they took 3 us to come back.
+    const int r = lane >> 2, c = lane & 3;
+    uint2 qw[NB];
+    float k_scale, v_scale;
+    auto load_q = [&]() {
+        k_scale = p.k_scale[kvh];
+        v_scale = p.v_scale[kvh];
+        if (warp < NT) {
+            const int h = warp * 8 + r;
+            const __nv_bfloat16 *qrow = p.q + ((size_t)b * p.num_q_heads + hq0 + (h < G ? h : 0)) * D;
+#pragma unroll
+            for (int ks = 0; ks < NB; ++ks) qw[ks] = *reinterpret_cast<const uint2 *>(qrow + 16 * ks + 4 * c);
+        }
+    };
+    if (!p.early_kv) load_q();
+
     int L = p.seq_lens[b];
     int c_begin = split * p.chunks_per_split;
-    if (p.window > 0 && L > p.window && L <= p.max_seq_len) c_begin += (L - p.window) / kChunk;
+    if (p.window > 0) {  // (a branch: without a window the table's loads do not wait for the length)
+        if (L > p.window && L <= p.max_seq_len) c_begin += (L - p.window) / kChunk;
+    }
+    auto page_of_chunk = [&](int chunk, int &in_page) {
+        int lp = (int)__umulhi((uint32_t)chunk, fp.page_mul);
+        in_page = chunk - lp * fp.chunks_per_page;
+        if (in_page >= fp.chunks_per_page) {
+            in_page -= fp.chunks_per_page;
+            ++lp;
+        }
+        return lp;
+    };
     const int32_t *bt = p.block_table + (size_t)b * p.max_pages_per_seq;
-    const int lp_first = (int)(((int64_t)c_begin * kChunk) / p.block_size);
-    const int lp_last = min((int)(((int64_t)(c_begin + p.chunks_per_split) * kChunk - 1) / p.block_size), p.max_pages_per_seq - 1);
+    int unused;
+    const int lp_first = page_of_chunk(c_begin, unused);
+    const int lp_last = min(page_of_chunk(c_begin + p.chunks_per_split - 1, unused), p.max_pages_per_seq - 1);
     const int n_pt = lp_last - lp_first + 1;
     const bool staged = n_pt <= kPageTab;
     if (staged)
@@ -138,78 +204,122 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     }
     __syncthreads();  // barrier initialisation and the page table are visible to every thread
 
-    // ---- this warp's chunks: warp, warp + NW, ... of the split ----
-    const int n_w = (n_my - warp + NW - 1) / NW;  // (<= 0 for a warp without chunks)
+    // ---- this warp's chunks: pairs warp, warp + NW, ... of the whole rounds, then its share of the rest ----
+    const int rounds = n_my / (2 * NW), rest = n_my - rounds * 2 * NW;
+    const int twos = max(0, rest - NW);  // warps that take two chunks of the rest
+    const int n_w = rounds + (warp < rest ? 1 : 0);
+    auto item = [&](int k, bool &two) {  // the split-relative first chunk of the warp's k-th item
+        two = k < rounds || warp < twos;
+        return k < rounds ? 2 * (warp + k * NW) : 2 * NW * rounds + warp + min(warp, twos);
+    };
     const uint64_t policy = l2_policy_evict_first();
     uint8_t *ring = smem + warp * SPW * C::STAGE_BYTES;
+    uint8_t *scales = smem + C::OFF_SC + warp * C::SC_BYTES;  // f16, in the order of the records' scale bytes
     uint64_t *bars = full + warp * SPW;
-    const int chunks_per_page = p.block_size / kChunk;
-    auto page_of = [&](int chunk, int &in_page) {
-        const int lp = chunk / chunks_per_page;
-        in_page = chunk - lp * chunks_per_page;
-        return staged ? page_tab[lp - lp_first] : bt[lp];
-    };
-    auto issue = [&](int k) {  // the warp's k-th chunk into its stage k % SPW
-        int in_page, page = page_of(c_begin + warp + k * NW, in_page);
+    // Byte offset of a chunk's record in either cache.
+    auto record_of = [&](int chunk, int &in_page) {
+        const int lp = page_of_chunk(chunk, in_page);
+        int page = staged ? page_tab[lp - lp_first] : bt[lp];
         if (page < 0 || (int64_t)page >= p.num_pages) {
             flags[1] = 1;  // the outputs of this CTA are zeroed; page 0 is read in its place
             set_status(p.status, PA_DEV_BAD_PAGE);
             page = 0;
         }
-        const size_t rec = (((size_t)page * hkv + kvh) * chunks_per_page + in_page) * C::REC;
-        uint8_t *st = ring + (k % SPW) * C::STAGE_BYTES;
-        uint64_t *bar = &bars[k % SPW];
-        mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-        fp4::bulk_load(st, p.k_cache + rec, C::REC, bar, policy);
-        fp4::bulk_load(st + C::REC, p.v_cache + rec, C::REC, bar, policy);
+        return (((size_t)page * hkv + kvh) * fp.chunks_per_page + in_page) * REC;
+    };
+    int at_page = 0;    // where the copies of the last pair were: chunk of the page,
+    size_t at_rec = 0;  // byte offset of the record
+    auto issue = [&](int k, uint8_t *st, uint64_t *bar) {  // the warp's k-th item
+        bool two;
+        const int i = item(k, two);
+        at_rec = record_of(c_begin + i, at_page);
+        mbar_arrive_expect_tx(bar, two ? 4 * REC : 2 * REC);
+        const bool joined = two && at_page + 1 < fp.chunks_per_page;  // one run of the page
+        const uint32_t bytes = joined ? 2 * REC : REC;
+        fp4::bulk_load(st, p.k_cache + at_rec, bytes, bar, policy);
+        fp4::bulk_load(st + 2 * REC, p.v_cache + at_rec, bytes, bar, policy);
+        if (two && !joined) {
+            int in_page;
+            const size_t rec2 = record_of(c_begin + i + 1, in_page);
+            fp4::bulk_load(st + REC, p.k_cache + rec2, REC, bar, policy);
+            fp4::bulk_load(st + 3 * REC, p.v_cache + rec2, REC, bar, policy);
+        }
+    };
+    // A refill: the next pair of a whole round lies 2 NW chunks on, mostly in the same page.
+    auto refill = [&](int k, uint8_t *st, uint64_t *bar) {
+        if (k < rounds && at_page + 2 * NW + 1 < fp.chunks_per_page) {
+            at_page += 2 * NW;
+            at_rec += 2 * NW * REC;
+            mbar_arrive_expect_tx(bar, 4 * REC);
+            fp4::bulk_load(st, p.k_cache + at_rec, 2 * REC, bar, policy);
+            fp4::bulk_load(st + 2 * REC, p.v_cache + at_rec, 2 * REC, bar, policy);
+        } else {
+            issue(k, st, bar);
+        }
     };
     const int i_new = (L - 1) / kChunk - c_begin;  // the split-relative chunk of the new row
-    bool first_done = false;                       // this lane's first stage is on its way
+    // the warp whose items hold the new row's chunk
+    const int j_new = i_new - 2 * NW * rounds;
+    const int w_new = j_new < 0 ? (i_new >> 1) % NW : j_new < 2 * twos ? j_new >> 1 : j_new - twos;
+    // The first copies go out stage by stage, not warp by warp: the copy engine
+    // works them off in order, so the first pairs land while the later ones are
+    // still on their way (32K call: 19.7 us with both stages of a warp at once).
+    int n_issued = 0;
     if (p.early_kv) {
-        if (lane < min(SPW, n_w) && warp + lane * NW < i_new) {
-            issue(lane);
-            first_done = true;
-        }
+        if (lane == 0)
+            for (; n_issued < min(SPW, n_w); ++n_issued) {
+                bool two;
+                const int i = item(n_issued, two);
+                if (i + (two ? 1 : 0) >= i_new) break;
+                issue(n_issued, ring + n_issued * C::STAGE_BYTES, &bars[n_issued]);
+            }
         pdl_wait_primary();
+        load_q();
+    } else if (lane == 0 && n_w > 0 && (p.k_new == nullptr || n_w > 1 || warp != w_new)) {
+        issue(0, ring, &bars[0]);
+        n_issued = 1;
     }
-    if (p.k_new != nullptr && i_new < n_my && i_new >= 0 && warp == i_new % NW) {
+    if (warp < NT) {
+        if (warp * 8 + r >= G) {  // heads past the group
+#pragma unroll
+            for (int ks = 0; ks < NB; ++ks) qw[ks] = make_uint2(0u, 0u);
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int ks = 0; ks < NB; ++ks) amax = max(amax, max(bf16x2_absmax(qw[ks].x), bf16x2_absmax(qw[ks].y)));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const float mul = f16_prescale(amax);
+#pragma unroll
+        for (int ks = 0; ks < NB; ks += 2)
+            q_frag[(warp * (NB / 2) + ks / 2) * 32 + lane] =
+                make_uint4(bf16x2_to_f16x2_scaled(qw[ks].x, mul), bf16x2_to_f16x2_scaled(qw[ks].y, mul),
+                           bf16x2_to_f16x2_scaled(qw[ks + 1].x, mul), bf16x2_to_f16x2_scaled(qw[ks + 1].y, mul));
+        if (c == 0) q_mul[8 * warp + r] = p.scale_log2 * k_scale * (1.f / mul);  // (1 / a power of two: exact)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+    }
+    if (p.k_new != nullptr && i_new < n_my && i_new >= 0 && warp == w_new) {
         int in_page;
-        const int page = page_of(c_begin + i_new, in_page);
+        const int lp = page_of_chunk(c_begin + i_new, in_page);
+        const int page = staged ? page_tab[lp - lp_first] : bt[lp];
         if (page >= 0 && (int64_t)page < p.num_pages)  // (a bad page is flagged when its chunk is copied)
             append_new_row_fp4<D>(p, b, kvh, L - 1, page);
     }
-    if (!first_done && lane < min(SPW, n_w)) issue(lane);
+    if (lane == 0)
+        for (; n_issued < min(SPW, n_w); ++n_issued)
+            issue(n_issued, ring + n_issued * C::STAGE_BYTES, &bars[n_issued]);
 
-    const int r = lane >> 2, c = lane & 3;
+    // (an mbarrier rather than a CTA barrier: a warp whose copies the copy engine has yet to take holds no other up)
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, &flags[0]));
+    if (!ok) flags[0] = 1;
     float m_run[NT][2], l_run[NT][2];
     float oacc[NB][NT][4];
-    // Q^T as B fragments, in f16: n-tile nt, k-step ks -> dims 16 ks + 4c (+1)
-    // and 16 ks + 4c + 2 (+3) of head 8 nt + r
-    uint32_t qf[NT][NB][2];
     float qsc[NT][2];  // multiplier of the raw scores of heads 8 nt + 2c + j (log2 units)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int h = nt * 8 + r;
-        const bool live = h < G;
-        const __nv_bfloat16 *qrow = p.q + ((size_t)b * p.num_q_heads + hq0 + (live ? h : 0)) * D;
-        uint2 w[NB];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int ks = 0; ks < NB; ++ks) {
-            w[ks] = live ? *reinterpret_cast<const uint2 *>(qrow + 16 * ks + 4 * c) : make_uint2(0u, 0u);
-            amax = max(amax, max(bf16x2_absmax(w[ks].x), bf16x2_absmax(w[ks].y)));
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const float qmul = f16_prescale(amax);
-#pragma unroll
-        for (int ks = 0; ks < NB; ++ks) {
-            qf[nt][ks][0] = bf16x2_to_f16x2_scaled(w[ks].x, qmul);
-            qf[nt][ks][1] = bf16x2_to_f16x2_scaled(w[ks].y, qmul);
-        }
-        const float mine = p.scale_log2 * p.k_scale[kvh] * (1.f / qmul);  // (1 / a power of two: exact)
-        qsc[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * c);
-        qsc[nt][1] = __shfl_sync(0xffffffffu, mine, 8 * c + 4);
+        qsc[nt][0] = q_mul[8 * nt + 2 * c];
+        qsc[nt][1] = q_mul[8 * nt + 2 * c + 1];
         m_run[nt][0] = m_run[nt][1] = -INFINITY;
         l_run[nt][0] = l_run[nt][1] = 0.f;
 #pragma unroll
@@ -218,9 +328,12 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
             for (int i = 0; i < 4; ++i) oacc[mt][nt][i] = 0.f;
     }
 
-    for (int k = 0; k < n_w; ++k) {
-        const int s = k % SPW;
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (k / SPW) & 1, &flags[0]))) {
+    int s = 0;
+    uint32_t phase = 0;
+    const int t_rest = (c_begin + 2 * NW * rounds + warp + min(warp, twos)) * kChunk;
+    for (int k = 0, t_round = (c_begin + 2 * warp) * kChunk; k < n_w; ++k, t_round += 2 * NW * kChunk) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars[s], phase, &flags[0]));
+        if (!ok) {
             flags[0] = 1;
             set_status(p.status, PA_DEV_TIMEOUT);
             // giving up: let the copies in flight land before the CTA ends
@@ -229,87 +342,117 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 }
             break;
         }
-        const uint8_t *kb = ring + s * C::STAGE_BYTES, *vb = kb + C::REC;
-        const int t_chunk = (c_begin + warp + k * NW) * kChunk;
-        const int nv = min(kChunk, L - t_chunk);  // visible rows [lead, nv)
-        const int lead = p.window > 0 ? max(0, L - p.window - t_chunk) : 0;
-        const bool partial = nv < kChunk || lead > 0;  // warp-uniform
+        const uint8_t *kb = ring + s * C::STAGE_BYTES, *vb = kb + 2 * REC;
+        const int t_pair = k < rounds ? t_round : t_rest;
+        // visible tokens [lead, nv) of the pair (the second half of a single chunk's stage holds stale bytes)
+        const int nv = min((k < rounds || warp < twos ? 2 : 1) * kChunk, L - t_pair);
+        const int lead = p.window > 0 ? max(0, L - p.window - t_pair) : 0;
+        const bool partial = nv < 2 * kChunk || lead > 0;  // warp-uniform
 
-        // ---- S^T = K Q^T, two accumulators per n-tile (even / odd k-steps) ----
-        float sa[NT][2][4];
+        // ---- the pair's scales to f16, once (each is used by 4 lanes of K, by 8 of V) ----
+        if (lane < 2 * NB) {
+            const int ch = lane / NB, part = (lane % NB) * 16;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sa[nt][u][q] = 0.f;
-        uint32_t ksc[2][NB / 4];  // scale bytes of tokens r, r + 8
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint8_t *sp = kb + 8 * D + (r + 8 * h) * NB;
-            if constexpr (NB == 16) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(sp);
-                ksc[h][0] = w.x; ksc[h][1] = w.y; ksc[h][2] = w.z; ksc[h][3] = w.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(sp);
-                ksc[h][0] = w.x; ksc[h][1] = w.y;
+            for (int t = 0; t < 2; ++t) {
+                const uint4 w = *reinterpret_cast<const uint4 *>((t == 0 ? kb : vb) + ch * REC + 8 * D + part);
+                uint4 lo, hi;
+                fp4::e4m3x4_f16(w.x, lo.x, lo.y);
+                fp4::e4m3x4_f16(w.y, lo.z, lo.w);
+                fp4::e4m3x4_f16(w.z, hi.x, hi.y);
+                fp4::e4m3x4_f16(w.w, hi.z, hi.w);
+                uint4 *dst = reinterpret_cast<uint4 *>(scales + t * (C::SC_BYTES / 2) + (ch * 16 * NB + part) * 2);
+                dst[0] = lo;
+                dst[1] = hi;
             }
         }
+        __syncwarp();
+        const uint8_t *ksc = scales, *vsc = scales + C::SC_BYTES / 2;
+
+        // ---- S^T = K Q^T per chunk, two accumulators per n-tile (even / odd k-steps) ----
+        float sa[2][NT][2][4];
 #pragma unroll
         for (int j = 0; j < NB / 8; ++j) {
-            const uint4 k0 = *reinterpret_cast<const uint4 *>(kb + (2 * j) * 512 + lane * 16);
-            const uint4 k1 = *reinterpret_cast<const uint4 *>(kb + (2 * j + 1) * 512 + lane * 16);
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            uint32_t kw[2][2][4], ks[2][2][4];  // [chunk][token r, r + 8]: codes and scale pairs of blocks 8 j .. + 7
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *rec = kb + ch * REC;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(rec + (2 * j + h) * 512 + lane * 16);
+                    const uint4 sw = *reinterpret_cast<const uint4 *>(ksc + ((ch * 16 + r + 8 * h) * NB + 8 * j) * 2);
+                    kw[ch][h][0] = w.x; kw[ch][h][1] = w.y; kw[ch][h][2] = w.z; kw[ch][h][3] = w.w;
+                    ks[ch][h][0] = sw.x; ks[ch][h][1] = sw.y; ks[ch][h][2] = sw.z; ks[ch][h][3] = sw.w;
+                }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1: one word of each token
-                uint32_t a[4], e[4], s0[2], s1[2];
-                fp4::e2m1x8_f16(w0[q], a);
-                fp4::e2m1x8_f16(w1[q], e);
-                const int blk = 8 * j + 2 * q;
-                fp4::e4m3x4_f16(ksc[0][blk / 4], s0[0], s0[1]);
-                fp4::e4m3x4_f16(ksc[1][blk / 4], s1[0], s1[1]);
-                const uint32_t t0 = s0[q & 1], t1 = s1[q & 1];  // scales of blocks blk (low), blk + 1 (high)
+                uint4 qf[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mm::mma<true>(sa[nt][0], fp4::hmul2_lo(a[0], t0), fp4::hmul2_lo(e[0], t1), fp4::hmul2_lo(a[1], t0),
-                                  fp4::hmul2_lo(e[1], t1), qf[nt][blk][0], qf[nt][blk][1]);
-                    mm::mma<true>(sa[nt][1], fp4::hmul2_hi(a[2], t0), fp4::hmul2_hi(e[2], t1), fp4::hmul2_hi(a[3], t0),
-                                  fp4::hmul2_hi(e[3], t1), qf[nt][blk + 1][0], qf[nt][blk + 1][1]);
+                for (int nt = 0; nt < NT; ++nt) qf[nt] = q_frag[(nt * (NB / 2) + 4 * j + q) * 32 + lane];
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t a[4], e[4];
+                    fp4::e2m1x8_f16(kw[ch][0][q], a);
+                    fp4::e2m1x8_f16(kw[ch][1][q], e);
+                    const uint32_t t0 = ks[ch][0][q], t1 = ks[ch][1][q];  // scales of the even (low) and odd block
+                    const uint32_t a0 = fp4::hmul2_lo(a[0], t0), a1 = fp4::hmul2_lo(a[1], t0);
+                    const uint32_t a2 = fp4::hmul2_hi(a[2], t0), a3 = fp4::hmul2_hi(a[3], t0);
+                    const uint32_t e0 = fp4::hmul2_lo(e[0], t1), e1 = fp4::hmul2_lo(e[1], t1);
+                    const uint32_t e2 = fp4::hmul2_hi(e[2], t1), e3 = fp4::hmul2_hi(e[3], t1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (j == 0 && q == 0) {
+                            fp4::mma0_f16(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
+                            fp4::mma0_f16(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
+                        } else {
+                            mm::mma<true>(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
+                            mm::mma<true>(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
+                        }
+                    }
                 }
             }
         }
 
-        // ---- online softmax on the fragments (log2 units) ----
-        float x[NT][4];
+        // ---- online softmax on the fragments (log2 units): x[ch][nt][tokens r, r + 8][heads 2c, 2c + 1] ----
+        float x[2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[nt][q] = (sa[nt][0][q] + sa[nt][1][q]) * qsc[nt][q & 1];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[ch][nt][q] = (sa[ch][nt][0][q] + sa[ch][nt][1][q]) * qsc[nt][q & 1];
         if (partial) {
-            const bool v0 = r >= lead && r < nv, v1 = r + 8 >= lead && r + 8 < nv;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (!v0) x[nt][0] = x[nt][1] = -INFINITY;
-                if (!v1) x[nt][2] = x[nt][3] = -INFINITY;
+            for (int ch = 0; ch < 2; ++ch) {
+                const int t0 = 16 * ch + r, t1 = t0 + 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (t0 < lead || t0 >= nv) x[ch][nt][0] = x[ch][nt][1] = -INFINITY;
+                    if (t1 < lead || t1 >= nv) x[ch][nt][2] = x[ch][nt][3] = -INFINITY;
+                }
             }
         }
+        float cm[NT][2];  // the lane's largest score per head
         bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) up |= x[nt][q] > m_run[nt][q & 1] + kLazyLog2;
+            for (int j = 0; j < 2; ++j) {
+                cm[nt][j] = fmaxf(fmax3(x[0][nt][j], x[0][nt][j + 2], x[1][nt][j]), x[1][nt][j + 2]);
+                up |= cm[nt][j] > m_run[nt][j] + kRaise;
+            }
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float cm = fmaxf(x[nt][j], x[nt][j + 2]);
-                    cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 4));
-                    cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 8));
-                    cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 16));
-                    if (cm > m_run[nt][j] + kLazyLog2) {
-                        const float alpha = fast_exp2(m_run[nt][j] - cm);  // 0 on the first chunk
-                        m_run[nt][j] = cm;
+                    float m = cm[nt][j];
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m > m_run[nt][j] + kRaise) {
+                        m += kAbove;
+                        const float alpha = fast_exp2(m_run[nt][j] - m);  // 0 on the first pair
+                        m_run[nt][j] = m;
                         l_run[nt][j] *= alpha;
 #pragma unroll
                         for (int mt = 0; mt < NB; ++mt) {
@@ -320,72 +463,115 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 }
         }
         // P^T fragments: head + residual, each transposed in registers
-        uint32_t bh[NT][2], bl[NT][2];
+        uint32_t bh[2][NT][2], bl[2][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float pr[4];
+        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) pr[q] = fast_exp2(x[nt][q] - m_run[nt][q & 1]);  // 0 for masked rows
-            l_run[nt][0] += pr[0] + pr[2];
-            l_run[nt][1] += pr[1] + pr[3];
-            uint32_t h01, h23, r01, r23;
-            split_f16(pr[0], pr[1], h01, r01);
-            split_f16(pr[2], pr[3], h23, r23);
-            bh[nt][0] = mm::movt(h01);
-            bh[nt][1] = mm::movt(h23);
-            bl[nt][0] = mm::movt(r01);
-            bl[nt][1] = mm::movt(r23);
-        }
+            for (int nt = 0; nt < NT; ++nt) {
+                float pr[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) pr[q] = fast_exp2(x[ch][nt][q] - m_run[nt][q & 1]);  // 0 for masked rows
+                l_run[nt][0] += pr[0] + pr[2];
+                l_run[nt][1] += pr[1] + pr[3];
+                uint32_t h01, h23, r01, r23;
+                if constexpr (RES) {
+                    split_f16(pr[0], pr[1], h01, r01);
+                    split_f16(pr[2], pr[3], h23, r23);
+                    bl[ch][nt][0] = mm::movt(r01);
+                    bl[ch][nt][1] = mm::movt(r23);
+                } else {
+                    h01 = pack_f16(pr[0], pr[1]);
+                    h23 = pack_f16(pr[2], pr[3]);
+                }
+                bh[ch][nt][0] = mm::movt(h01);
+                bh[ch][nt][1] = mm::movt(h23);
+            }
 
         // ---- O^T += V^T P^T ----
-        uint32_t vw[4][NB / 4];  // codes of tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: byte blk = dims 16 blk + 2r, + 1
+        // Tokens outside [lead, nv) may hold anything: in a partial pair their
+        // scales become 0 (the codes themselves are always finite).
+        auto pv = [&](auto masked) {
+            constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint8_t *vp = vb + u * 2 * D + lane * NB;
-            if constexpr (NB == 16) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vp);
-                vw[u][0] = w.x; vw[u][1] = w.y; vw[u][2] = w.z; vw[u][3] = w.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(vp);
-                vw[u][0] = w.x; vw[u][1] = w.y;
-            }
-        }
-        // rows outside [lead, nv) may hold anything: their scales become 0
-        // (the codes themselves are always finite)
-        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-        if (partial) {
-            auto in = [&](int t) { return t >= lead && t < nv; };
-            mlo = (in(2 * c) ? 0x0000ffffu : 0u) | (in(2 * c + 1) ? 0xffff0000u : 0u);
-            mhi = (in(2 * c + 8) ? 0x0000ffffu : 0u) | (in(2 * c + 9) ? 0xffff0000u : 0u);
-        }
+            for (int ch = 0; ch < 2; ++ch) {
+                const uint8_t *rec = vb + ch * REC;
+                uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+                if constexpr (MASK) {
+                    auto in = [&](int t) { return 16 * ch + t >= lead && 16 * ch + t < nv; };
+                    mlo = (in(2 * c) ? 0x0000ffffu : 0u) | (in(2 * c + 1) ? 0xffff0000u : 0u);
+                    mhi = (in(2 * c + 8) ? 0x0000ffffu : 0u) | (in(2 * c + 9) ? 0xffff0000u : 0u);
+                }
+                uint32_t vw[4][NB / 4];  // codes of tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: byte blk = dims 16 blk + 2r, + 1
 #pragma unroll
-        for (int w = 0; w < NB / 4; ++w) {
-            const uint4 sc4 = *reinterpret_cast<const uint4 *>(vb + 8 * D + w * 64 + c * 16);
-            const uint32_t sc[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
-            constexpr uint32_t LO = 0x0f0f0f0fu, HI = 0xf0f0f0f0u;
-            uint32_t a0[4], a1[4], a2[4], a3[4];
-            fp4::e2m1x8_f16((vw[0][w] & LO) | ((vw[1][w] << 4) & HI), a0);  // dims 16 blk + 2r, tokens 2c, 2c + 1
-            fp4::e2m1x8_f16(((vw[0][w] >> 4) & LO) | (vw[1][w] & HI), a1);  // dims 16 blk + 2r + 1
-            fp4::e2m1x8_f16((vw[2][w] & LO) | ((vw[3][w] << 4) & HI), a2);  // tokens 8 + 2c, 9 + 2c
-            fp4::e2m1x8_f16(((vw[2][w] >> 4) & LO) | (vw[3][w] & HI), a3);
+                for (int u = 0; u < 4; ++u) {
+                    const uint8_t *vp = rec + u * 2 * D + lane * NB;
+                    if constexpr (NB == 16) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(vp);
+                        vw[u][0] = w.x; vw[u][1] = w.y; vw[u][2] = w.z; vw[u][3] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(vp);
+                        vw[u][0] = w.x; vw[u][1] = w.y;
+                    }
+                }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int mt = 4 * w + q;
-                uint32_t slo, shi;
-                fp4::e4m3x4_f16(sc[q], slo, shi);
-                slo &= mlo;
-                shi &= mhi;
-                const uint32_t f0 = fp4::hmul2(a0[q], slo), f1 = fp4::hmul2(a1[q], slo);
-                const uint32_t f2 = fp4::hmul2(a2[q], shi), f3 = fp4::hmul2(a3[q], shi);
+                for (int w = 0; w < NB / 4; ++w) {
+                    const uint4 *sp = reinterpret_cast<const uint4 *>(vsc + ((ch * 16 * NB) + w * 64 + c * 16) * 2);
+                    const uint4 sA = sp[0], sB = sp[1];  // per block: scales of tokens 2c, 2c + 1 and 8 + 2c, 9 + 2c
+                    uint32_t slo[4] = {sA.x, sA.z, sB.x, sB.z}, shi[4] = {sA.y, sA.w, sB.y, sB.w};
+                    if constexpr (MASK) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mm::mma<true>(oacc[mt][nt], f0, f1, f2, f3, bh[nt][0], bh[nt][1]);
-                    mm::mma<true>(oacc[mt][nt], f0, f1, f2, f3, bl[nt][0], bl[nt][1]);
+                        for (int q = 0; q < 4; ++q) {
+                            slo[q] &= mlo;
+                            shi[q] &= mhi;
+                        }
+                    }
+                    constexpr uint32_t LO = 0x0f0f0f0fu, HI = 0xf0f0f0f0u;
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    fp4::e2m1x8_f16((vw[0][w] & LO) | ((vw[1][w] << 4) & HI), a0);  // dims 16 blk + 2r, tokens 2c, 2c + 1
+                    fp4::e2m1x8_f16(((vw[0][w] >> 4) & LO) | (vw[1][w] & HI), a1);  // dims 16 blk + 2r + 1
+                    fp4::e2m1x8_f16((vw[2][w] & LO) | ((vw[3][w] << 4) & HI), a2);  // tokens 8 + 2c, 9 + 2c
+                    fp4::e2m1x8_f16(((vw[2][w] >> 4) & LO) | (vw[3][w] & HI), a3);
+                    if constexpr (RES) {
+                        // V = code * S (exact); four tiles' heads, then their residuals: no product waits for
+                        // the one before it
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            a0[q] = fp4::hmul2(a0[q], slo[q]);
+                            a1[q] = fp4::hmul2(a1[q], slo[q]);
+                            a2[q] = fp4::hmul2(a2[q], shi[q]);
+                            a3[q] = fp4::hmul2(a3[q], shi[q]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bh[ch][nt][0], bh[ch][nt][1]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bl[ch][nt][0], bl[ch][nt][1]);
+                        }
+                    } else {
+                        // the scales go to P instead (half the multiplies): P S rounds once more, by 2^-12
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q],
+                                              fp4::hmul2(bh[ch][nt][0], slo[q]), fp4::hmul2(bh[ch][nt][1], shi[q]));
+                    }
                 }
             }
-        }
+        };
+        if (partial)
+            pv(std::true_type{});
+        else
+            pv(std::false_type{});
         __syncwarp();  // every lane has read the stage
-        if (lane == 0 && k + SPW < n_w) issue(k + SPW);
+        if (lane == 0 && k + SPW < n_w) refill(k + SPW, ring + s * C::STAGE_BYTES, &bars[s]);
+        if (++s == SPW) {
+            s = 0;
+            phase ^= 1;
+        }
     }
     // exponential sums: a lane holds tokens r and r + 8; sum over r
 #pragma unroll
@@ -400,62 +586,59 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         }
 
     // ---- CTA merge of the warps' states (log-sum-exp weights) ----
-    __syncthreads();  // every chunk is consumed: the stages become the merge area
-    const bool poisoned = flags[0] != 0 || flags[1] != 0;
-    float *macc = reinterpret_cast<float *>(smem);  // [NW][G][HS], unnormalised sums
-#pragma unroll
-    for (int mt = 0; mt < NB; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int h = nt * 8 + 2 * c + j;
-                if (h < G)
-                    *reinterpret_cast<float2 *>(macc + (warp * G + h) * HS + 16 * mt + 2 * r) =
-                        make_float2(oacc[mt][nt][j], oacc[mt][nt][j + 2]);
-            }
+    // Every warp sees all warps' (m, l), scales its own sums by its weight over
+    // the total and writes them; the outputs are then plain sums over the warps.
     if (r == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int h = nt * 8 + 2 * c + j;
-                if (h < G) merge_ml[warp * GMAX + h] = make_float2(m_run[nt][j], l_run[nt][j]);
+            for (int j = 0; j < 2; ++j)
+                merge_ml[warp * GMAX + nt * 8 + 2 * c + j] = make_float2(m_run[nt][j], l_run[nt][j]);
+    }
+    __syncthreads();  // every chunk is consumed: the stages become the merge area
+    const bool poisoned = flags[0] != 0 || flags[1] != 0;
+    const int n_act = min(NW, n_my);  // warps that had a chunk
+    float *macc = reinterpret_cast<float *>(smem);  // [NW][G][HS]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int h = nt * 8 + 2 * c + j;
+            float2 ml[NW];
+            float M = -INFINITY, lsum = 0.f;
+#pragma unroll
+            for (int st = 0; st < NW; ++st) ml[st] = merge_ml[st * GMAX + h];
+#pragma unroll
+            for (int st = 0; st < NW; ++st) M = fmaxf(M, ml[st].x);
+#pragma unroll
+            for (int st = 0; st < NW; ++st)  // (a warp without chunks has l = 0)
+                lsum = fmaf(ml[st].y, ml[st].y != 0.f ? fast_exp2(ml[st].x - M) : 0.f, lsum);
+            const float fac = l_run[nt][j] != 0.f && lsum != 0.f ? fast_exp2(m_run[nt][j] - M) * (v_scale / lsum) : 0.f;
+            if (h < G && warp < n_act) {
+                // a NaN sum (a NaN in a visible key or in q) goes on as a NaN output with
+                // a weight of its own: the reduce takes a sum that is not > 0 for an empty split
+                if (warp == 0 && r == 0 && p.num_splits > 1)
+                    p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + split] =
+                        make_float2(M, poisoned ? -1.f : lsum == lsum ? lsum : 1.f);
+                float *row = macc + (warp * G + h) * HS + 2 * r;
+#pragma unroll
+                for (int mt = 0; mt < NB; ++mt)
+                    *reinterpret_cast<float2 *>(row + 16 * mt) =
+                        make_float2(oacc[mt][nt][j] * fac, oacc[mt][nt][j + 2] * fac);
             }
-    }
-    __syncthreads();
-    if (threadIdx.x < G) {
-        const int h = threadIdx.x;
-        float M = -INFINITY;
-        for (int st = 0; st < NW; ++st) M = fmaxf(M, merge_ml[st * GMAX + h].x);
-        float lsum = 0.f;
-        for (int st = 0; st < NW; ++st) {
-            const float2 ml = merge_ml[st * GMAX + h];
-            const float e = ml.y != 0.f ? fast_exp2(ml.x - M) : 0.f;  // 0 for a warp without chunks
-            merge_w[st * GMAX + h] = e;
-            lsum = fmaf(ml.y, e, lsum);
         }
-        const float norm = poisoned || lsum == 0.f ? 0.f : p.v_scale[kvh] / lsum;
-        for (int st = 0; st < NW; ++st) merge_w[st * GMAX + h] *= norm;
-        // a NaN sum (a NaN in a visible key or in q) goes on as a NaN output with
-        // a weight of its own: the reduce takes a sum that is not > 0 for an empty split
-        if (p.num_splits > 1)
-            p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + split] =
-                make_float2(M, poisoned ? -1.f : lsum == lsum ? lsum : 1.f);
-    }
     __syncthreads();
     for (int idx = threadIdx.x; idx < G * D / 4; idx += C::THREADS) {
         const int h = (4 * idx) / D, d = 4 * idx - h * D;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         if (!poisoned) {  // (a bad page's stand-in may hold NaN)
 #pragma unroll 4
-            for (int st = 0; st < NW; ++st) {
-                const float wg = merge_w[st * GMAX + h];
+            for (int st = 0; st < n_act; ++st) {
                 const float4 v = *reinterpret_cast<const float4 *>(macc + (st * G + h) * HS + d);
-                o.x = fmaf(v.x, wg, o.x);
-                o.y = fmaf(v.y, wg, o.y);
-                o.z = fmaf(v.z, wg, o.z);
-                o.w = fmaf(v.w, wg, o.w);
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
             }
         }
         const size_t row = (size_t)b * p.num_q_heads + hq0 + h;

@@ -6,10 +6,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int NT, int NW, int SPW>
-cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
+template <int D, int NT, int NW, int SPW, bool RES>
+cudaError_t launch_res(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
-    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW>;
+    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW, RES>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch, as for the other decode kernels
@@ -23,7 +23,16 @@ cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p, group);
+    const int cpp = p.block_size / kChunk;
+    const Fp4Params fp{group, cpp, cpp == 1 ? 0xffffffffu : (uint32_t)((1ull << 32) / (unsigned)cpp)};
+    return cudaLaunchKernelEx(&cfg, kern, p, fp);
+}
+
+// bf16 outputs go without the P residual (two kernel slots per layout)
+template <int D, int NT, int NW, int SPW>
+cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
+    return p.out_bf16 ? launch_res<D, NT, NW, SPW, false>(group, p, grid, stream, slot)
+                      : launch_res<D, NT, NW, SPW, true>(group, p, grid, stream, slot + 1);
 }
 
 }  // namespace
@@ -32,11 +41,11 @@ cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t s
 // are run-time values (they change a handful of instructions per chunk).
 cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     if (head_dim == 256)
-        return group <= 8 ? launch_t<256, 1, 8, 6>(group, p, grid, stream, 140)
-                          : launch_t<256, 2, 8, 6>(group, p, grid, stream, 141);
+        return group <= 8 ? launch_t<256, 1, 8, 2>(group, p, grid, stream, 146)
+                          : launch_t<256, 2, 8, 2>(group, p, grid, stream, 148);
     if (head_dim == 128)
-        return group <= 8 ? launch_t<128, 1, 8, 12>(group, p, grid, stream, 142)
-                          : launch_t<128, 2, 8, 12>(group, p, grid, stream, 143);
+        return group <= 8 ? launch_t<128, 1, 12, 3>(group, p, grid, stream, 150)
+                          : launch_t<128, 2, 8, 4>(group, p, grid, stream, 152);
     return cudaErrorInvalidValue;
 }
 

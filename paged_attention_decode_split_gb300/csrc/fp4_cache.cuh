@@ -175,6 +175,16 @@ __device__ __forceinline__ void load_block(const uint8_t *rec, int t, int blk, u
     }
 }
 
+// D = A B for one m16n8k16 tile of f16 (mm::mma with a zero addend).
+__device__ __forceinline__ void mma0_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Untiled bulk copy global -> shared (16-byte aligned addresses, a multiple of
 // 16 bytes), completion signalled on `bar` as bytes.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {

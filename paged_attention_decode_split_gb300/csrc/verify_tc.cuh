@@ -276,7 +276,7 @@ struct VerifyTcCfg {
     static constexpr int Q_COL = D + NSB * TK;
     static constexpr int Q_TCOLS = QSM ? 0 : D / 2;
     static constexpr int SBUF(int j) { return S_COL + j * TK; }
-    static constexpr int CW = 2;                       // fp8: widening warps per tensor
+    static constexpr int CW = F4 ? 4 : 2;              // fp8, fp4: widening warps per tensor
     static constexpr int SROW = D * 4 + 16;            // epilogue: output rows staged in the K/V rings
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
     static constexpr int THREADS = (F8 ? 6 + 2 * CW : 6) * 32;
@@ -735,9 +735,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         }
     } else if (warp >= 6) {
         if constexpr (F4) {
-            // ---------------- fp4: widen staged records into the K (warps 6, 7) / V (8, 9) ring ----------------
-            // A warp takes the tokens 8 part .. 8 part + 7 of every record.
-            const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
+            // ---------------- fp4: widen staged records into the K (warps 6-9) / V (10-13) ring ----------------
+            // A warp takes one record of the tile.
+            const int tensor = (warp - 6) / C::CW, rc = (warp - 6) % C::CW;
+            static_assert(!F4 || C::CW == C::CPT, "a widening warp per record of a tile");
             const int NR = tensor == 0 ? NK : NV;
             uint64_t *ring_full = tensor == 0 ? k_full : v_full;
             uint64_t *ring_empty = tensor == 0 ? k_empty : v_empty;
@@ -756,28 +757,27 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     flags[0] = 1;
                     break;
                 }
-                const uint8_t *stg_tile = stg + (i % NSG) * C::STG_BYTES;
-                uint8_t *ring_tile = ring + (i % NR) * C::TILE_BYTES;
-                const int t0 = (c_begin + i * CPT) * kChunk;
+                const uint8_t *rec = stg + (i % NSG) * C::STG_BYTES + rc * REC;
+                uint8_t *ring_rows = ring + (i % NR) * C::TILE_BYTES + rc * kChunk * 128;
+                const int t0 = (c_begin + i * CPT + rc) * kChunk;
                 if (tensor == 0) {
-                    // lane: token r, quarter c of every block; r and r + 4 in the same quarter-warp, so that its
-                    // eight 16-byte ring writes fall in eight bank groups (rows past the tile's end may hold
-                    // anything: their scores are masked)
+                    // lane: token r of a half, quarter c of every block; r and r + 4 in the same quarter-warp, so
+                    // that its eight 16-byte ring writes fall in eight bank groups (rows past the tile's end may
+                    // hold anything: their scores are masked)
                     const int c = lane & 3, r = ((lane >> 3) & 3) | (lane & 4);
-#pragma unroll 2
-                    for (int rc = 0; rc < CPT; ++rc) {
-                        const uint8_t *rec = stg_tile + rc * REC;
-                        uint8_t *dst = ring_tile + (rc * kChunk + 8 * part + r) * 128;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint8_t *dst = ring_rows + (8 * half + r) * 128;
                         uint32_t sc[NBL / 4];
 #pragma unroll
                         for (int q = 0; q < NBL / 4; q += 2) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * part + r) * NBL + 4 * q);
+                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * half + r) * NBL + 4 * q);
                             sc[q] = w.x;
                             sc[q + 1] = w.y;
                         }
 #pragma unroll
                         for (int j = 0; j < NBL / 8; ++j) {
-                            const uint4 kw = *reinterpret_cast<const uint4 *>(rec + (2 * j + part) * 512 + (4 * r + c) * 16);
+                            const uint4 kw = *reinterpret_cast<const uint4 *>(rec + (2 * j + half) * 512 + (4 * r + c) * 16);
                             const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1
@@ -795,46 +795,48 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     }
                 } else {
                     const int c = lane & 3, r = lane >> 2;
-#pragma unroll 2
-                    for (int rc = 0; rc < CPT; ++rc) {
-                        const uint8_t *rec = stg_tile + rc * REC;
-                        const int ta = 8 * part + 2 * c;  // the lane's tokens ta, ta + 1 of the record
-                        // rows outside the block's visible keys may hold anything: their scales become 0
-                        const int tg = t0 + rc * kChunk + ta;
-                        const uint32_t vm = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
-                                            (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
-                        uint32_t wd[2][NBL / 4];
+                    uint32_t wd[4][NBL / 4];  // the lane's tokens u = 2 half + par: 8 half + 2 c + par
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                    for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                            for (int q = 0; q < NBL / 4; q += 2) {
-                                const uint2 w = *reinterpret_cast<const uint2 *>(rec + (2 * part + e) * 2 * D + lane * NBL + 4 * q);
-                                wd[e][q] = w.x;
-                                wd[e][q + 1] = w.y;
-                            }
+                        for (int q = 0; q < NBL / 4; q += 2) {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + u * 2 * D + lane * NBL + 4 * q);
+                            wd[u][q] = w.x;
+                            wd[u][q + 1] = w.y;
                         }
-                        uint8_t *dst = ring_tile + (rc * kChunk + ta) * 128;
-                        const int p0 = (r ^ (2 * c)) << 4, p1 = (r ^ (2 * c + 1)) << 4;
+                    }
+                    // rows outside the block's visible keys may hold anything: their scales become 0
+                    uint32_t vm[2];
 #pragma unroll
-                        for (int w = 0; w < NBL / 4; ++w) {
-                            uint32_t s2[4];  // scale pairs (tokens ta, ta + 1) of blocks 4 w .. 4 w + 3
-                            const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
-                            const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
+                    for (int half = 0; half < 2; ++half) {
+                        const int tg = t0 + 8 * half + 2 * c;
+                        vm[half] = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
+                                   (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
+                    }
+                    uint8_t *dst = ring_rows + 2 * c * 128;
+                    const int p0 = (r ^ (2 * c)) << 4, p1 = (r ^ (2 * c + 1)) << 4;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t lo2, hi2;
-                                fp4::e4m3x4_f16(sb[q], lo2, hi2);
-                                s2[q] = (part == 0 ? lo2 : hi2) & vm;
-                            }
+                    for (int w = 0; w < NBL / 4; ++w) {
+                        uint32_t s2[2][4];  // [half]: scale pairs of its two tokens, blocks 4 w .. 4 w + 3
+                        const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
+                        const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            fp4::e4m3x4_f16(sb[q], s2[0][q], s2[1][q]);
+                            s2[0][q] &= vm[0];
+                            s2[1][q] &= vm[1];
+                        }
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
                             uint32_t a[4];
-                            fp4::e2m1x8_f16(wd[0][w], a);
-                            *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + p0) =
-                                make_uint4(fp4::hmul2_lo(a[0], s2[0]), fp4::hmul2_lo(a[1], s2[1]),
-                                           fp4::hmul2_lo(a[2], s2[2]), fp4::hmul2_lo(a[3], s2[3]));
-                            fp4::e2m1x8_f16(wd[1][w], a);
-                            *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + 128 + p1) =
-                                make_uint4(fp4::hmul2_hi(a[0], s2[0]), fp4::hmul2_hi(a[1], s2[1]),
-                                           fp4::hmul2_hi(a[2], s2[2]), fp4::hmul2_hi(a[3], s2[3]));
+                            fp4::e2m1x8_f16(wd[2 * half][w], a);
+                            *reinterpret_cast<uint4 *>(dst + half * 1024 + w * (TT * 128) + p0) =
+                                make_uint4(fp4::hmul2_lo(a[0], s2[half][0]), fp4::hmul2_lo(a[1], s2[half][1]),
+                                           fp4::hmul2_lo(a[2], s2[half][2]), fp4::hmul2_lo(a[3], s2[half][3]));
+                            fp4::e2m1x8_f16(wd[2 * half + 1][w], a);
+                            *reinterpret_cast<uint4 *>(dst + half * 1024 + 128 + w * (TT * 128) + p1) =
+                                make_uint4(fp4::hmul2_hi(a[0], s2[half][0]), fp4::hmul2_hi(a[1], s2[half][1]),
+                                           fp4::hmul2_hi(a[2], s2[half][2]), fp4::hmul2_hi(a[3], s2[half][3]));
                         }
                     }
                 }
