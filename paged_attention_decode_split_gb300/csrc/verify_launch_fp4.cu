@@ -6,10 +6,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int NK, int NV, int NSG>
-cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
+template <int D, int NK, int NV, int NSG, bool RES>
+cudaError_t launch_res(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = VerifyTcCfg<D, NK, NV, NSG, 2, 64, true>;
-    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true>;
+    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true, RES>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -26,13 +26,20 @@ cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int 
     return cudaLaunchKernelEx(&cfg, kern, none, none, none, none, p);
 }
 
+// bf16 outputs go without the P residual (two kernel slots per layout)
+template <int D, int NK, int NV, int NSG>
+cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
+    return p.out_bf16 ? launch_res<D, NK, NV, NSG, false>(p, grid, stream, slot)
+                      : launch_res<D, NK, NV, NSG, true>(p, grid, stream, slot + 1);
+}
+
 }  // namespace
 
 // The f16 rings of the fp8 form, and as many staging slots (9 KiB per tensor
 // and tile at D = 256, 4.5 KiB at D = 128) as fit beside them.
 cudaError_t launch_verify_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
-    if (head_dim == 256) return launch_t<256, 2, 3, 3>(p, grid, stream, 144);
-    if (head_dim == 128) return launch_t<128, 5, 5, 6>(p, grid, stream, 145);
+    if (head_dim == 256) return launch_t<256, 2, 3, 3>(p, grid, stream, 140);
+    if (head_dim == 128) return launch_t<128, 5, 5, 6>(p, grid, stream, 142);
     return cudaErrorInvalidValue;
 }
 

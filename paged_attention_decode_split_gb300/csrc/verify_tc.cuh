@@ -291,13 +291,17 @@ struct VerifyTcCfg {
 // tm_k64 / tm_v64: 5-D boxes of a whole 64-token tile, both with the 128-byte
 // swizzle).
 // tm_k64: 5-D boxes of a whole K tile of TK keys (64, or 128 with TK = 128).
-template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false>
+// RES: the residual of P is multiplied too (F4 with bf16 output goes without:
+// a weight is then off by at most 2^-12, an eighth of the half step that the
+// output is rounded by).
+template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
                         const VerifyParams p) {
     using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>;
     constexpr bool F8 = C::F8, QSM = C::QSM;
+    static_assert(RES || (F4 && C::VPK == 1), "the residual is left out over an fp4 cache only");
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
     extern __shared__ uint8_t smem_dyn[];
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                             // V: MN-major; 64-dim blocks TT x 128 B apart (LBO), 8-token groups 1 KiB apart (SBO)
                             const uint64_t bdesc = tc::sdesc(v_addr + ks * 16 * 128, TT * 128, 1024, 2);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                            for (int h = 0; h < (RES ? 2 : 1); ++h) {
                                 // P (head, then residual) of this 64-key half: 16 tokens = 8 columns per step
                                 const uint32_t a_tm = tmem + C::SBUF(j) + h2 * TT + h * (TT / 2) + ks * 8;
                                 tc::mma_bf16_ta(tmem + C::O_COL, a_tm, bdesc, kIdPV,
@@ -1015,20 +1019,23 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 // with no visible key yet (m = -inf) every p is 0: 2^(x - inf)
                 const float m_use = m_ref == -INFINITY ? INFINITY : m_ref;
                 float2 ps2 = make_float2(0.f, 0.f);
-                uint32_t hw[TT / 2], lw[TT / 2];
+                uint32_t hw[TT / 2];
+                [[maybe_unused]] uint32_t lw[TT / 2];
 #pragma unroll
                 for (int c = 0; c < TT / 2; ++c) {
                     const float p0 = fast_exp2(fmaf(sv[2 * c], mul, -m_use));
                     const float p1 = fast_exp2(fmaf(sv[2 * c + 1], mul, -m_use));
                     ps2 = __fadd2_rn(ps2, make_float2(p0, p1));
-                    if constexpr (F8)
+                    if constexpr (!RES)
+                        hw[c] = pack_f16(p0, p1);
+                    else if constexpr (F8)
                         split_f16(p0, p1, hw[c], lw[c]);
                     else
                         split_bf16(p0, p1, hw[c], lw[c]);
                 }
                 l_sum += ps2.x + ps2.y;
                 tc::st32(lane_base + C::SBUF(j), hw);
-                tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
+                if constexpr (RES) tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
                 tc::wait_st();
                 tc::fence_before();
             } else {
