@@ -10,6 +10,13 @@
 // no CTA waits for another and nothing that one CTA reads is written by
 // another (the new lengths and the new pool size go to buffers of their own),
 // so a call is one kernel and its results do not depend on any order.
+//
+// What bounds them is latency: a slot needs its request (a binary search over
+// the prefix), then its page (a table entry or a free-list entry), then a
+// store.  Up to 512 requests each thread keeps one request and its prefix in
+// shared memory, a slot's search reads nothing else, and a thread works on
+// four pairs of slots at once, each pair one 16-byte store; beyond that the
+// prefix is kept per group of requests and the group is walked.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -130,10 +137,191 @@ __device__ __forceinline__ bool served(const TableParams &p, const Request &q, D
     return q.ok && upto.rows <= p.num_tokens && (q.want == q.have || upto.pages <= F);
 }
 
-__global__ void __launch_bounds__(kTabThreads) pa_extend_block_tables_kernel(const TableParams p) {
+// ---- up to kTabThreads requests: one per thread --------------------------------
+
+// A request as the slot and page loops read it.
+struct Entry {
+    int32_t row_end, page_end;  // prefix sums, its own included (clamped to INT32_MAX)
+    int32_t rows, len;          // new tokens; tokens held
+    int32_t have, taken;        // pages held; pages taken (0 if refused)
+    int32_t served, pad;
+};
+
+struct FastPrefix {
+    int32_t row_end[kTabThreads], page_end[kTabThreads];
+    Entry e[kTabThreads];
+    int64_t pages;                       // wanted by all requests
+    unsigned long long moved;            // pages taken or returned by the served ones
+    Demand warp_sum[kTabThreads / 32];
+};
+
+// The first index whose (ascending) entry exceeds i; the entries past the
+// requests are INT32_MAX.
+__device__ __forceinline__ int upper(const int32_t *end, int32_t i) {
+    int b = 0;
+#pragma unroll
+    for (int step = kTabThreads / 2; step > 0; step >>= 1)
+        if (end[b + step - 1] <= i) b += step;
+    return b;
+}
+
+template <bool RELEASE>
+__device__ __forceinline__ int64_t build_fast(const TableParams &p, FastPrefix &f) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int raw_free = p.num_free[0];
+    Request q{0, 0, 0, 0, true};
+    Demand d{0, 0};
+    if (t < p.B) {
+        q = request<RELEASE>(p, t);
+        d = demand<RELEASE>(p, q);
+    }
+    Demand incl = d;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int64_t rows = __shfl_up_sync(0xffffffffu, incl.rows, k), pages = __shfl_up_sync(0xffffffffu, incl.pages, k);
+        if (lane >= k) incl = incl + Demand{rows, pages};
+    }
+    if (lane == 31) f.warp_sum[warp] = incl;
+    if (t == 0) f.moved = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTabThreads / 32; ++w)
+        if (w < warp) incl = incl + f.warp_sum[w];
+    const int64_t F = max((int64_t)0, min((int64_t)raw_free, p.num_pages));
+    // extend: pages and rows suffice up to this request; release: the pool has room up to it
+    const bool yes = RELEASE ? q.n != 0 && incl.pages <= p.num_pages - F : served(p, q, incl, F);
+    const bool live = t < p.B;
+    Entry e;
+    e.row_end = live ? (int32_t)min(incl.rows, (int64_t)INT32_MAX) : INT32_MAX;
+    e.page_end = live ? (int32_t)min(incl.pages, (int64_t)INT32_MAX) : INT32_MAX;
+    e.rows = q.n;
+    e.len = q.len;
+    e.have = q.have;
+    e.taken = yes ? (int32_t)d.pages : 0;
+    e.served = live && yes;
+    e.pad = 0;
+    f.row_end[t] = e.row_end;
+    f.page_end[t] = e.page_end;
+    f.e[t] = e;
+    if (t == kTabThreads - 1) f.pages = incl.pages;
+    if (blockIdx.x == 0) {
+        if (live) {
+            p.lens_out[t] = RELEASE ? (yes ? 0 : max(q.len, 0)) : yes ? q.len + q.n : max(q.len, 0);
+            if (!q.ok) set_status(p.status, PA_DEV_BAD_SEQLEN);
+            else if (RELEASE && q.n != 0 && !yes) set_status(p.status, PA_DEV_BAD_PAGE);
+            else if (!RELEASE && incl.rows > p.num_tokens && q.n > 0) set_status(p.status, PA_DEV_BAD_SLOT);
+            else if (!RELEASE && !yes && q.n > 0) set_status(p.status, PA_DEV_NO_PAGES);
+            if (yes && d.pages > 0) atomicMax(&f.moved, (unsigned long long)incl.pages);
+        }
+        if (t == 0 && F != raw_free) set_status(p.status, PA_DEV_BAD_PAGE);
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && t == 0)
+        p.num_free_out[0] = (int32_t)(RELEASE ? F + (int64_t)f.moved : F - (int64_t)f.moved);
+    return F;
+}
+
+__global__ void __launch_bounds__(kTabThreads) pa_extend_block_tables_few_kernel(const TableParams p) {
     // (no early launch of dependents: a kernel behind this one may start a
     // third one early, which must not read the tables before they are written)
     pdl_wait_primary();
+    __shared__ FastPrefix f;
+    const int64_t F = build_fast<false>(p, f);
+    const int64_t tid = (int64_t)blockIdx.x * kTabThreads + threadIdx.x, stride = (int64_t)gridDim.x * kTabThreads;
+
+    // slot of the token at offset `pos` of request b; its page by way of `lp`
+    auto page_at = [&](int b, const Entry &e, int lp) {
+        return lp < e.have ? p.table[(int64_t)b * p.width + lp]
+                           : p.free_pages[F - 1 - ((int64_t)e.page_end - e.taken + (lp - e.have))];
+    };
+    auto slot_in = [&](int page, int off) {
+        return page >= 0 && page < p.num_pages ? (int64_t)page * p.block_size + off : (int64_t)-1;
+    };
+    auto slot_of = [&](int32_t i) -> int64_t {
+        const int b = upper(f.row_end, i);
+        if (b >= p.B) return -1;
+        const Entry e = f.e[b];
+        if (!e.served || i >= e.row_end) return -1;  // (past the last row, upper() ends at the last entry)
+        const int pos = e.len + (i - (e.row_end - e.rows)), lp = pos / p.block_size;
+        return slot_in(page_at(b, e, lp), pos - lp * p.block_size);
+    };
+    constexpr int U = 4;
+    const int64_t n_pairs = ((int64_t)p.num_tokens + 1) / 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(p.slots) & 15u) == 0;
+    for (int64_t k0 = tid; k0 < n_pairs; k0 += U * stride) {
+        int page[U], off[U], left[U];  // left: tokens of the request from this one on, within its page
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {  // all searches and loads first
+            const int64_t k = k0 + u * stride;
+            on[u] = false;
+            page[u] = -1;
+            off[u] = left[u] = 0;
+            if (k < n_pairs) {
+                const int32_t i = (int32_t)(2 * k);
+                const int b = upper(f.row_end, i);
+                if (b < p.B) {
+                    const Entry e = f.e[b];
+                    if (e.served && i < e.row_end) {
+                        const int pos = e.len + (i - (e.row_end - e.rows)), lp = pos / p.block_size;
+                        off[u] = pos - lp * p.block_size;
+                        left[u] = min(e.row_end - i, p.block_size - off[u]);
+                        page[u] = page_at(b, e, lp);
+                        on[u] = true;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * stride;
+            if (k >= n_pairs) break;
+            const int64_t s0 = on[u] ? slot_in(page[u], off[u]) : -1;
+            const bool second = 2 * k + 1 < p.num_tokens;
+            int64_t s1 = -1;
+            if (second) s1 = left[u] > 1 ? (s0 < 0 ? -1 : s0 + 1) : slot_of((int32_t)(2 * k + 1));
+            if (second && vec) {
+                *reinterpret_cast<longlong2 *>(p.slots + 2 * k) = make_longlong2(s0, s1);
+            } else {
+                p.slots[2 * k] = s0;
+                if (second) p.slots[2 * k + 1] = s1;
+            }
+        }
+    }
+    // table entry of the k-th page taken from the pool
+    const int64_t pages = min(f.pages, F);
+#pragma unroll 4
+    for (int64_t k = tid; k < pages; k += stride) {
+        const int page = p.free_pages[F - 1 - k];
+        const int b = upper(f.page_end, (int32_t)k);
+        const Entry e = f.e[b];
+        if (e.taken == 0) continue;  // refused
+        if (page < 0 || page >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
+        p.table[(int64_t)b * p.width + e.have + (k - (e.page_end - e.taken))] = page;
+    }
+}
+
+__global__ void __launch_bounds__(kTabThreads) pa_release_block_tables_few_kernel(const TableParams p) {
+    pdl_wait_primary();  // (no early launch of dependents, as above)
+    __shared__ FastPrefix f;
+    const int64_t F = build_fast<true>(p, f);
+    const int64_t tid = (int64_t)blockIdx.x * kTabThreads + threadIdx.x, stride = (int64_t)gridDim.x * kTabThreads;
+    const int64_t pages = min(f.pages, p.num_pages - F);
+#pragma unroll 4
+    for (int64_t k = tid; k < pages; k += stride) {  // the k-th returned page
+        const int b = upper(f.page_end, (int32_t)k);
+        const Entry e = f.e[b];
+        if (e.taken == 0) continue;  // refused: the pool has no room for all of its pages
+        const int page = p.table[(int64_t)b * p.width + (k - (e.page_end - e.taken))];
+        if (page < 0 || page >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
+        p.free_pages[F + k] = page;
+    }
+}
+
+// ---- more requests: the prefix kept per group ----------------------------------
+
+__global__ void __launch_bounds__(kTabThreads) pa_extend_block_tables_kernel(const TableParams p) {
+    pdl_wait_primary();  // (no early launch of dependents, as above)
     __shared__ Prefix f;
     const int per = (p.B + kTabThreads - 1) / kTabThreads;
     build_prefix<false>(p, per, f);
@@ -304,7 +492,8 @@ pa_status pa_extend_block_tables(const int32_t *context_lens, const int32_t *num
                         num_tokens};
     const pa_status st = check_tables(p, num_tokens > 0 ? static_cast<const void *>(slot_mapping) : free_pages);
     if (st != PA_OK) return st;
-    return launch_tables(pa_extend_block_tables_kernel, p, num_tokens, stream);
+    return launch_tables(num_seqs <= kTabThreads ? pa_extend_block_tables_few_kernel : pa_extend_block_tables_kernel, p,
+                         num_tokens, stream);
 }
 
 pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,
@@ -315,7 +504,8 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
                         nullptr, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size, 0};
     const pa_status st = check_tables(p, free_pages);
     if (st != PA_OK) return st;
-    return launch_tables(pa_release_block_tables_kernel, p, (int64_t)num_seqs * max_pages_per_seq, stream);
+    return launch_tables(num_seqs <= kTabThreads ? pa_release_block_tables_few_kernel : pa_release_block_tables_kernel,
+                         p, (int64_t)num_seqs * max_pages_per_seq, stream);
 }
 
 }  // extern "C"

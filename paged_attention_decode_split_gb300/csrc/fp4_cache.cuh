@@ -125,53 +125,40 @@ __device__ __forceinline__ uint32_t code_byte(uint32_t w, float r) {
     return r == 0.f ? 0u : e2m1x2_rn(__fmul_rn(bf16lo(w), r), __fmul_rn(bf16hi(w), r));
 }
 
-// Quantises the 16-dim block `blk` of a new row (32 bytes at src) of token t
-// of the record at rec.  V: the V layout, else K's.
-template <int D, bool V>
-__device__ __forceinline__ void store_block(uint8_t *rec, int t, int blk, const uint4 *src, float g) {
-    const uint4 a = src[0], b = src[1];
+// Quantises a 16-dim block (32 bytes of bf16): its eight code bytes (dims 2 m,
+// 2 m + 1 in byte m) and its scale code.
+__device__ __forceinline__ uint2 quantise_block(const uint4 &a, const uint4 &b, float g, uint32_t &s) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t amax = 0;
 #pragma unroll
     for (int m = 0; m < 8; ++m) amax = max(amax, bf16x2_absmax(w[m]));
-    const uint32_t s = scale_code(amax, g);
+    s = scale_code(amax, g);
     const float r = code_factor(s, g);
+    uint32_t o[2] = {0u, 0u};
+#pragma unroll
+    for (int m = 0; m < 8; ++m) o[m >> 2] |= code_byte(w[m], r) << (8 * (m & 3));
+    return make_uint2(o[0], o[1]);
+}
+
+__device__ __forceinline__ uint32_t byte_of(uint2 v, int m) { return ((m < 4 ? v.x : v.y) >> (8 * (m & 3))) & 0xffu; }
+
+// Quantises the 16-dim block `blk` of a new row (32 bytes at src) into token t
+// of the record at rec.  V: the V layout, else K's.
+template <int D, bool V>
+__device__ __forceinline__ void store_block(uint8_t *rec, int t, int blk, const uint4 *src, float g) {
+    uint32_t s;
+    const uint2 q = quantise_block(src[0], src[1], g, s);
     if constexpr (V) {
         uint8_t *p = rec + v_code_off<D>(t, blk);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) p[m * (D / 4)] = (uint8_t)code_byte(w[m], r);
+        for (int m = 0; m < 8; ++m) p[m * (D / 4)] = (uint8_t)byte_of(q, m);
         rec[v_scale_off<D>(t, blk)] = (uint8_t)s;
     } else {
         uint8_t *p = rec + k_code_off(t, blk);
 #pragma unroll
-        for (int m = 0; m < 8; m += 2)
-            *reinterpret_cast<uint16_t *>(p + m * 8) = (uint16_t)(code_byte(w[m], r) | (code_byte(w[m + 1], r) << 8));
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint16_t *>(p + c * 16) = (uint16_t)((c < 2 ? q.x : q.y) >> (16 * (c & 1)));
         rec[k_scale_off<D>(t, blk)] = (uint8_t)s;
-    }
-}
-
-// The 16 values of block `blk` of token t, without the head scale, as 8 f16 pairs.
-template <int D, bool V>
-__device__ __forceinline__ void load_block(const uint8_t *rec, int t, int blk, uint32_t (&o)[8], uint32_t &s) {
-    uint32_t w[2] = {0u, 0u};
-    if constexpr (V) {
-        const uint8_t *p = rec + v_code_off<D>(t, blk);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) w[m >> 2] |= (uint32_t)p[m * (D / 4)] << (8 * (m & 3));
-        s = rec[v_scale_off<D>(t, blk)];
-    } else {
-        const uint8_t *p = rec + k_code_off(t, blk);
-#pragma unroll
-        for (int m = 0; m < 8; m += 2)
-            w[m >> 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p + m * 8) << (8 * (m & 3));
-        s = rec[k_scale_off<D>(t, blk)];
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        uint32_t q[4];
-        e2m1x8_f16(w[k], q);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) o[4 * k + m] = q[m];
     }
 }
 
