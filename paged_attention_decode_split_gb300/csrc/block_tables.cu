@@ -11,12 +11,16 @@
 // another (the new lengths and the new pool size go to buffers of their own),
 // so a call is one kernel and its results do not depend on any order.
 //
-// What bounds them is latency: a slot needs its request (a binary search over
-// the prefix), then its page (a table entry or a free-list entry), then a
-// store.  Up to 512 requests each thread keeps one request and its prefix in
-// shared memory, a slot's search reads nothing else, and a thread works on
-// four pairs of slots at once, each pair one 16-byte store; beyond that the
-// prefix is kept per group of requests and the group is walked.
+// What bounds them is latency, and for many tokens the index arithmetic: a slot
+// needs its request (a binary search over the prefix), then its page (a table
+// entry or a free-list entry), then a store.  Up to 512 requests each thread
+// keeps one request and its prefix in shared memory, and a thread writes a run
+// of consecutive slots from one search, searching again only where a page or a
+// request ends: runs of two, which fill the GPU up to 311,000 tokens, and of
+// eight beyond that (a step of 32 single tokens: 3.6 us against 7.3 with runs
+// of eight; 1M slots: 8.0 against 9.7 us).  CTAs of their own write the table
+// entries.  Beyond 512 requests the prefix is kept per group of requests and
+// the group is walked.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -26,6 +30,7 @@ namespace pa {
 namespace {
 
 constexpr int kTabThreads = 512;
+constexpr int64_t kMost = 304;  // CTAs of 512 threads: two on each of 152 SMs
 
 struct TableParams {
     const int32_t *lens;      // [B] tokens held
@@ -39,6 +44,7 @@ struct TableParams {
     int32_t *status;
     int64_t num_pages;        // P
     int B, width, block_size, num_tokens;
+    int slot_ctas;  // extend, up to 512 requests: the CTAs that write slots (the others: table entries)
 };
 
 // A request's demand: rows it takes in the packed batch and pages it wants.
@@ -137,7 +143,7 @@ __device__ __forceinline__ bool served(const TableParams &p, const Request &q, D
     return q.ok && upto.rows <= p.num_tokens && (q.want == q.have || upto.pages <= F);
 }
 
-// ---- up to kTabThreads requests: one per thread --------------------------------
+// ---- up to 512 requests: one per thread of CTAs of T = 128, 256 or 512 -----------
 
 // A request as the slot and page loops read it.
 struct Entry {
@@ -147,153 +153,149 @@ struct Entry {
     int32_t served, pad;
 };
 
+// Prefix sums that stop at 2^32 - 1: what passes the rows or the pages there are
+// is refused either way.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < a ? 0xffffffffu : s;
+}
+
+template <int T>
 struct FastPrefix {
-    int32_t row_end[kTabThreads], page_end[kTabThreads];
-    Entry e[kTabThreads];
-    int64_t pages;                       // wanted by all requests
-    unsigned long long moved;            // pages taken or returned by the served ones
-    Demand warp_sum[kTabThreads / 32];
+    int32_t row_end[T], page_end[T];
+    Entry e[T];
+    uint32_t pages;  // wanted by all requests
+    uint32_t moved;  // pages taken or returned by the served ones
+    uint32_t warp_rows[T / 32], warp_pages[T / 32];
 };
 
 // The first index whose (ascending) entry exceeds i; the entries past the
 // requests are INT32_MAX.
+template <int T>
 __device__ __forceinline__ int upper(const int32_t *end, int32_t i) {
     int b = 0;
 #pragma unroll
-    for (int step = kTabThreads / 2; step > 0; step >>= 1)
+    for (int step = T / 2; step > 0; step >>= 1)
         if (end[b + step - 1] <= i) b += step;
     return b;
 }
 
-template <bool RELEASE>
-__device__ __forceinline__ int64_t build_fast(const TableParams &p, FastPrefix &f) {
+template <bool RELEASE, int T>
+__device__ __forceinline__ int build_fast(const TableParams &p, FastPrefix<T> &f) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int raw_free = p.num_free[0];
+    const bool live = t < p.B;
     Request q{0, 0, 0, 0, true};
-    Demand d{0, 0};
-    if (t < p.B) {
-        q = request<RELEASE>(p, t);
-        d = demand<RELEASE>(p, q);
-    }
-    Demand incl = d;
+    if (live) q = request<RELEASE>(p, t);
+    const int wants = RELEASE ? (q.n != 0 ? q.have : 0) : q.want - q.have;
+    uint32_t rows = RELEASE ? 0u : (uint32_t)q.n, pages = (uint32_t)wants;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
-        const int64_t rows = __shfl_up_sync(0xffffffffu, incl.rows, k), pages = __shfl_up_sync(0xffffffffu, incl.pages, k);
-        if (lane >= k) incl = incl + Demand{rows, pages};
+        const uint32_t r = __shfl_up_sync(0xffffffffu, rows, k), g = __shfl_up_sync(0xffffffffu, pages, k);
+        if (lane >= k) {
+            rows = add_sat(rows, r);
+            pages = add_sat(pages, g);
+        }
     }
-    if (lane == 31) f.warp_sum[warp] = incl;
+    if (lane == 31) {
+        f.warp_rows[warp] = rows;
+        f.warp_pages[warp] = pages;
+    }
     if (t == 0) f.moved = 0;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kTabThreads / 32; ++w)
-        if (w < warp) incl = incl + f.warp_sum[w];
-    const int64_t F = max((int64_t)0, min((int64_t)raw_free, p.num_pages));
+    for (int w = 0; w < T / 32; ++w)
+        if (w < warp) {
+            rows = add_sat(rows, f.warp_rows[w]);
+            pages = add_sat(pages, f.warp_pages[w]);
+        }
+    const int F = (int)max((int64_t)0, min((int64_t)raw_free, p.num_pages));
     // extend: pages and rows suffice up to this request; release: the pool has room up to it
-    const bool yes = RELEASE ? q.n != 0 && incl.pages <= p.num_pages - F : served(p, q, incl, F);
-    const bool live = t < p.B;
+    const bool fits_rows = rows <= (uint32_t)p.num_tokens;
+    const bool yes = RELEASE ? q.n != 0 && pages <= (uint32_t)(p.num_pages - F)
+                             : q.ok && fits_rows && (wants == 0 || pages <= (uint32_t)F);
     Entry e;
-    e.row_end = live ? (int32_t)min(incl.rows, (int64_t)INT32_MAX) : INT32_MAX;
-    e.page_end = live ? (int32_t)min(incl.pages, (int64_t)INT32_MAX) : INT32_MAX;
+    e.row_end = live ? (int32_t)min(rows, 0x7fffffffu) : INT32_MAX;
+    e.page_end = live ? (int32_t)min(pages, 0x7fffffffu) : INT32_MAX;
     e.rows = q.n;
     e.len = q.len;
     e.have = q.have;
-    e.taken = yes ? (int32_t)d.pages : 0;
+    e.taken = yes ? wants : 0;
     e.served = live && yes;
     e.pad = 0;
     f.row_end[t] = e.row_end;
     f.page_end[t] = e.page_end;
     f.e[t] = e;
-    if (t == kTabThreads - 1) f.pages = incl.pages;
+    if (t == T - 1) f.pages = pages;
     if (blockIdx.x == 0) {
         if (live) {
             p.lens_out[t] = RELEASE ? (yes ? 0 : max(q.len, 0)) : yes ? q.len + q.n : max(q.len, 0);
             if (!q.ok) set_status(p.status, PA_DEV_BAD_SEQLEN);
             else if (RELEASE && q.n != 0 && !yes) set_status(p.status, PA_DEV_BAD_PAGE);
-            else if (!RELEASE && incl.rows > p.num_tokens && q.n > 0) set_status(p.status, PA_DEV_BAD_SLOT);
+            else if (!RELEASE && !fits_rows && q.n > 0) set_status(p.status, PA_DEV_BAD_SLOT);
             else if (!RELEASE && !yes && q.n > 0) set_status(p.status, PA_DEV_NO_PAGES);
-            if (yes && d.pages > 0) atomicMax(&f.moved, (unsigned long long)incl.pages);
+            if (yes && wants > 0) atomicMax(&f.moved, pages);
         }
         if (t == 0 && F != raw_free) set_status(p.status, PA_DEV_BAD_PAGE);
     }
     __syncthreads();
-    if (blockIdx.x == 0 && t == 0)
-        p.num_free_out[0] = (int32_t)(RELEASE ? F + (int64_t)f.moved : F - (int64_t)f.moved);
+    if (blockIdx.x == 0 && t == 0) p.num_free_out[0] = RELEASE ? F + (int)f.moved : F - (int)f.moved;
     return F;
 }
 
-__global__ void __launch_bounds__(kTabThreads) pa_extend_block_tables_few_kernel(const TableParams p) {
+template <int T, int U>  // U: slots per thread
+__global__ void __launch_bounds__(T) pa_extend_block_tables_few_kernel(const TableParams p) {
     // (no early launch of dependents: a kernel behind this one may start a
     // third one early, which must not read the tables before they are written)
     pdl_wait_primary();
-    __shared__ FastPrefix f;
-    const int64_t F = build_fast<false>(p, f);
-    const int64_t tid = (int64_t)blockIdx.x * kTabThreads + threadIdx.x, stride = (int64_t)gridDim.x * kTabThreads;
+    __shared__ FastPrefix<T> f;
+    const int F = build_fast<false, T>(p, f);
+    const bool slots = (int)blockIdx.x < p.slot_ctas;
+    const int64_t tid = (int64_t)(slots ? blockIdx.x : blockIdx.x - p.slot_ctas) * T + threadIdx.x;
+    const int64_t stride = (int64_t)(slots ? p.slot_ctas : gridDim.x - p.slot_ctas) * T;
 
-    // slot of the token at offset `pos` of request b; its page by way of `lp`
-    auto page_at = [&](int b, const Entry &e, int lp) {
-        return lp < e.have ? p.table[(int64_t)b * p.width + lp]
-                           : p.free_pages[F - 1 - ((int64_t)e.page_end - e.taken + (lp - e.have))];
-    };
-    auto slot_in = [&](int page, int off) {
-        return page >= 0 && page < p.num_pages ? (int64_t)page * p.block_size + off : (int64_t)-1;
-    };
-    auto slot_of = [&](int32_t i) -> int64_t {
-        const int b = upper(f.row_end, i);
+    // the slot of token i, and how many tokens from it on have slots in a row
+    // (-1: tokens without one, of a refused request or past the last row)
+    auto find = [&](int32_t i, int &run) -> int64_t {
+        const int b = upper<T>(f.row_end, i);
+        run = INT32_MAX;
         if (b >= p.B) return -1;
         const Entry e = f.e[b];
-        if (!e.served || i >= e.row_end) return -1;  // (past the last row, upper() ends at the last entry)
-        const int pos = e.len + (i - (e.row_end - e.rows)), lp = pos / p.block_size;
-        return slot_in(page_at(b, e, lp), pos - lp * p.block_size);
+        if (i >= e.row_end) return -1;  // (past the last row, upper() ends at the last entry)
+        run = e.row_end - i;
+        if (!e.served) return -1;
+        const int pos = e.len + (i - (e.row_end - e.rows)), lp = pos / p.block_size, off = pos - lp * p.block_size;
+        run = min(run, p.block_size - off);
+        const int page = lp < e.have ? p.table[(int64_t)b * p.width + lp]
+                                     : p.free_pages[F - 1 - (e.page_end - e.taken + (lp - e.have))];
+        return page >= 0 && page < p.num_pages ? (int64_t)page * p.block_size + off : -1;
     };
-    constexpr int U = 4;
-    const int64_t n_pairs = ((int64_t)p.num_tokens + 1) / 2;
     const bool vec = (reinterpret_cast<uintptr_t>(p.slots) & 15u) == 0;
-    for (int64_t k0 = tid; k0 < n_pairs; k0 += U * stride) {
-        int page[U], off[U], left[U];  // left: tokens of the request from this one on, within its page
-        bool on[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {  // all searches and loads first
-            const int64_t k = k0 + u * stride;
-            on[u] = false;
-            page[u] = -1;
-            off[u] = left[u] = 0;
-            if (k < n_pairs) {
-                const int32_t i = (int32_t)(2 * k);
-                const int b = upper(f.row_end, i);
-                if (b < p.B) {
-                    const Entry e = f.e[b];
-                    if (e.served && i < e.row_end) {
-                        const int pos = e.len + (i - (e.row_end - e.rows)), lp = pos / p.block_size;
-                        off[u] = pos - lp * p.block_size;
-                        left[u] = min(e.row_end - i, p.block_size - off[u]);
-                        page[u] = page_at(b, e, lp);
-                        on[u] = true;
-                    }
-                }
-            }
-        }
+    for (int64_t i0 = U * tid; slots && i0 < p.num_tokens; i0 += U * stride) {
+        int64_t slot[U], next = -1;
+        int run = 0;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * stride;
-            if (k >= n_pairs) break;
-            const int64_t s0 = on[u] ? slot_in(page[u], off[u]) : -1;
-            const bool second = 2 * k + 1 < p.num_tokens;
-            int64_t s1 = -1;
-            if (second) s1 = left[u] > 1 ? (s0 < 0 ? -1 : s0 + 1) : slot_of((int32_t)(2 * k + 1));
-            if (second && vec) {
-                *reinterpret_cast<longlong2 *>(p.slots + 2 * k) = make_longlong2(s0, s1);
-            } else {
-                p.slots[2 * k] = s0;
-                if (second) p.slots[2 * k + 1] = s1;
-            }
+            if (run == 0 && i0 + u < p.num_tokens) next = find((int32_t)(i0 + u), run);
+            slot[u] = next;
+            if (next >= 0) ++next;
+            --run;
+        }
+        if (vec && i0 + U <= p.num_tokens) {
+#pragma unroll
+            for (int u = 0; u < U; u += 2)
+                *reinterpret_cast<longlong2 *>(p.slots + i0 + u) = make_longlong2(slot[u], slot[u + 1]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < p.num_tokens) p.slots[i0 + u] = slot[u];
         }
     }
     // table entry of the k-th page taken from the pool
-    const int64_t pages = min(f.pages, F);
-#pragma unroll 4
-    for (int64_t k = tid; k < pages; k += stride) {
+    const int64_t pages = min(f.pages, (uint32_t)F);
+    for (int64_t k = tid; !slots && k < pages; k += stride) {
         const int page = p.free_pages[F - 1 - k];
-        const int b = upper(f.page_end, (int32_t)k);
+        const int b = upper<T>(f.page_end, (int32_t)k);
         const Entry e = f.e[b];
         if (e.taken == 0) continue;  // refused
         if (page < 0 || page >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
@@ -301,20 +303,31 @@ __global__ void __launch_bounds__(kTabThreads) pa_extend_block_tables_few_kernel
     }
 }
 
-__global__ void __launch_bounds__(kTabThreads) pa_release_block_tables_few_kernel(const TableParams p) {
+template <int T>
+__global__ void __launch_bounds__(T) pa_release_block_tables_few_kernel(const TableParams p) {
     pdl_wait_primary();  // (no early launch of dependents, as above)
-    __shared__ FastPrefix f;
-    const int64_t F = build_fast<true>(p, f);
-    const int64_t tid = (int64_t)blockIdx.x * kTabThreads + threadIdx.x, stride = (int64_t)gridDim.x * kTabThreads;
-    const int64_t pages = min(f.pages, p.num_pages - F);
-#pragma unroll 4
-    for (int64_t k = tid; k < pages; k += stride) {  // the k-th returned page
-        const int b = upper(f.page_end, (int32_t)k);
-        const Entry e = f.e[b];
-        if (e.taken == 0) continue;  // refused: the pool has no room for all of its pages
-        const int page = p.table[(int64_t)b * p.width + (k - (e.page_end - e.taken))];
-        if (page < 0 || page >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
-        p.free_pages[F + k] = page;
+    __shared__ FastPrefix<T> f;
+    const int F = build_fast<true, T>(p, f);
+    const int64_t tid = (int64_t)blockIdx.x * T + threadIdx.x, stride = (int64_t)gridDim.x * T;
+    const int64_t pages = min((int64_t)f.pages, p.num_pages - F);
+    constexpr int U = 4;
+    for (int64_t k0 = tid; k0 < pages; k0 += U * stride) {  // the k-th returned page, four at once
+        int page[U];
+        bool on[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = min(k0 + u * stride, pages - 1);
+            const int b = upper<T>(f.page_end, (int32_t)k);
+            const Entry e = f.e[b];
+            on[u] = e.taken > 0 && k0 + u * stride < pages;  // (refused: the pool has no room for all of its pages)
+            page[u] = *(on[u] ? p.table + ((int64_t)b * p.width + (k - (e.page_end - e.taken))) : p.num_free);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!on[u]) continue;
+            if (page[u] < 0 || page[u] >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
+            p.free_pages[F + k0 + u * stride] = page[u];
+        }
     }
 }
 
@@ -460,11 +473,14 @@ pa_status check_tables(const TableParams &p, const void *slots_needed) {
     return PA_OK;
 }
 
-pa_status launch_tables(void (*kern)(TableParams), const TableParams &p, int64_t items, void *stream) {
+int64_t ctas_for(int64_t items, int per_thread, int threads) {
+    return std::max<int64_t>(1, (items + (int64_t)per_thread * threads - 1) / ((int64_t)per_thread * threads));
+}
+
+pa_status launch_tables(void (*kern)(TableParams), const TableParams &p, int64_t ctas, int threads, void *stream) {
     cudaLaunchConfig_t cfg = {};
-    // about four items per thread, at most two CTAs on each of 152 SMs
-    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(304, (items + 4 * kTabThreads - 1) / (4 * kTabThreads))));
-    cfg.blockDim = dim3(kTabThreads);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -487,13 +503,25 @@ pa_status pa_extend_block_tables(const int32_t *context_lens, const int32_t *num
                                  int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages, int32_t num_tokens,
                                  int32_t *seq_lens, int64_t *slot_mapping, int32_t *num_free_out,
                                  int32_t *device_status, void *stream) {
-    const TableParams p{context_lens, num_new, block_table, const_cast<int32_t *>(free_pages), num_free, seq_lens,
-                        slot_mapping, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size,
-                        num_tokens};
+    TableParams p{context_lens, num_new, block_table, const_cast<int32_t *>(free_pages), num_free, seq_lens,
+                  slot_mapping, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size,
+                  num_tokens, 0};
     const pa_status st = check_tables(p, num_tokens > 0 ? static_cast<const void *>(slot_mapping) : free_pages);
     if (st != PA_OK) return st;
-    return launch_tables(num_seqs <= kTabThreads ? pa_extend_block_tables_few_kernel : pa_extend_block_tables_kernel, p,
-                         num_tokens, stream);
+    if (num_seqs > kTabThreads)
+        return launch_tables(pa_extend_block_tables_kernel, p, std::min(kMost, ctas_for(num_tokens, 4, kTabThreads)),
+                             kTabThreads, stream);
+    // as many threads as requests need (the scan of a small batch is shorter), 512 for many tokens
+    const bool few = num_tokens <= 2 * kMost * kTabThreads;
+    const int T = !few || num_seqs > 256 ? 512 : num_seqs > 128 ? 256 : 128, most = (int)(kMost * (512 / T));
+    p.slot_ctas = (int)std::min<int64_t>(most, ctas_for(num_tokens, few ? 2 : 8, T));
+    // every page taken holds a new token: at most one per block_size tokens, and one more per request
+    const int64_t page_ctas = std::min<int64_t>(most / 2, ctas_for((int64_t)num_tokens / block_size + num_seqs, 1, T));
+    auto *kern = !few       ? pa_extend_block_tables_few_kernel<512, 8>
+                 : T == 512 ? pa_extend_block_tables_few_kernel<512, 2>
+                 : T == 256 ? pa_extend_block_tables_few_kernel<256, 2>
+                            : pa_extend_block_tables_few_kernel<128, 2>;
+    return launch_tables(kern, p, p.slot_ctas + page_ctas, T, stream);
 }
 
 pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,
@@ -501,11 +529,16 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
                                   int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
                                   int32_t *seq_lens_out, int32_t *num_free_out, int32_t *device_status, void *stream) {
     const TableParams p{seq_lens, finished, const_cast<int32_t *>(block_table), free_pages, num_free, seq_lens_out,
-                        nullptr, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size, 0};
+                        nullptr, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size, 0, 0};
     const pa_status st = check_tables(p, free_pages);
     if (st != PA_OK) return st;
-    return launch_tables(num_seqs <= kTabThreads ? pa_release_block_tables_few_kernel : pa_release_block_tables_kernel,
-                         p, (int64_t)num_seqs * max_pages_per_seq, stream);
+    const int64_t items = (int64_t)num_seqs * max_pages_per_seq;
+    const int T = num_seqs > 256 ? 512 : num_seqs > 128 ? 256 : 128;
+    auto *kern = num_seqs > kTabThreads ? pa_release_block_tables_kernel
+                 : T == 512             ? pa_release_block_tables_few_kernel<512>
+                 : T == 256             ? pa_release_block_tables_few_kernel<256>
+                                        : pa_release_block_tables_few_kernel<128>;
+    return launch_tables(kern, p, std::min<int64_t>(kMost * (512 / T), ctas_for(items, 4, T)), T, stream);
 }
 
 }  // extern "C"

@@ -20,7 +20,6 @@ struct RowCfg {
     static constexpr int RW = 32 / NB;       // rows per warp
     static constexpr int WARPS = 4;
     static constexpr int ROW_BYTES = D / 2;  // code bytes of a row
-    static constexpr int PIECE_V = NB;       // V bytes of a row that stand together
 };
 
 // Byte offset in a record of piece j of token t's codes: K's 16-byte pieces (j
