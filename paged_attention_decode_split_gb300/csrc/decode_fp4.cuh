@@ -104,8 +104,10 @@ __device__ __forceinline__ void append_new_row_fp4(const DecodeParams &p, int b,
     __syncwarp();
 }
 
-// NW warps, SPW stages per warp, RES: the P residual is multiplied too.
-template <int D, int NT, int NW, int SPW, bool RES>
+// NW warps, SPW stages per warp, RES: the P residual is multiplied too, PACK:
+// up to 4 heads, whose heads' and residuals' weights share the 8 columns of one
+// product (columns 4-7 repeat Q, and carry the residuals into P.V).
+template <int D, int NT, int NW, int SPW, bool RES, bool PACK>
 __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const Fp4Params fp) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
     constexpr int NB = C::NB, HS = C::HS, GMAX = C::GMAX, REC = C::REC;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         k_scale = p.k_scale[kvh];
         v_scale = p.v_scale[kvh];
         if (warp < NT) {
-            const int h = warp * 8 + r;
+            const int h = warp * 8 + (PACK ? r & 3 : r);
             const __nv_bfloat16 *qrow = p.q + ((size_t)b * p.num_q_heads + hq0 + (h < G ? h : 0)) * D;
 #pragma unroll
             for (int ks = 0; ks < NB; ++ks) qw[ks] = *reinterpret_cast<const uint2 *>(qrow + 16 * ks + 4 * c);
@@ -227,34 +229,24 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         }
         return (((size_t)page * hkv + kvh) * fp.chunks_per_page + in_page) * REC;
     };
-    int at_page = 0;    // where the copies of the last pair were: chunk of the page,
-    size_t at_rec = 0;  // byte offset of the record
-    auto issue = [&](int k, uint8_t *st, uint64_t *bar) {  // the warp's k-th item
+    // Lane 2 s + tensor issues the copies of one tensor into stage s (two copies
+    // by one lane took 0.3 us).  The bytes may land before the other lane's
+    // expect_tx: the phase cannot end before that lane's arrival.
+    const int tensor = lane & 1;
+    uint8_t *my_stage = ring + (lane >> 1) * C::STAGE_BYTES + tensor * 2 * REC;
+    uint64_t *my_bar = &bars[lane >> 1];
+    const uint8_t *my_cache = tensor == 0 ? p.k_cache : p.v_cache;
+    auto issue = [&](int k) {  // the warp's k-th item into the lane's stage
         bool two;
         const int i = item(k, two);
-        at_rec = record_of(c_begin + i, at_page);
-        mbar_arrive_expect_tx(bar, two ? 4 * REC : 2 * REC);
-        const bool joined = two && at_page + 1 < fp.chunks_per_page;  // one run of the page
-        const uint32_t bytes = joined ? 2 * REC : REC;
-        fp4::bulk_load(st, p.k_cache + at_rec, bytes, bar, policy);
-        fp4::bulk_load(st + 2 * REC, p.v_cache + at_rec, bytes, bar, policy);
+        int in_page;
+        const size_t rec = record_of(c_begin + i, in_page);
+        if (tensor == 0) mbar_arrive_expect_tx(my_bar, two ? 4 * REC : 2 * REC);
+        const bool joined = two && in_page + 1 < fp.chunks_per_page;  // one run of the page
+        fp4::bulk_load(my_stage, my_cache + rec, joined ? 2 * REC : REC, my_bar, policy);
         if (two && !joined) {
-            int in_page;
             const size_t rec2 = record_of(c_begin + i + 1, in_page);
-            fp4::bulk_load(st + REC, p.k_cache + rec2, REC, bar, policy);
-            fp4::bulk_load(st + 3 * REC, p.v_cache + rec2, REC, bar, policy);
-        }
-    };
-    // A refill: the next pair of a whole round lies 2 NW chunks on, mostly in the same page.
-    auto refill = [&](int k, uint8_t *st, uint64_t *bar) {
-        if (k < rounds && at_page + 2 * NW + 1 < fp.chunks_per_page) {
-            at_page += 2 * NW;
-            at_rec += 2 * NW * REC;
-            mbar_arrive_expect_tx(bar, 4 * REC);
-            fp4::bulk_load(st, p.k_cache + at_rec, 2 * REC, bar, policy);
-            fp4::bulk_load(st + 2 * REC, p.v_cache + at_rec, 2 * REC, bar, policy);
-        } else {
-            issue(k, st, bar);
+            fp4::bulk_load(my_stage + REC, my_cache + rec2, REC, my_bar, policy);
         }
     };
     const int i_new = (L - 1) / kChunk - c_begin;  // the split-relative chunk of the new row
@@ -263,24 +255,24 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     const int w_new = j_new < 0 ? (i_new >> 1) % NW : j_new < 2 * twos ? j_new >> 1 : j_new - twos;
     // The first copies go out stage by stage, not warp by warp: the copy engine
     // works them off in order, so the first pairs land while the later ones are
-    // still on their way (32K call: 19.7 us with both stages of a warp at once).
-    int n_issued = 0;
+    // still on their way (32K call: 19.7 us with all stages of a warp at once).
+    const bool my_first = lane < 2 * min(SPW, n_w);  // the lane has a first copy to issue
+    bool issued = false;
     if (p.early_kv) {
-        if (lane == 0)
-            for (; n_issued < min(SPW, n_w); ++n_issued) {
-                bool two;
-                const int i = item(n_issued, two);
-                if (i + (two ? 1 : 0) >= i_new) break;
-                issue(n_issued, ring + n_issued * C::STAGE_BYTES, &bars[n_issued]);
-            }
+        bool two;
+        const int i = item(lane >> 1, two);
+        if (my_first && i + (two ? 1 : 0) < i_new) {
+            issue(lane >> 1);
+            issued = true;
+        }
         pdl_wait_primary();
         load_q();
-    } else if (lane == 0 && n_w > 0 && (p.k_new == nullptr || n_w > 1 || warp != w_new)) {
-        issue(0, ring, &bars[0]);
-        n_issued = 1;
+    } else if (my_first && lane < 2 && (p.k_new == nullptr || n_w > 1 || warp != w_new)) {
+        issue(0);
+        issued = true;
     }
     if (warp < NT) {
-        if (warp * 8 + r >= G) {  // heads past the group
+        if (warp * 8 + (PACK ? r & 3 : r) >= G) {  // heads past the group
 #pragma unroll
             for (int ks = 0; ks < NB; ++ks) qw[ks] = make_uint2(0u, 0u);
         }
@@ -306,9 +298,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         if (page >= 0 && (int64_t)page < p.num_pages)  // (a bad page is flagged when its chunk is copied)
             append_new_row_fp4<D>(p, b, kvh, L - 1, page);
     }
-    if (lane == 0)
-        for (; n_issued < min(SPW, n_w); ++n_issued)
-            issue(n_issued, ring + n_issued * C::STAGE_BYTES, &bars[n_issued]);
+    if (my_first && !issued) issue(lane >> 1);
 
     // (an mbarrier rather than a CTA barrier: a warp whose copies the copy engine has yet to take holds no other up)
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, &flags[0]));
@@ -345,7 +335,8 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         const uint8_t *kb = ring + s * C::STAGE_BYTES, *vb = kb + 2 * REC;
         const int t_pair = k < rounds ? t_round : t_rest;
         // visible tokens [lead, nv) of the pair (the second half of a single chunk's stage holds stale bytes)
-        const int nv = min((k < rounds || warp < twos ? 2 : 1) * kChunk, L - t_pair);
+        const bool two = k < rounds || warp < twos;
+        const int nv = min((two ? 2 : 1) * kChunk, L - t_pair);
         const int lead = p.window > 0 ? max(0, L - p.window - t_pair) : 0;
         const bool partial = nv < 2 * kChunk || lead > 0;  // warp-uniform
 
@@ -369,12 +360,16 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         const uint8_t *ksc = scales, *vsc = scales + C::SC_BYTES / 2;
 
         // ---- S^T = K Q^T per chunk, two accumulators per n-tile (even / odd k-steps) ----
-        float sa[2][NT][2][4];
+        // x: log2 units, [chunk][n-tile][tokens r, r + 8][heads 2c, 2c + 1]
+        float x[2][NT][4];
+        auto scores = [&](auto chunks) {
+        constexpr int NCH = decltype(chunks)::value;
+        float sa[NCH][NT][2][4];
 #pragma unroll
         for (int j = 0; j < NB / 8; ++j) {
-            uint32_t kw[2][2][4], ks[2][2][4];  // [chunk][token r, r + 8]: codes and scale pairs of blocks 8 j .. + 7
+            uint32_t kw[NCH][2][4], ks[NCH][2][4];  // [chunk][token r, r + 8]: codes and scale pairs of blocks 8 j .. + 7
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch)
+            for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t *rec = kb + ch * REC;
@@ -389,7 +384,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) qf[nt] = q_frag[(nt * (NB / 2) + 4 * j + q) * 32 + lane];
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
+                for (int ch = 0; ch < NCH; ++ch) {
                     uint32_t a[4], e[4];
                     fp4::e2m1x8_f16(kw[ch][0][q], a);
                     fp4::e2m1x8_f16(kw[ch][1][q], e);
@@ -411,15 +406,21 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 }
             }
         }
-
-        // ---- online softmax on the fragments (log2 units): x[ch][nt][tokens r, r + 8][heads 2c, 2c + 1] ----
-        float x[2][NT][4];
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[ch][nt][q] = (sa[ch][nt][0][q] + sa[ch][nt][1][q]) * qsc[nt][q & 1];
+                for (int q = 0; q < 4; ++q)
+                    x[ch][nt][q] = ch < NCH ? (sa[ch < NCH ? ch : 0][nt][0][q] + sa[ch < NCH ? ch : 0][nt][1][q]) * qsc[nt][q & 1]
+                                            : -INFINITY;
+        };
+        if (two)
+            scores(std::integral_constant<int, 2>{});
+        else
+            scores(std::integral_constant<int, 1>{});
+
+        // ---- online softmax on the fragments ----
         if (partial) {
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
@@ -463,7 +464,8 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 }
         }
         // P^T fragments: head + residual, each transposed in registers
-        uint32_t bh[2][NT][2], bl[2][NT][2];
+        uint32_t bh[2][NT][2];
+        [[maybe_unused]] uint32_t bl[2][NT][2];
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
@@ -477,8 +479,13 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 if constexpr (RES) {
                     split_f16(pr[0], pr[1], h01, r01);
                     split_f16(pr[2], pr[3], h23, r23);
-                    bl[ch][nt][0] = mm::movt(r01);
-                    bl[ch][nt][1] = mm::movt(r23);
+                    if constexpr (PACK) {
+                        h01 = c < 2 ? h01 : r01;
+                        h23 = c < 2 ? h23 : r23;
+                    } else {
+                        bl[ch][nt][0] = mm::movt(r01);
+                        bl[ch][nt][1] = mm::movt(r23);
+                    }
                 } else {
                     h01 = pack_f16(pr[0], pr[1]);
                     h23 = pack_f16(pr[2], pr[3]);
@@ -494,6 +501,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
             constexpr bool MASK = decltype(masked)::value;
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
+                if (MASK && ch == 1 && !two) break;
                 const uint8_t *rec = vb + ch * REC;
                 uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
                 if constexpr (MASK) {
@@ -546,9 +554,12 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bh[ch][nt][0], bh[ch][nt][1]);
+                            if constexpr (!PACK) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bl[ch][nt][0], bl[ch][nt][1]);
+                                for (int q = 0; q < 4; ++q)
+                                    mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bl[ch][nt][0],
+                                                  bl[ch][nt][1]);
+                            }
                         }
                     } else {
                         // the scales go to P instead (half the multiplies): P S rounds once more, by 2^-12
@@ -567,7 +578,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         else
             pv(std::false_type{});
         __syncwarp();  // every lane has read the stage
-        if (lane == 0 && k + SPW < n_w) refill(k + SPW, ring + s * C::STAGE_BYTES, &bars[s]);
+        if (lane >> 1 == s && k + SPW < n_w) issue(k + SPW);
         if (++s == SPW) {
             s = 0;
             phase ^= 1;
@@ -584,6 +595,14 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             l_run[nt][j] = l;
         }
+
+    if constexpr (PACK) {  // head and residual columns of a head: lanes c and c + 2
+        static_assert(RES && NT == 1, "packed residuals");
+#pragma unroll
+        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oacc[mt][0][i] += __shfl_xor_sync(0xffffffffu, oacc[mt][0][i], 2);
+    }
 
     // ---- CTA merge of the warps' states (log-sum-exp weights) ----
     // Every warp sees all warps' (m, l), scales its own sums by its weight over

@@ -6,10 +6,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int NT, int NW, int SPW, bool RES>
+template <int D, int NT, int NW, int SPW, bool RES, bool PACK>
 cudaError_t launch_res(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
-    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW, RES>;
+    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW, RES, PACK>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch, as for the other decode kernels
@@ -28,11 +28,15 @@ cudaError_t launch_res(int group, const DecodeParams &p, dim3 grid, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kern, p, fp);
 }
 
-// bf16 outputs go without the P residual (two kernel slots per layout)
+// bf16 outputs go without the P residual; up to 4 heads carry it in the unused
+// columns of the product.  Three kernel slots per layout.
 template <int D, int NT, int NW, int SPW>
 cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
-    return p.out_bf16 ? launch_res<D, NT, NW, SPW, false>(group, p, grid, stream, slot)
-                      : launch_res<D, NT, NW, SPW, true>(group, p, grid, stream, slot + 1);
+    if (p.out_bf16) return launch_res<D, NT, NW, SPW, false, false>(group, p, grid, stream, slot);
+    if constexpr (NT == 1) {
+        if (group <= 4) return launch_res<D, NT, NW, SPW, true, true>(group, p, grid, stream, slot + 2);
+    }
+    return launch_res<D, NT, NW, SPW, true, false>(group, p, grid, stream, slot + 1);
 }
 
 }  // namespace
@@ -42,10 +46,10 @@ cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t s
 cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     if (head_dim == 256)
         return group <= 8 ? launch_t<256, 1, 8, 2>(group, p, grid, stream, 146)
-                          : launch_t<256, 2, 8, 2>(group, p, grid, stream, 148);
+                          : launch_t<256, 2, 8, 2>(group, p, grid, stream, 149);
     if (head_dim == 128)
-        return group <= 8 ? launch_t<128, 1, 12, 3>(group, p, grid, stream, 150)
-                          : launch_t<128, 2, 8, 4>(group, p, grid, stream, 152);
+        return group <= 8 ? launch_t<128, 1, 12, 3>(group, p, grid, stream, 151)
+                          : launch_t<128, 2, 8, 4>(group, p, grid, stream, 154);
     return cudaErrorInvalidValue;
 }
 
