@@ -107,7 +107,10 @@ __device__ __forceinline__ void append_new_row_fp4(const DecodeParams &p, int b,
 // NW warps, SPW stages per warp, RES: the P residual is multiplied too, PACK:
 // up to 4 heads, whose heads' and residuals' weights share the 8 columns of one
 // product (columns 4-7 repeat Q, and carry the residuals into P.V).
-template <int D, int NT, int NW, int SPW, bool RES, bool PACK>
+// FAR: the accumulators are moved to a second sum every kFp4FarPairs of a
+// warp's pairs (splits that give a warp kFp4FarMin pairs or more, fp32 output).
+constexpr int kFp4FarPairs = 64, kFp4FarMin = 96;
+template <int D, int NT, int NW, int SPW, bool RES, bool PACK, bool FAR>
 __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const Fp4Params fp) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
     constexpr int NB = C::NB, HS = C::HS, GMAX = C::GMAX, REC = C::REC;
@@ -318,6 +321,16 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
             for (int i = 0; i < 4; ++i) oacc[mt][nt][i] = 0.f;
     }
 
+    // The tensor core cuts each addition to an accumulator off towards zero: the
+    // accumulators lose 2.4e-9 of themselves per key.  FAR moves them to a sum in
+    // local memory every kFar pairs (2048 keys: 5e-6), unless fewer than half as
+    // many follow.  A kernel of its own: it costs the other one 0.5 us of 16.5.
+    constexpr int kFar = kFp4FarPairs;
+    static_assert(!FAR || (RES && !PACK), "a second sum of O: fp32 output");
+    [[maybe_unused]] volatile float o_far[FAR ? NB * NT * 4 : 1];  // (volatile: kept out of the registers)
+    [[maybe_unused]] volatile float m_far[FAR ? NT * 2 : 1];       // the reference maxima that o_far stands for
+    auto far_weight = [&](int nt, int j) { return fast_exp2(m_far[2 * nt + j] - m_run[nt][j]); };
+
     int s = 0;
     uint32_t phase = 0;
     const int t_rest = (c_begin + 2 * NW * rounds + warp + min(warp, twos)) * kChunk;
@@ -363,57 +376,57 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         // x: log2 units, [chunk][n-tile][tokens r, r + 8][heads 2c, 2c + 1]
         float x[2][NT][4];
         auto scores = [&](auto chunks) {
-        constexpr int NCH = decltype(chunks)::value;
-        float sa[NCH][NT][2][4];
+            constexpr int NCH = decltype(chunks)::value;
+            float sa[NCH][NT][2][4];
 #pragma unroll
-        for (int j = 0; j < NB / 8; ++j) {
-            uint32_t kw[NCH][2][4], ks[NCH][2][4];  // [chunk][token r, r + 8]: codes and scale pairs of blocks 8 j .. + 7
+            for (int j = 0; j < NB / 8; ++j) {
+                uint32_t kw[NCH][2][4], ks[NCH][2][4];  // [chunk][token r, r + 8]: codes and scale pairs of blocks 8 j .. + 7
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch)
+                for (int ch = 0; ch < NCH; ++ch)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t *rec = kb + ch * REC;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(rec + (2 * j + h) * 512 + lane * 16);
-                    const uint4 sw = *reinterpret_cast<const uint4 *>(ksc + ((ch * 16 + r + 8 * h) * NB + 8 * j) * 2);
-                    kw[ch][h][0] = w.x; kw[ch][h][1] = w.y; kw[ch][h][2] = w.z; kw[ch][h][3] = w.w;
-                    ks[ch][h][0] = sw.x; ks[ch][h][1] = sw.y; ks[ch][h][2] = sw.z; ks[ch][h][3] = sw.w;
-                }
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t *rec = kb + ch * REC;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(rec + (2 * j + h) * 512 + lane * 16);
+                        const uint4 sw = *reinterpret_cast<const uint4 *>(ksc + ((ch * 16 + r + 8 * h) * NB + 8 * j) * 2);
+                        kw[ch][h][0] = w.x; kw[ch][h][1] = w.y; kw[ch][h][2] = w.z; kw[ch][h][3] = w.w;
+                        ks[ch][h][0] = sw.x; ks[ch][h][1] = sw.y; ks[ch][h][2] = sw.z; ks[ch][h][3] = sw.w;
+                    }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1: one word of each token
-                uint4 qf[NT];
+                for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1: one word of each token
+                    uint4 qf[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) qf[nt] = q_frag[(nt * (NB / 2) + 4 * j + q) * 32 + lane];
+                    for (int nt = 0; nt < NT; ++nt) qf[nt] = q_frag[(nt * (NB / 2) + 4 * j + q) * 32 + lane];
 #pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    uint32_t a[4], e[4];
-                    fp4::e2m1x8_f16(kw[ch][0][q], a);
-                    fp4::e2m1x8_f16(kw[ch][1][q], e);
-                    const uint32_t t0 = ks[ch][0][q], t1 = ks[ch][1][q];  // scales of the even (low) and odd block
-                    const uint32_t a0 = fp4::hmul2_lo(a[0], t0), a1 = fp4::hmul2_lo(a[1], t0);
-                    const uint32_t a2 = fp4::hmul2_hi(a[2], t0), a3 = fp4::hmul2_hi(a[3], t0);
-                    const uint32_t e0 = fp4::hmul2_lo(e[0], t1), e1 = fp4::hmul2_lo(e[1], t1);
-                    const uint32_t e2 = fp4::hmul2_hi(e[2], t1), e3 = fp4::hmul2_hi(e[3], t1);
+                    for (int ch = 0; ch < NCH; ++ch) {
+                        uint32_t a[4], e[4];
+                        fp4::e2m1x8_f16(kw[ch][0][q], a);
+                        fp4::e2m1x8_f16(kw[ch][1][q], e);
+                        const uint32_t t0 = ks[ch][0][q], t1 = ks[ch][1][q];  // scales of the even (low) and odd block
+                        const uint32_t a0 = fp4::hmul2_lo(a[0], t0), a1 = fp4::hmul2_lo(a[1], t0);
+                        const uint32_t a2 = fp4::hmul2_hi(a[2], t0), a3 = fp4::hmul2_hi(a[3], t0);
+                        const uint32_t e0 = fp4::hmul2_lo(e[0], t1), e1 = fp4::hmul2_lo(e[1], t1);
+                        const uint32_t e2 = fp4::hmul2_hi(e[2], t1), e3 = fp4::hmul2_hi(e[3], t1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (j == 0 && q == 0) {
-                            fp4::mma0_f16(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
-                            fp4::mma0_f16(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
-                        } else {
-                            mm::mma<true>(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
-                            mm::mma<true>(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (j == 0 && q == 0) {
+                                fp4::mma0_f16(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
+                                fp4::mma0_f16(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
+                            } else {
+                                mm::mma<true>(sa[ch][nt][0], a0, e0, a1, e1, qf[nt].x, qf[nt].y);
+                                mm::mma<true>(sa[ch][nt][1], a2, e2, a3, e3, qf[nt].z, qf[nt].w);
+                            }
                         }
                     }
                 }
             }
-        }
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
+            for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    x[ch][nt][q] = ch < NCH ? (sa[ch < NCH ? ch : 0][nt][0][q] + sa[ch < NCH ? ch : 0][nt][1][q]) * qsc[nt][q & 1]
-                                            : -INFINITY;
+                    for (int q = 0; q < 4; ++q)
+                        x[ch][nt][q] = ch < NCH ? (sa[ch < NCH ? ch : 0][nt][0][q] + sa[ch < NCH ? ch : 0][nt][1][q]) * qsc[nt][q & 1]
+                                                : -INFINITY;
         };
         if (two)
             scores(std::integral_constant<int, 2>{});
@@ -582,6 +595,40 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         if (++s == SPW) {
             s = 0;
             phase ^= 1;
+        }
+        if constexpr (FAR) {
+            if (k % kFar == kFar - 1 && n_w - k > kFp4FarMin - kFar) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float w = k < kFar ? 0.f : far_weight(nt, j);
+#pragma unroll
+                        for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+                            for (int h = 0; h < 4; h += 2) {
+                                volatile float &far = o_far[(mt * NT + nt) * 4 + j + h];
+                                far = k < kFar ? oacc[mt][nt][j + h] : fmaf(far, w, oacc[mt][nt][j + h]);
+                                oacc[mt][nt][j + h] = 0.f;
+                            }
+                        m_far[2 * nt + j] = m_run[nt][j];
+                    }
+            }
+        }
+    }
+    if constexpr (FAR) {
+        if (n_w >= kFp4FarMin && ok) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float w = far_weight(nt, j);
+#pragma unroll
+                    for (int mt = 0; mt < NB; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 4; h += 2)
+                            oacc[mt][nt][j + h] = fmaf(o_far[(mt * NT + nt) * 4 + j + h], w, oacc[mt][nt][j + h]);
+                }
         }
     }
     // exponential sums: a lane holds tokens r and r + 8; sum over r

@@ -6,10 +6,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int NT, int NW, int SPW, bool RES, bool PACK>
+template <int D, int NT, int NW, int SPW, bool RES, bool PACK, bool FAR>
 cudaError_t launch_res(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
-    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW, RES, PACK>;
+    auto kern = pa_decode_fp4_kernel<D, NT, NW, SPW, RES, PACK, FAR>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch, as for the other decode kernels
@@ -28,15 +28,19 @@ cudaError_t launch_res(int group, const DecodeParams &p, dim3 grid, cudaStream_t
     return cudaLaunchKernelEx(&cfg, kern, p, fp);
 }
 
-// bf16 outputs go without the P residual; up to 4 heads carry it in the unused
-// columns of the product.  Three kernel slots per layout.
+// bf16 outputs go without the P residual; fp32 outputs of splits so long that a
+// warp's accumulators need the second sum have a kernel of their own; up to 4
+// heads carry the residual in the unused columns of the product.  Four kernel
+// slots per layout.
 template <int D, int NT, int NW, int SPW>
 cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t stream, int slot) {
-    if (p.out_bf16) return launch_res<D, NT, NW, SPW, false, false>(group, p, grid, stream, slot);
+    if (p.out_bf16) return launch_res<D, NT, NW, SPW, false, false, false>(group, p, grid, stream, slot);
+    if (p.chunks_per_split > 2 * NW * (kFp4FarMin - 1))
+        return launch_res<D, NT, NW, SPW, true, false, true>(group, p, grid, stream, slot + 1);
     if constexpr (NT == 1) {
-        if (group <= 4) return launch_res<D, NT, NW, SPW, true, true>(group, p, grid, stream, slot + 2);
+        if (group <= 4) return launch_res<D, NT, NW, SPW, true, true, false>(group, p, grid, stream, slot + 3);
     }
-    return launch_res<D, NT, NW, SPW, true, false>(group, p, grid, stream, slot + 1);
+    return launch_res<D, NT, NW, SPW, true, false, false>(group, p, grid, stream, slot + 2);
 }
 
 }  // namespace
@@ -46,10 +50,10 @@ cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t s
 cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     if (head_dim == 256)
         return group <= 8 ? launch_t<256, 1, 8, 2>(group, p, grid, stream, 146)
-                          : launch_t<256, 2, 8, 2>(group, p, grid, stream, 149);
+                          : launch_t<256, 2, 8, 2>(group, p, grid, stream, 150);
     if (head_dim == 128)
-        return group <= 8 ? launch_t<128, 1, 12, 3>(group, p, grid, stream, 151)
-                          : launch_t<128, 2, 8, 4>(group, p, grid, stream, 154);
+        return group <= 8 ? launch_t<128, 1, 12, 3>(group, p, grid, stream, 153)
+                          : launch_t<128, 2, 8, 4>(group, p, grid, stream, 157);
     return cudaErrorInvalidValue;
 }
 

@@ -6,10 +6,10 @@ namespace pa {
 
 namespace {
 
-template <int D, int NK, int NV, int NSG, bool RES>
+template <int D, int NK, int NV, int NSG, bool RES, bool FAR>
 cudaError_t launch_res(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = VerifyTcCfg<D, NK, NV, NSG, 2, 64, true>;
-    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true, RES>;
+    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true, RES, FAR>;
     const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -26,11 +26,14 @@ cudaError_t launch_res(const VerifyParams &p, dim3 grid, cudaStream_t stream, in
     return cudaLaunchKernelEx(&cfg, kern, none, none, none, none, p);
 }
 
-// bf16 outputs go without the P residual (two kernel slots per layout)
+// bf16 outputs go without the P residual; fp32 outputs of long splits need the
+// second sum of O (three kernel slots per layout)
 template <int D, int NK, int NV, int NSG>
 cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
-    return p.out_bf16 ? launch_res<D, NK, NV, NSG, false>(p, grid, stream, slot)
-                      : launch_res<D, NK, NV, NSG, true>(p, grid, stream, slot + 1);
+    if (p.out_bf16) return launch_res<D, NK, NV, NSG, false, false>(p, grid, stream, slot);
+    if (p.chunks_per_split > (kVerifyFarMin - 1) * 4)
+        return launch_res<D, NK, NV, NSG, true, true>(p, grid, stream, slot + 1);
+    return launch_res<D, NK, NV, NSG, true, false>(p, grid, stream, slot + 2);
 }
 
 }  // namespace
@@ -39,7 +42,7 @@ cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int 
 // and tile at D = 256, 4.5 KiB at D = 128) as fit beside them.
 cudaError_t launch_verify_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
     if (head_dim == 256) return launch_t<256, 2, 3, 3>(p, grid, stream, 140);
-    if (head_dim == 128) return launch_t<128, 5, 5, 6>(p, grid, stream, 142);
+    if (head_dim == 128) return launch_t<128, 5, 5, 6>(p, grid, stream, 143);
     return cudaErrorInvalidValue;
 }
 

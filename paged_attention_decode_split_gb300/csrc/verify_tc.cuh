@@ -266,7 +266,9 @@ struct VerifyTcCfg {
     static constexpr int OFF_TMEM = OFF_BAR + (2 * NK + 2 * NV + 3 * NSB + 1 + 4 * NSG) * 8;
     static constexpr int OFF_FLAGS = OFF_TMEM + 16;
     static constexpr int OFF_PT = OFF_FLAGS + 16;                    // the split's block-table entries
-    static constexpr int SMEM_BYTES = OFF_PT + kVerifyPageTab * 4 + 1024;
+    static constexpr int OFF_NAN = OFF_PT + kVerifyPageTab * 4;      // fp4: NaN V blocks that some rows see
+    static constexpr int NAN_WORDS = F4 ? D / 16 * 8 : 0;
+    static constexpr int SMEM_BYTES = OFF_NAN + NAN_WORDS * 4 + 1024;
     // tensor-memory columns: O (fp32, D), NSB S/P buffers (TK each), Q (bf16
     // pairs, D / 2; not with QSM).  P of a score tile is written over its S
     // buffer, per 64-key half: a bf16 head in 32 columns, then the residual in 32.
@@ -294,7 +296,11 @@ struct VerifyTcCfg {
 // RES: the residual of P is multiplied too (F4 with bf16 output goes without:
 // a weight is then off by at most 2^-12, an eighth of the half step that the
 // output is rounded by).
-template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true>
+// FAR: O is moved to a second sum every kVerifyFarTiles tiles (splits of
+// kVerifyFarMin tiles and more with fp32 output).
+constexpr int kVerifyFarTiles = 32, kVerifyFarMin = 48;
+template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
+          bool FAR = false>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
@@ -303,6 +309,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     constexpr bool F8 = C::F8, QSM = C::QSM;
     static_assert(RES || (F4 && C::VPK == 1), "the residual is left out over an fp4 cache only");
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
+    static_assert(!FAR || (F4 && RES), "a second sum of O: fp4 cache with fp32 output");
+    constexpr int kFar = kVerifyFarTiles;
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -321,8 +329,13 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     uint64_t *vst_full = kst_empty + NSG;
     uint64_t *vst_empty = vst_full + NSG;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page, [2] nan_bits holds something
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
+    // F4: a V block with a NaN scale whose token only some of the rows see
+    // enters the product as zeros (0 * NaN would reach every row) and is noted
+    // here; the rows that see the token get their NaN in the epilogue.
+    // [scale block][0-3: token - (first row's last key + 1), 4-7: token - k_first]
+    uint32_t *nan_bits = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);
 
     const int split = blockIdx.x, b = blockIdx.z;
     const int kvh = blockIdx.y % p.num_kv_heads;
@@ -360,8 +373,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         }
         flags[0] = 0;
         flags[1] = 0;
+        flags[2] = 0;
         fence_mbar_init();
     }
+    for (int j = threadIdx.x; j < C::NAN_WORDS; j += C::THREADS) nan_bits[j] = 0;
     if (!F4 && warp == 5 && lane == 0) {  // (the fp4 records are copied without tensor maps)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -749,9 +764,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             uint64_t *stg_full = tensor == 0 ? kst_full : vst_full;
             uint64_t *stg_empty = tensor == 0 ? kst_empty : vst_empty;
             uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V);
-            const uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES;
+            uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES;
             constexpr int REC = fp4::rec_bytes(D), NBL = D / 16;
-            const int t_end = min(L, (c_begin + n_my) * kChunk);
+            const int t_end = min(k_last + 1, (c_begin + n_my) * kChunk);
+            // every row sees the tokens [w_last, f_last]
+            const int f_last = L - p.q_len + row0 / G, w_last = p.window > 0 ? k_last - p.window + 1 : 0;
             for (int i = 0; i < n_tiles; ++i) {
                 // the staged records have landed, and the ring slot's previous tile has been consumed
                 bool ok = __all_sync(0xffffffffu, mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]));
@@ -798,6 +815,29 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                         }
                     }
                 } else {
+                    // NaN scales of tokens hidden from some rows: noted, and 0 in the staged record
+                    if (t0 + kChunk - 1 > f_last || t0 < w_last) {
+                        constexpr int WB = D / 32;  // scale bytes of a lane
+                        uint8_t *sb = stg + (i % NSG) * C::STG_BYTES + rc * REC + 8 * D + lane * WB;
+                        uint32_t found = 0;
+#pragma unroll
+                        for (int o = 0; o < WB; o += 4)
+                            found |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(sb + o) & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        if (found != 0) {
+#pragma unroll 1
+                            for (int o = 0; o < WB; ++o) {
+                                const int at = lane * WB + o, blk = (at >> 6) * 4 + ((at >> 2) & 3);
+                                const int t = t0 + ((at >> 3) & 6) + (at & 1) + ((at & 2) << 2);
+                                if ((sb[o] & 0x7f) != 0x7f || t > k_last || t < k_first || (t <= f_last && t >= w_last))
+                                    continue;
+                                const int bit = t > f_last ? t - f_last - 1 : 128 + t - k_first;
+                                atomicOr(&nan_bits[blk * 8 + (bit >> 5)], 1u << (bit & 31));
+                                flags[2] = 1;
+                                sb[o] = 0;
+                            }
+                        }
+                        __syncwarp();
+                    }
                     const int c = lane & 3, r = lane >> 2;
                     uint32_t wd[4][NBL / 4];  // the lane's tokens u = 2 half + par: 8 half + 2 c + par
 #pragma unroll
@@ -920,6 +960,12 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
+        // The tensor core cuts each addition to the accumulator off towards
+        // zero: O loses 2.2e-9 of itself per key.  FAR moves O to this row's sum
+        // every kFar tiles (2048 keys: 5e-6), unless fewer than half as many
+        // follow.  A kernel of its own: it costs the other one 4 us of 74.
+        [[maybe_unused]] float o_far[FAR ? D : 1];  // (indexed at run time: local memory)
+        [[maybe_unused]] float m_far = -INFINITY;   // the reference max that o_far stands for
         bool ok = true;
         // O += P_k V_k of tile k is waited for in order per barrier (tile k +
         // NSB, where it is long finished), so no wait ever tests a phase parity
@@ -929,6 +975,28 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         };
         for (int i = 0; i < n_tiles; ++i) {
             const int j = i % NSB;
+            if constexpr (FAR) {
+                if (i > 0 && i % kFar == 0 && n_tiles - i >= kVerifyFarMin - kFar) {
+                    if (!wait_pv(i - 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const float alpha = m_far == -INFINITY ? 0.f : fast_exp2(m_far - m_ref);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        float ov[16];
+                        tc::ld16(lane_base + C::O_COL + c0, ov);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            o_far[c0 + c] = i == kFar ? ov[c] : fmaf(o_far[c0 + c], alpha, ov[c]);
+                            ov[c] = 0.f;
+                        }
+                        tc::st16(lane_base + C::O_COL + c0, ov);
+                    }
+                    m_far = m_ref;
+                }
+            }
             // waits ahead of a warp-collective tensor-memory access end the same way for the whole warp
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j], (i / NSB) & 1, &flags[0]))) {
                 ok = false;
@@ -1169,6 +1237,17 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         const bool poisoned = !ok || flags[1] != 0;
         const float inv = (poisoned || !(l_sum > 0.f)) ? 0.f : (F8 ? p.v_scale[kvh] : 1.f) / l_sum;
         const size_t orow = live ? ((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G : 0;
+        [[maybe_unused]] auto sees_nan = [&](int blk) {  // the row sees a token of nan_bits in this scale block
+            const int f_next = L - p.q_len + row0 / G + 1;
+            bool hit = false;
+            for (int w = 0; w < 8; ++w) {
+                for (uint32_t bits = nan_bits[blk * 8 + w]; bits != 0; bits &= bits - 1) {
+                    const int t = (w < 4 ? f_next + w * 32 : k_first + (w - 4) * 32) + __ffs(bits) - 1;
+                    hit |= t >= lo && t <= lim;
+                }
+            }
+            return hit;
+        };
         const bool direct = p.num_splits == 1;  // the final output, else this split's record
         if (ok) {
             // Every tile has been consumed by the tensor core, so the K/V rings
@@ -1178,6 +1257,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             // rows going out as 32 separate segments per store.
             const bool bf = direct && p.out_bf16;
             uint8_t *srow = smem + threadIdx.x * C::SROW;
+            const float far_w = m_far == -INFINITY ? 0.f : fast_exp2(m_far - m_ref);
+            [[maybe_unused]] const bool some_nan = F4 && flags[2] != 0;
 #pragma unroll 1
             for (int c1 = 0; c1 < D; c1 += 64) {
                 uint32_t r[4][16];  // 64 columns: four loads in flight, one wait
@@ -1192,10 +1273,20 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     for (int c = 0; c < 16; ++c) {
                         if constexpr (F4) {  // column 8 r' + 2 q + e of a 64-dim group holds dim 16 q + 2 r' + e
                             const int col = (c >> 1) * 8 + 2 * k + (c & 1);
+                            float o = __uint_as_float(r[col >> 4][col & 15]);
+                            if constexpr (FAR) {
+                                if (n_tiles >= kVerifyFarMin) o = fmaf(o_far[c1 + col], far_w, o);
+                            }
                             // (a bad page's stand-in may hold NaN)
-                            ov[c] = poisoned ? 0.f : __uint_as_float(r[col >> 4][col & 15]) * inv;
+                            ov[c] = poisoned ? 0.f : o * inv;
                         } else {
                             ov[c] = __uint_as_float(r[k][c]) * inv;
+                        }
+                    }
+                    if constexpr (F4) {
+                        if (some_nan && !poisoned && sees_nan(c0 / 16)) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) ov[c] = NAN;
                         }
                     }
                     if (bf) {

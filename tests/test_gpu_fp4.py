@@ -315,6 +315,64 @@ def test_a_visible_nan_shows_and_stays_in_its_head(what, splits, q_len):
     assert np.isfinite(out[:q_len, 4:]).all() and np.isfinite(out[q_len:]).all()
 
 
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("d,q_len,hq,hkv,window", [(128, 9, 12, 2, 0), (256, 60, 6, 1, 0), (128, 30, 8, 2, 7),
+                                                   (256, 40, 4, 4, 25)])
+def test_verify_rows_that_do_not_see_a_nan_stay_finite(what, d, q_len, hq, hkv, window):
+    """NaN scales in new rows that earlier rows do not see, and with a window in
+    rows that later rows do not see: the same rows and dims are NaN as by the formula."""
+    p = Problem(q_len + window, [q_len, 100, 203], hq, hkv, d, 16, q_len=q_len)
+    cache = p.k if what == "k" else p.v
+    for b, n in enumerate(p.lens):
+        for i, blk in ((q_len // 2, 1), (q_len - 1, 0), (q_len // 3, 5)):
+            t = n - q_len + i
+            cache[p.table[b, t // 16], i % hkv, 0, ref.byte_places(what, t % 16, d)[1][blk]] = 0x7F
+    if window:  # a row that the first rows see and the last ones do not
+        t = 203 - q_len - window + 4
+        cache[p.table[2, t // 16], 0, 0, ref.byte_places(what, t % 16, d)[1][3]] = 0xFF
+    want, mag, reach = ref.attention(p.q.float().numpy(), p.k, p.v, p.g, p.table, p.lens, p.scale, q_len, window)
+    clean = [np.where(np.isnan(x), 0.0, x) for x in (mag, reach)]
+    tol = ref.tolerance(*clean, d, max(p.lens), False, want)
+    assert np.isnan(want).any() and np.isfinite(want).any()
+    for kw in (dict(), dict(num_splits=1), dict(num_splits=3, flags=pa.PA_FLAG_EARLY_KV_READ)):
+        out, status = p.run(window=window, **kw)
+        assert status == 0
+        assert np.array_equal(np.isnan(out), np.isnan(want))
+        assert (np.abs(out - want) <= tol)[np.isfinite(want)].all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,q_len,length", [
+    (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (12, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
+    (16, 1, 128, 1, 40000), (6, 1, 256, 4, 20011), (8, 1, 128, 16, 40000)])
+def test_fp32_outputs_of_long_unsplit_contexts(hq, hkv, d, q_len, length):
+    """Against float64 over the rows read back.  The tensor core cuts additions
+    off towards zero: half a step, 2^-24 of at most 2048 / 16 x 2 growing sums
+    before they move to another sum, is a loss of 5.5e-6 at most on the
+    average (the mean of 1 / mantissa is 0.72, of a growing sum half its end);
+    what rounds both ways averages out below that.  1e-5 overall."""
+    rng = np.random.default_rng(length)
+    bs, pages = 784, -(-length // 784)
+    g = [ref.cuda(x) for x in ref.head_scales(hkv)]
+    cache = [torch.zeros(pa.fp4_cache_shape(pages, bs, hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    rows = [bf16_rows(rng, length, hkv, d).cuda() for _ in range(2)]
+    slots = torch.arange(length, device="cuda")
+    pa.reshape_and_cache_fp4(*rows, *cache, slots, *g)
+    k, v = (torch.empty((length, hkv, d), device="cuda") for _ in range(2))
+    pa.gather_cache_fp4(*cache, slots, *g, k, v)
+    q = bf16_rows(rng, q_len, hq, d).cuda()
+    desc = pa.make_desc(num_seqs=1, q_len=q_len, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs,
+                        max_pages_per_seq=pages, max_seq_len=length, num_pages=pages, scale=d ** -0.5, num_splits=1)
+    ws = torch.empty(max(1, pa.workspace_bytes(desc)), dtype=torch.uint8, device="cuda")
+    out = torch.empty((q_len, hq, d), device="cuda")
+    call = pa.paged_attention_decode_fp4 if q_len == 1 else pa.paged_attention_verify_fp4
+    call(q, *cache, *g, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+         torch.tensor([length], dtype=torch.int32, device="cuda"), desc, out, ws)
+    x = torch.einsum("qhd,td->qht", q.double(), k[:, 0].double()) * d ** -0.5
+    hidden = torch.arange(length, device="cuda") > length - q_len + torch.arange(q_len, device="cuda")[:, None]
+    want = x.masked_fill(hidden[:, None], -math.inf).softmax(-1) @ v[:, 0].double()
+    assert ((out.double() - want).norm() / want.norm()).item() <= 1e-5
+
+
 def test_offsets_past_32_bits():
     """Pages whose byte offset passes 2^32 in each cache."""
     bs, hkv, d = 784, 4, 256
