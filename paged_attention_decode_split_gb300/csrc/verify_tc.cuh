@@ -134,6 +134,12 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // D[tmem] (+)= A[smem] * B[smem], bf16 inputs, fp32 accumulate.
@@ -656,10 +662,25 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             set_status(p.status, PA_DEV_TIMEOUT);
         }
     } else if (warp == 4) {
-        // ---------------- MMA issue: one lane ----------------
-        if (lane == 0) {
+        // ---------------- MMA issue ----------------
+        // The warp runs the loop together and one elected lane issues, so that
+        // descriptors and addresses stay in uniform registers: issued by a
+        // branch of one lane, the 16 products of S_i took 720 clocks and more,
+        // not the tensor core's 517.
+        {
             constexpr uint32_t kIdQK = tc::idesc_bf16(128, TK, 0, F8);
             constexpr uint32_t kIdPV = tc::idesc_bf16(128, D, 1, F8);
+            const bool leader = tc::elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            // descriptors of the first K and V slots; offsets are added in 16-byte units
+            // K: 16-element k steps: +32 B inside a 128-byte swizzle row, next 64-dim block further on
+            // V: MN-major; 64-dim blocks TT x 128 B apart (LBO), 8-token groups 1 KiB apart (SBO)
+            const uint64_t k_desc0 = tc::sdesc(smem_addr(smem), 16, 1024, 2);
+            const uint64_t v_desc0 = tc::sdesc(smem_addr(smem + C::OFF_V), TT * 128, 1024, 2);
+            [[maybe_unused]] const uint64_t q_desc = tc::sdesc(smem_addr(smem + C::OFF_Q), 16, 1024, 2);
+            auto ready = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+            };
             // Event loop: each product is issued as soon as its own inputs are
             // ready -- O += P_i V_i when the softmax warps have written P_i,
             // S_i = Q K_i^T when tile i has landed and P_{i-2}, which shares
@@ -674,83 +695,87 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 // the V tiles of score tile next_pv (VPK, fewer at a split's end) have landed
                 auto v_ready = [&](int i) {
                     if constexpr (VPK == 1) {
-                        return mbar_test_wait(&v_full[i % NV], (i / NV) & 1);
+                        return ready(&v_full[i % NV], (i / NV) & 1);
                     } else {
                         const int nvt = min(VPK, n_vtiles - i * VPK);
                         for (int h2 = 0; h2 < nvt; ++h2) {
                             const int vt = i * VPK + h2;
-                            if (!mbar_test_wait(&v_full[vt % NV], (vt / NV) & 1)) return false;
+                            if (!ready(&v_full[vt % NV], (vt / NV) & 1)) return false;
                         }
                         return true;
                     }
                 };
-                if (next_pv < next_qk && mbar_test_wait(&p_full[next_pv % NSB], (next_pv / NSB) & 1) &&
-                    v_ready(next_pv)) {
+                if (next_pv < next_qk && ready(&p_full[next_pv % NSB], (next_pv / NSB) & 1) && v_ready(next_pv)) {
                     const int i = next_pv, j = i % NSB;
                     const int nvt = VPK == 1 ? 1 : min(VPK, n_vtiles - i * VPK);
                     tc::fence_after();
+                    if (leader) {
 #pragma unroll 1
-                    for (int h2 = 0; h2 < nvt; ++h2) {
-                        const int vt = i * VPK + h2;
-                        const uint32_t v_addr = smem_addr(smem + C::OFF_V + (vt % NV) * C::TILE_BYTES);
+                        for (int h2 = 0; h2 < nvt; ++h2) {
+                            const int vt = i * VPK + h2;
+                            const uint64_t v_desc = v_desc0 + (uint32_t)(vt % NV) * (C::TILE_BYTES >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < TT / 16; ++ks) {
-                            // V: MN-major; 64-dim blocks TT x 128 B apart (LBO), 8-token groups 1 KiB apart (SBO)
-                            const uint64_t bdesc = tc::sdesc(v_addr + ks * 16 * 128, TT * 128, 1024, 2);
+                            for (int ks = 0; ks < TT / 16; ++ks) {
 #pragma unroll
-                            for (int h = 0; h < (RES ? 2 : 1); ++h) {
-                                // P (head, then residual) of this 64-key half: 16 tokens = 8 columns per step
-                                const uint32_t a_tm = tmem + C::SBUF(j) + h2 * TT + h * (TT / 2) + ks * 8;
-                                tc::mma_bf16_ta(tmem + C::O_COL, a_tm, bdesc, kIdPV,
-                                                (i > 0 || h2 > 0 || ks > 0 || h > 0) ? 1u : 0u);
+                                for (int h = 0; h < (RES ? 2 : 1); ++h) {
+                                    // P (head, then residual) of this 64-key half: 16 tokens = 8 columns per step
+                                    const uint32_t a_tm = tm + C::SBUF(j) + h2 * TT + h * (TT / 2) + ks * 8;
+                                    tc::mma_bf16_ta(tm + C::O_COL, a_tm, v_desc + (ks * 16 * 128 >> 4), kIdPV,
+                                                    (i > 0 || h2 > 0 || ks > 0 || h > 0) ? 1u : 0u);
+                                }
                             }
+                            tc::commit(&v_empty[vt % NV]);
                         }
-                        tc::commit(&v_empty[vt % NV]);
+                        tc::commit(&o_done[j]);
                     }
-                    tc::commit(&o_done[j]);
+                    __syncwarp();
                     ++next_pv;
                     progress = true;
                 }
                 if (next_qk < n_tiles && next_qk - next_pv < NSB) {
                     const int i = next_qk, s = i % NK, j = i % NSB;
-                    if (mbar_test_wait(&k_full[s], (i / NK) & 1)) {
+                    if (ready(&k_full[s], (i / NK) & 1)) {
                         tc::fence_after();
-                        const uint32_t k_addr = smem_addr(smem + s * C::KTILE_BYTES);
+                        if (leader) {
+                            const uint64_t k_desc = k_desc0 + (uint32_t)s * (C::KTILE_BYTES >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            // 16-element k steps: +32 B inside a 128-byte swizzle row, next 64-dim block further on
-                            const uint32_t koff = (kk >> 2) * (TK * 128) + (kk & 3) * 32;
-                            if constexpr (QSM) {  // Q from shared memory, laid out like K with M rows
-                                const uint32_t qoff = (kk >> 2) * (C::M * 128) + (kk & 3) * 32;
-                                tc::mma_bf16(tmem + C::SBUF(j), tc::sdesc(smem_addr(smem + C::OFF_Q) + qoff, 16, 1024, 2),
-                                             tc::sdesc(k_addr + koff, 16, 1024, 2), kIdQK, kk > 0 ? 1u : 0u);
-                            } else {
-                                tc::mma_bf16_ta(tmem + C::SBUF(j), tmem + C::Q_COL + kk * 8,
-                                                tc::sdesc(k_addr + koff, 16, 1024, 2), kIdQK, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t koff = ((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4;
+                                if constexpr (QSM) {  // Q from shared memory, laid out like K with M rows
+                                    const uint32_t qoff = ((kk >> 2) * (C::M * 128) + (kk & 3) * 32) >> 4;
+                                    tc::mma_bf16(tm + C::SBUF(j), q_desc + qoff, k_desc + koff, kIdQK, kk > 0 ? 1u : 0u);
+                                } else {
+                                    tc::mma_bf16_ta(tm + C::SBUF(j), tm + C::Q_COL + kk * 8, k_desc + koff, kIdQK,
+                                                    kk > 0 ? 1u : 0u);
+                                }
                             }
+                            tc::commit(&k_empty[s]);
+                            tc::commit(&s_full[j]);
                         }
-                        tc::commit(&k_empty[s]);
-                        tc::commit(&s_full[j]);
+                        __syncwarp();
                         ++next_qk;
                         progress = true;
                     }
                 }
                 if (progress) {
                     idle = 0;
-                } else if (++idle > kWaitPollLimit || flags[0]) {
+                } else if (__any_sync(0xffffffffu, ++idle > kWaitPollLimit || flags[0] != 0)) {
                     ok = false;
                     break;
                 }
             }
-            if (!ok) {
-                flags[0] = 1;
-                set_status(p.status, PA_DEV_TIMEOUT);
+            if (leader) {
+                if (!ok) {
+                    flags[0] = 1;
+                    set_status(p.status, PA_DEV_TIMEOUT);
+                }
+                // Whatever happened, let every issued MMA finish before tensor
+                // memory is released at the end of the CTA.
+                tc::commit(mma_fin);
+                for (uint32_t n = 0; n < kWaitPollLimit && !mbar_try_wait(mma_fin, 0); ++n) {
+                }
             }
-            // Whatever happened, let every issued MMA finish before tensor
-            // memory is released at the end of the CTA.
-            tc::commit(mma_fin);
-            for (uint32_t n = 0; n < kWaitPollLimit && !mbar_try_wait(mma_fin, 0); ++n) {
-            }
+            __syncwarp();
         }
     } else if (warp >= 6) {
         if constexpr (F4) {
