@@ -678,41 +678,28 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             const uint64_t k_desc0 = tc::sdesc(smem_addr(smem), 16, 1024, 2);
             const uint64_t v_desc0 = tc::sdesc(smem_addr(smem + C::OFF_V), TT * 128, 1024, 2);
             [[maybe_unused]] const uint64_t q_desc = tc::sdesc(smem_addr(smem + C::OFF_Q), 16, 1024, 2);
-            auto ready = [&](uint64_t *bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait(bar, parity, &flags[0]));
             };
-            // Event loop: each product is issued as soon as its own inputs are
-            // ready -- O += P_i V_i when the softmax warps have written P_i,
-            // S_i = Q K_i^T when tile i has landed and P_{i-2}, which shares
-            // S_i's columns, has been consumed.  The tensor core runs this
-            // thread's MMAs in issue order, so S_i never overwrites P_{i-2}
-            // before O += P_{i-2} V_{i-2} has read it.
-            int next_qk = 0, next_pv = 0;
-            uint32_t idle = 0;
+            // S_i = Q K_i^T for the first NSB tiles, then per tile O += P_i V_i
+            // as soon as the softmax warps have written P_i, and S_{i+NSB},
+            // which shares P_i's columns: the tensor core runs this thread's
+            // MMAs in issue order, so S_{i+NSB} never overwrites P_i before
+            // O += P_i V_i has read it.  (Polling for whichever of the two was
+            // ready first left 0.3 us between a product's inputs and its issue:
+            // a fixed order can wait without polling.)
             bool ok = true;
-            while (next_pv < n_tiles) {
-                bool progress = false;
-                // the V tiles of score tile next_pv (VPK, fewer at a split's end) have landed
-                auto v_ready = [&](int i) {
-                    if constexpr (VPK == 1) {
-                        return ready(&v_full[i % NV], (i / NV) & 1);
-                    } else {
-                        const int nvt = min(VPK, n_vtiles - i * VPK);
-                        for (int h2 = 0; h2 < nvt; ++h2) {
-                            const int vt = i * VPK + h2;
-                            if (!ready(&v_full[vt % NV], (vt / NV) & 1)) return false;
-                        }
-                        return true;
-                    }
-                };
-                if (next_pv < next_qk && ready(&p_full[next_pv % NSB], (next_pv / NSB) & 1) && v_ready(next_pv)) {
-                    const int i = next_pv, j = i % NSB;
+            for (int step = 0; step < n_tiles + NSB; ++step) {
+                if (step >= NSB) {
+                    const int i = step - NSB, j = i % NSB;
                     const int nvt = VPK == 1 ? 1 : min(VPK, n_vtiles - i * VPK);
-                    tc::fence_after();
-                    if (leader) {
-#pragma unroll 1
-                        for (int h2 = 0; h2 < nvt; ++h2) {
-                            const int vt = i * VPK + h2;
+                    ok = wait(&p_full[j], (i / NSB) & 1);
+                    for (int h2 = 0; h2 < nvt && ok; ++h2) {
+                        const int vt = i * VPK + h2;
+                        ok = wait(&v_full[vt % NV], (vt / NV) & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        if (leader) {
                             const uint64_t v_desc = v_desc0 + (uint32_t)(vt % NV) * (C::TILE_BYTES >> 4);
 #pragma unroll
                             for (int ks = 0; ks < TT / 16; ++ks) {
@@ -725,43 +712,34 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                                 }
                             }
                             tc::commit(&v_empty[vt % NV]);
-                        }
-                        tc::commit(&o_done[j]);
-                    }
-                    __syncwarp();
-                    ++next_pv;
-                    progress = true;
-                }
-                if (next_qk < n_tiles && next_qk - next_pv < NSB) {
-                    const int i = next_qk, s = i % NK, j = i % NSB;
-                    if (ready(&k_full[s], (i / NK) & 1)) {
-                        tc::fence_after();
-                        if (leader) {
-                            const uint64_t k_desc = k_desc0 + (uint32_t)s * (C::KTILE_BYTES >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t koff = ((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4;
-                                if constexpr (QSM) {  // Q from shared memory, laid out like K with M rows
-                                    const uint32_t qoff = ((kk >> 2) * (C::M * 128) + (kk & 3) * 32) >> 4;
-                                    tc::mma_bf16(tm + C::SBUF(j), q_desc + qoff, k_desc + koff, kIdQK, kk > 0 ? 1u : 0u);
-                                } else {
-                                    tc::mma_bf16_ta(tm + C::SBUF(j), tm + C::Q_COL + kk * 8, k_desc + koff, kIdQK,
-                                                    kk > 0 ? 1u : 0u);
-                                }
-                            }
-                            tc::commit(&k_empty[s]);
-                            tc::commit(&s_full[j]);
+                            if (h2 == nvt - 1) tc::commit(&o_done[j]);
                         }
                         __syncwarp();
-                        ++next_qk;
-                        progress = true;
                     }
+                    if (!ok) break;
                 }
-                if (progress) {
-                    idle = 0;
-                } else if (__any_sync(0xffffffffu, ++idle > kWaitPollLimit || flags[0] != 0)) {
-                    ok = false;
-                    break;
+                if (step < n_tiles) {
+                    const int i = step, s = i % NK, j = i % NSB;
+                    ok = wait(&k_full[s], (i / NK) & 1);
+                    if (!ok) break;
+                    tc::fence_after();
+                    if (leader) {
+                        const uint64_t k_desc = k_desc0 + (uint32_t)s * (C::KTILE_BYTES >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t koff = ((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4;
+                            if constexpr (QSM) {  // Q from shared memory, laid out like K with M rows
+                                const uint32_t qoff = ((kk >> 2) * (C::M * 128) + (kk & 3) * 32) >> 4;
+                                tc::mma_bf16(tm + C::SBUF(j), q_desc + qoff, k_desc + koff, kIdQK, kk > 0 ? 1u : 0u);
+                            } else {
+                                tc::mma_bf16_ta(tm + C::SBUF(j), tm + C::Q_COL + kk * 8, k_desc + koff, kIdQK,
+                                                kk > 0 ? 1u : 0u);
+                            }
+                        }
+                        tc::commit(&k_empty[s]);
+                        tc::commit(&s_full[j]);
+                    }
+                    __syncwarp();
                 }
             }
             if (leader) {
@@ -807,10 +785,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 uint8_t *ring_rows = ring + (i % NR) * C::TILE_BYTES + rc * kChunk * 128;
                 const int t0 = (c_begin + i * CPT + rc) * kChunk;
                 if (tensor == 0) {
-                    // lane: token r of a half, quarter c of every block; r and r + 4 in the same quarter-warp, so
-                    // that its eight 16-byte ring writes fall in eight bank groups (rows past the tile's end may
-                    // hold anything: their scores are masked)
-                    const int c = lane & 3, r = ((lane >> 3) & 3) | (lane & 4);
+                    // lane: token r of a half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so
+                    // that its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups (rows
+                    // past the tile's end may hold anything: their scores are masked)
+                    const int c = lane & 3, r = (lane >> 3) ^ (lane & 4 ? 5 : 0);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint8_t *dst = ring_rows + (8 * half + r) * 128;
@@ -867,11 +845,13 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     uint32_t wd[4][NBL / 4];  // the lane's tokens u = 2 half + par: 8 half + 2 c + par
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-#pragma unroll
-                        for (int q = 0; q < NBL / 4; q += 2) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + u * 2 * D + lane * NBL + 4 * q);
-                            wd[u][q] = w.x;
-                            wd[u][q + 1] = w.y;
+                        const uint8_t *src = rec + u * 2 * D + lane * NBL;
+                        if constexpr (NBL == 16) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                            wd[u][0] = w.x, wd[u][1] = w.y, wd[u][2] = w.z, wd[u][3] = w.w;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                            wd[u][0] = w.x, wd[u][1] = w.y;
                         }
                     }
                     // rows outside the block's visible keys may hold anything: their scales become 0
@@ -981,6 +961,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // split's last chunk (a tile may reach into the next split's tokens)
         const int t_end = min(L, (c_begin + n_my) * kChunk);
         const int lim = live ? min(L - p.q_len + rho / G, t_end - 1) : -1;
+        // a warp without live rows only keeps the phases (its rows of S come from zeros of Q, its rows of O go nowhere)
+        const bool idle_warp = F4 && warp * 32 >= R;
         const int lo = p.window > 0 ? L - p.q_len + rho / G - p.window + 1 : 0;  // first key of the row's window
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
@@ -1032,6 +1014,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             // halves first and loads each half again for P (the one-load form
             // for 128 keys would not fit the registers, and the two-pass form
             // makes the fp8 variants spill).
+            if (idle_warp) {
+                mbar_arrive(&p_full[j]);
+                continue;
+            }
             if constexpr (VPK == 1) {
                 tc::fence_after();
                 float sv[TT];
@@ -1056,11 +1042,15 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 // scaled and masked scores with mul = 1
                 float mul = 1.f;
                 if (sl > 0.f && t0 + TT - 1 <= lim && t0 >= lo) {
-                    float mr = sv[0];
+                    float mr[4];  // four chains: one alone is 32 dependent steps
 #pragma unroll
-                    for (int c = 1; c + 1 < TT; c += 2) mr = fmax3(mr, sv[c], sv[c + 1]);
-                    mr = fmaxf(mr, sv[TT - 1]);
-                    mx = mr * sl;
+                    for (int c = 0; c < 4; ++c) mr[c] = fmax3(sv[c], sv[c + 4], sv[c + 8]);
+#pragma unroll
+                    for (int c = 12; c + 7 < TT; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mr[e] = fmax3(mr[e], sv[c + e], sv[c + e + 4]);
+                    mr[0] = fmaxf(fmax3(mr[0], sv[TT - 4], sv[TT - 3]), sv[TT - 2]);
+                    mx = fmaxf(fmax3(mr[0], mr[1], mr[2]), fmaxf(mr[3], sv[TT - 1])) * sl;
                     mul = sl;
                 } else {
 #pragma unroll
