@@ -267,9 +267,11 @@ struct VerifyTcCfg {
     static constexpr int OFF_Q = OFF_STG + 2 * NSG * STG_BYTES;  // QSM: Q as [D/64][M rows][128 B], swizzled
     static constexpr int Q_BYTES = QSM ? M * D * 2 : 0;
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
-    // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NSB], p_full[NSB], o_done[NSB], mma_fin,
-    // then (fp8) kst_full[NSG], kst_empty[NSG], vst_full[NSG], vst_empty[NSG]
-    static constexpr int OFF_TMEM = OFF_BAR + (2 * NK + 2 * NV + 3 * NSB + 1 + 4 * NSG) * 8;
+    // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NSB], p_full[NP], o_done[NSB], mma_fin,
+    // then (fp8, fp4) kst_full[NSG], kst_empty[NSG], vst_full[NSG], vst_empty[NSG]
+    static constexpr int CW = F4 ? 4 : 2;              // fp8, fp4: widening warps per tensor
+    static constexpr int NP = F8 ? NV : NSB;           // P barriers (fp8, fp4: the V slot's too)
+    static constexpr int OFF_TMEM = OFF_BAR + (2 * NK + 2 * NV + 2 * NSB + NP + 1 + 4 * NSG) * 8;
     static constexpr int OFF_FLAGS = OFF_TMEM + 16;
     static constexpr int OFF_PT = OFF_FLAGS + 16;                    // the split's block-table entries
     static constexpr int OFF_NAN = OFF_PT + kVerifyPageTab * 4;      // fp4: NaN V blocks that some rows see
@@ -284,10 +286,9 @@ struct VerifyTcCfg {
     static constexpr int Q_COL = D + NSB * TK;
     static constexpr int Q_TCOLS = QSM ? 0 : D / 2;
     static constexpr int SBUF(int j) { return S_COL + j * TK; }
-    static constexpr int CW = F4 ? 4 : 2;              // fp8, fp4: widening warps per tensor
     static constexpr int SROW = D * 4 + 16;            // epilogue: output rows staged in the K/V rings
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
-    static constexpr int THREADS = (F8 ? 6 + 2 * CW : 6) * 32;
+    static constexpr int THREADS = (F4 ? 7 + 2 * CW : F8 ? 6 + 2 * CW : 6) * 32;
     static_assert(D == 256 || D == 128, "head_dim 256 or 128");
     static_assert(Q_COL + Q_TCOLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(TK == 64 || (TK == 128 && !F8), "128-key score tiles: bf16 cache only");
@@ -327,10 +328,13 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     uint64_t *v_full = k_empty + NK;
     uint64_t *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV;   // [NSB]: S_i written (buffer i % NSB)
-    uint64_t *p_full = s_full + NSB;   // [NSB]: P_i written by the softmax warps
-    uint64_t *o_done = p_full + NSB;   // [NSB]: O += P_i V_i finished
+    // [NP] (i % NP): P_i written by the softmax warps and, over an fp8 or fp4
+    // cache, V_i widened: one wait for both (NP = NV then, so that V_i, whose
+    // slot O += P_{i-NV} V_{i-NV} has freed, never arrives on an open phase of P_{i-NV})
+    uint64_t *p_full = s_full + NSB;
+    uint64_t *o_done = p_full + C::NP;  // [NSB]: O += P_i V_i finished
     uint64_t *mma_fin = o_done + NSB;
-    uint64_t *kst_full = mma_fin + 1;  // fp8: e4m3 tile landed in a staging slot
+    uint64_t *kst_full = mma_fin + 1;  // fp8, fp4: cached tile landed in a staging slot
     uint64_t *kst_empty = kst_full + NSG;  // fp8: staging slot widened, free again
     uint64_t *vst_full = kst_empty + NSG;
     uint64_t *vst_empty = vst_full + NSG;
@@ -362,14 +366,14 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             mbar_init(&k_empty[s], 1);
         }
         for (int s = 0; s < NV; ++s) {
-            mbar_init(&v_full[s], F8 ? C::CW : 1);
+            mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], 1);
         }
         for (int j = 0; j < NSB; ++j) {
             mbar_init(&s_full[j], 1);
-            mbar_init(&p_full[j], 128);
             mbar_init(&o_done[j], 1);
         }
+        for (int j = 0; j < C::NP; ++j) mbar_init(&p_full[j], F8 ? 4 + C::CW : 4);
         mbar_init(mma_fin, 1);
         for (int s = 0; s < NSG; ++s) {
             mbar_init(&kst_full[s], 1);
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         const CUtensorMap *m5 = tensor == 0 ? &tm_k64 : &tm_v64;
         const int cpt = tensor == 0 ? CPK : CPT, tt = cpt * kChunk;  // chunks and tokens per tile
         const int nc = min(cpt, n_my - i * cpt);  // chunks in this tile
-        if (lane == 0) mbar_arrive_expect_tx(bar, nc * (F4 ? fp4::rec_bytes(D) : C::CHUNK_BYTES));
+        if (lane == 0) mbar_arrive_expect_tx(bar, nc * C::CHUNK_BYTES);
         __syncwarp();
         auto page_of = [&](int lp) {
             const int page = staged ? page_tab[lp - lp_first] : bt[lp];
@@ -480,23 +484,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         };
         const int t00 = (c_begin + i * cpt) * kChunk;
         const int lp0 = t00 / p.block_size, off0 = t00 - lp0 * p.block_size;
-        if constexpr (F4) {
-            // the chunks of a page are contiguous: one copy for a tile inside one page, else one per chunk
-            constexpr int REC = fp4::rec_bytes(D);
-            const bool whole = off0 + nc * kChunk <= p.block_size;
-            const int n_copies = whole ? 1 : nc;
-            if (lane < n_copies) {
-                const int t0 = t00 + lane * kChunk, lp = t0 / p.block_size;
-                int page = page_of(lp);
-                if (page < 0 || (int64_t)page >= p.num_pages) page = 0;  // (flagged: the rows are zeroed)
-                const size_t rec = (((size_t)page * p.num_kv_heads + kvh) * (p.block_size / kChunk) +
-                                    (t0 - lp * p.block_size) / kChunk) * REC;
-                fp4::bulk_load(dst0 + lane * REC, (tensor == 0 ? p.k_cache : p.v_cache) + rec,
-                               (whole ? nc : 1) * REC, bar, policy);
-            }
-            __syncwarp();
-            return;
-        }
         if (nc == cpt && off0 + tt <= p.block_size) {
             // the whole tile lies in one page: one copy lands it as [blocks][tt tokens][128 B]
             if (lane == 0) tma_load_5d(dst0, m5, bar, 0, off0, 0, kvh, page_of(lp0), policy);
@@ -509,13 +496,53 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         __syncwarp();
     };
     static_assert(CPK * (F8 ? D / 128 : C::DB) <= 32, "a lane per box of a tile");
+    // fp4: warp 5 copies K, the last warp V (a copy's issue takes one lane 0.15
+    // us: both tensors' would fill one warp's time).  A lane keeps the page and
+    // the place in it of its chunk of the next tile.
+    [[maybe_unused]] const int f4_tensor = warp == 5 ? 0 : 1, f4_cpp = p.block_size / kChunk;
+    [[maybe_unused]] int f4_lp = 0, f4_in = 0, f4_next = 0;
+    if (F4 && (warp == 5 || warp == C::THREADS / 32 - 1)) {
+        f4_lp = (c_begin + lane) / f4_cpp;
+        f4_in = c_begin + lane - f4_lp * f4_cpp;
+    }
+    [[maybe_unused]] const int f4_step_lp = CPT / f4_cpp, f4_step_in = CPT % f4_cpp;
+    [[maybe_unused]] auto issue_f4 = [&](uint64_t policy) {
+        constexpr int REC = fp4::rec_bytes(D);
+        const int i = f4_next++, s = i % (NSG > 0 ? NSG : 1);
+        const int nc = min(CPT, n_my - i * CPT);
+        uint64_t *bar = (f4_tensor == 0 ? kst_full : vst_full) + s;
+        if (lane == 0) mbar_arrive_expect_tx(bar, nc * REC);
+        // the chunks of a page are contiguous: one copy for a tile inside one page, else one per chunk
+        const bool whole = __shfl_sync(0xffffffffu, f4_in, 0) + nc <= f4_cpp;
+        if (lane < (whole ? 1 : nc)) {
+            int page = staged ? page_tab[f4_lp - lp_first] : bt[f4_lp];
+            if (page < 0 || (int64_t)page >= p.num_pages) {
+                flags[1] = 1;  // the rows are zeroed; page 0 is read in its place
+                set_status(p.status, PA_DEV_BAD_PAGE);
+                page = 0;
+            }
+            const int64_t rec = ((int64_t)page * p.num_kv_heads + kvh) * f4_cpp + f4_in;
+            fp4::bulk_load(smem + C::OFF_STG + (f4_tensor * NSG + s) * C::STG_BYTES + lane * REC,
+                           (f4_tensor == 0 ? p.k_cache : p.v_cache) + rec * REC, (whole ? nc : 1) * REC, bar, policy);
+        }
+        f4_lp += f4_step_lp;
+        f4_in += f4_step_in;
+        if (f4_in >= f4_cpp) {
+            f4_in -= f4_cpp;
+            ++f4_lp;
+        }
+        __syncwarp();
+    };
     // tiles that end before the new rows (early_kv reads only those before the wait)
     auto before_new_rows = [&](int i, int cpt) {
         return (c_begin + i * cpt + min(cpt, n_my - i * cpt)) * kChunk <= L - p.q_len;
     };
     if (p.early_kv) {
         __syncthreads();  // barrier initialisation and the page table are visible to the producer warp
-        if (warp == 5) {
+        if constexpr (F4) {
+            if (warp == 5 || warp == C::THREADS / 32 - 1)
+                while (f4_next < min(NSG, n_tiles) && before_new_rows(f4_next, CPT)) issue_f4(l2_policy_evict_first());
+        } else if (warp == 5) {
             // first use of each slot: tiles that end before the new rows
             const uint64_t policy = l2_policy_evict_first();
             constexpr int FK = F8 ? NSG : NK, FV = F8 ? NSG : NV;  // slots the copies land in
@@ -615,7 +642,29 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         tc::fence_after();
     }
 
-    if (warp == 5) {
+    if (F4 && (warp == 5 || warp == C::THREADS / 32 - 1)) {
+        // ---------------- fp4 producers: records of K (warp 5) and V (the last warp) ----------------
+        const uint64_t policy = l2_policy_evict_first();
+        constexpr int NS = NSG > 0 ? NSG : 1;
+        uint64_t *full = f4_tensor == 0 ? kst_full : vst_full, *empty = f4_tensor == 0 ? kst_empty : vst_empty;
+        while (f4_next < n_tiles) {
+            const int i = f4_next;
+            if (i >= NS && !__all_sync(0xffffffffu, mbar_wait(&empty[i % NS], ((i / NS) - 1) & 1, &flags[0]))) {
+                if (lane == 0) {
+                    flags[0] = 1;
+                    set_status(p.status, PA_DEV_TIMEOUT);
+                }
+                break;
+            }
+            issue_f4(policy);
+        }
+        if (lane == 0 && flags[0]) {
+            // let the copies in flight land before the CTA ends
+            for (int i = max(0, f4_next - NS); i < f4_next; ++i)
+                for (uint32_t n = 0; n < kWaitPollLimit && !mbar_try_wait(&full[i % NS], (i / NS) & 1); ++n) {
+                }
+        }
+    } else if (warp == 5) {
         // ---------------- producer: TMA copies of K and V, 4 chunks per tile ----------------
         // Two rings refilled independently: lane 0 probes the next slot of
         // each without blocking and the warp issues the tile; within a ring
@@ -693,10 +742,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 if (step >= NSB) {
                     const int i = step - NSB, j = i % NSB;
                     const int nvt = VPK == 1 ? 1 : min(VPK, n_vtiles - i * VPK);
-                    ok = wait(&p_full[j], (i / NSB) & 1);
+                    ok = wait(&p_full[i % C::NP], (i / C::NP) & 1);
                     for (int h2 = 0; h2 < nvt && ok; ++h2) {
                         const int vt = i * VPK + h2;
-                        ok = wait(&v_full[vt % NV], (vt / NV) & 1);
+                        if (!F8) ok = wait(&v_full[vt % NV], (vt / NV) & 1);
                         if (!ok) break;
                         tc::fence_after();
                         if (leader) {
@@ -758,58 +807,108 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     } else if (warp >= 6) {
         if constexpr (F4) {
             // ---------------- fp4: widen staged records into the K (warps 6-9) / V (10-13) ring ----------------
-            // A warp takes one record of the tile.
+            // A warp takes one record of the tile.  Its bytes come to registers a
+            // tile ahead: the loads' latency, and the wait for the next record,
+            // pass while the current one is widened.
+            static_assert(C::CW == C::CPT, "a widening warp per record of a tile");
+            constexpr int REC = fp4::rec_bytes(D), NBL = D / 16;
             const int tensor = (warp - 6) / C::CW, rc = (warp - 6) % C::CW;
-            static_assert(!F4 || C::CW == C::CPT, "a widening warp per record of a tile");
             const int NR = tensor == 0 ? NK : NV;
-            uint64_t *ring_full = tensor == 0 ? k_full : v_full;
+            uint64_t *ring_full = tensor == 0 ? k_full : p_full;
             uint64_t *ring_empty = tensor == 0 ? k_empty : v_empty;
             uint64_t *stg_full = tensor == 0 ? kst_full : vst_full;
             uint64_t *stg_empty = tensor == 0 ? kst_empty : vst_empty;
-            uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V);
-            uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES;
-            constexpr int REC = fp4::rec_bytes(D), NBL = D / 16;
+            uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V) + rc * kChunk * 128;
+            uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES + rc * REC;
             const int t_end = min(k_last + 1, (c_begin + n_my) * kChunk);
             // every row sees the tokens [w_last, f_last]
             const int f_last = L - p.q_len + row0 / G, w_last = p.window > 0 ? k_last - p.window + 1 : 0;
-            for (int i = 0; i < n_tiles; ++i) {
-                // the staged records have landed, and the ring slot's previous tile has been consumed
-                bool ok = __all_sync(0xffffffffu, mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]));
-                if (ok && i >= NR)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]));
-                if (!ok) {
-                    flags[0] = 1;
-                    break;
-                }
-                const uint8_t *rec = stg + (i % NSG) * C::STG_BYTES + rc * REC;
-                uint8_t *ring_rows = ring + (i % NR) * C::TILE_BYTES + rc * kChunk * 128;
+            // K: lane = token r of a half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so that
+            // its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups
+            // V: lane = token pair c, dims 2 r, 2 r + 1 of every block
+            const int c = lane & 3, r = tensor == 0 ? (lane >> 3) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+            struct Record {
+                uint32_t code[4][NBL / 4];  // K: [2 j + half]; V: [u], tokens 8 (u / 2) + 2 c + u % 2
+                uint32_t sc[NBL / 4][4];    // K: [q] of 8-byte halves; V: [w]
+            };
+            auto load = [&](int i, Record &x) {  // the staged record of tile i, once it has landed
+                if (!mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0])) return false;
+                uint8_t *rec = stg + (i % NSG) * C::STG_BYTES;
                 const int t0 = (c_begin + i * CPT + rc) * kChunk;
+                // NaN scales of V's tokens hidden from some rows: noted, and 0 in the staged record
+                if (tensor == 1 && (t0 + kChunk - 1 > f_last || t0 < w_last)) {
+                    constexpr int WB = D / 32;  // scale bytes of a lane
+                    uint8_t *sb = rec + 8 * D + lane * WB;
+                    uint32_t found = 0;
+#pragma unroll
+                    for (int o = 0; o < WB; o += 4)
+                        found |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(sb + o) & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    if (found != 0) {
+#pragma unroll 1
+                        for (int o = 0; o < WB; ++o) {
+                            const int at = lane * WB + o, blk = (at >> 6) * 4 + ((at >> 2) & 3);
+                            const int t = t0 + ((at >> 3) & 6) + (at & 1) + ((at & 2) << 2);
+                            if ((sb[o] & 0x7f) != 0x7f || t > k_last || t < k_first || (t <= f_last && t >= w_last))
+                                continue;
+                            const int bit = t > f_last ? t - f_last - 1 : 128 + t - k_first;
+                            atomicOr(&nan_bits[blk * 8 + (bit >> 5)], 1u << (bit & 31));
+                            flags[2] = 1;
+                            sb[o] = 0;
+                        }
+                        tc::fence_async_smem();  // before the slot's next copy
+                    }
+                    __syncwarp();
+                }
                 if (tensor == 0) {
-                    // lane: token r of a half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so
-                    // that its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups (rows
-                    // past the tile's end may hold anything: their scores are masked)
-                    const int c = lane & 3, r = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+#pragma unroll
+                    for (int g = 0; g < NBL / 4; ++g) {  // 2 j + half
+                        const uint4 w = *reinterpret_cast<const uint4 *>(rec + g * 512 + (4 * r + c) * 16);
+                        x.code[0][g] = w.x, x.code[1][g] = w.y, x.code[2][g] = w.z, x.code[3][g] = w.w;
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < NBL / 8; ++j) {
+                            const uint2 w =
+                                *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * half + r) * NBL + 8 * j);
+                            x.sc[2 * j + half][0] = w.x, x.sc[2 * j + half][1] = w.y;
+                        }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint8_t *src = rec + u * 2 * D + lane * NBL;
+                        if constexpr (NBL == 16) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                            x.code[u][0] = w.x, x.code[u][1] = w.y, x.code[u][2] = w.z, x.code[u][3] = w.w;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                            x.code[u][0] = w.x, x.code[u][1] = w.y;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < NBL / 4; ++w) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
+                        x.sc[w][0] = v.x, x.sc[w][1] = v.y, x.sc[w][2] = v.z, x.sc[w][3] = v.w;
+                    }
+                }
+                return true;
+            };
+            auto widen = [&](int i, const Record &x) {  // into the ring slot
+                uint8_t *ring_rows = ring + (i % NR) * C::TILE_BYTES;
+                const int t0 = (c_begin + i * CPT + rc) * kChunk;
+                if (tensor == 0) {  // (rows past the tile's end may hold anything: their scores are masked)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint8_t *dst = ring_rows + (8 * half + r) * 128;
-                        uint32_t sc[NBL / 4];
-#pragma unroll
-                        for (int q = 0; q < NBL / 4; q += 2) {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * half + r) * NBL + 4 * q);
-                            sc[q] = w.x;
-                            sc[q + 1] = w.y;
-                        }
 #pragma unroll
                         for (int j = 0; j < NBL / 8; ++j) {
-                            const uint4 kw = *reinterpret_cast<const uint4 *>(rec + (2 * j + half) * 512 + (4 * r + c) * 16);
-                            const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1
                                 const int g = 4 * j + q;
                                 uint32_t a[4], s2[2];
-                                fp4::e2m1x8_f16(wd[q], a);
-                                fp4::e4m3x4_f16(sc[g / 2], s2[0], s2[1]);
-                                const uint32_t sv2 = s2[g & 1];
+                                fp4::e2m1x8_f16(x.code[q][2 * j + half], a);
+                                fp4::e4m3x4_f16(x.sc[2 * j + half][q / 2], s2[0], s2[1]);
+                                const uint32_t sv2 = s2[q & 1];
                                 const uint4 o = make_uint4(fp4::hmul2_lo(a[0], sv2), fp4::hmul2_lo(a[1], sv2),
                                                            fp4::hmul2_hi(a[2], sv2), fp4::hmul2_hi(a[3], sv2));
                                 const int ch = 4 * g + c;
@@ -818,42 +917,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                         }
                     }
                 } else {
-                    // NaN scales of tokens hidden from some rows: noted, and 0 in the staged record
-                    if (t0 + kChunk - 1 > f_last || t0 < w_last) {
-                        constexpr int WB = D / 32;  // scale bytes of a lane
-                        uint8_t *sb = stg + (i % NSG) * C::STG_BYTES + rc * REC + 8 * D + lane * WB;
-                        uint32_t found = 0;
-#pragma unroll
-                        for (int o = 0; o < WB; o += 4)
-                            found |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(sb + o) & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        if (found != 0) {
-#pragma unroll 1
-                            for (int o = 0; o < WB; ++o) {
-                                const int at = lane * WB + o, blk = (at >> 6) * 4 + ((at >> 2) & 3);
-                                const int t = t0 + ((at >> 3) & 6) + (at & 1) + ((at & 2) << 2);
-                                if ((sb[o] & 0x7f) != 0x7f || t > k_last || t < k_first || (t <= f_last && t >= w_last))
-                                    continue;
-                                const int bit = t > f_last ? t - f_last - 1 : 128 + t - k_first;
-                                atomicOr(&nan_bits[blk * 8 + (bit >> 5)], 1u << (bit & 31));
-                                flags[2] = 1;
-                                sb[o] = 0;
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    const int c = lane & 3, r = lane >> 2;
-                    uint32_t wd[4][NBL / 4];  // the lane's tokens u = 2 half + par: 8 half + 2 c + par
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint8_t *src = rec + u * 2 * D + lane * NBL;
-                        if constexpr (NBL == 16) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(src);
-                            wd[u][0] = w.x, wd[u][1] = w.y, wd[u][2] = w.z, wd[u][3] = w.w;
-                        } else {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                            wd[u][0] = w.x, wd[u][1] = w.y;
-                        }
-                    }
                     // rows outside the block's visible keys may hold anything: their scales become 0
                     uint32_t vm[2];
 #pragma unroll
@@ -867,41 +930,60 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
 #pragma unroll
                     for (int w = 0; w < NBL / 4; ++w) {
                         uint32_t s2[2][4];  // [half]: scale pairs of its two tokens, blocks 4 w .. 4 w + 3
-                        const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
-                        const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            fp4::e4m3x4_f16(sb[q], s2[0][q], s2[1][q]);
+                            fp4::e4m3x4_f16(x.sc[w][q], s2[0][q], s2[1][q]);
                             s2[0][q] &= vm[0];
                             s2[1][q] &= vm[1];
                         }
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t a[4];
-                            fp4::e2m1x8_f16(wd[2 * half][w], a);
+                            fp4::e2m1x8_f16(x.code[2 * half][w], a);
                             *reinterpret_cast<uint4 *>(dst + half * 1024 + w * (TT * 128) + p0) =
                                 make_uint4(fp4::hmul2_lo(a[0], s2[half][0]), fp4::hmul2_lo(a[1], s2[half][1]),
                                            fp4::hmul2_lo(a[2], s2[half][2]), fp4::hmul2_lo(a[3], s2[half][3]));
-                            fp4::e2m1x8_f16(wd[2 * half + 1][w], a);
+                            fp4::e2m1x8_f16(x.code[2 * half + 1][w], a);
                             *reinterpret_cast<uint4 *>(dst + half * 1024 + 128 + w * (TT * 128) + p1) =
                                 make_uint4(fp4::hmul2_hi(a[0], s2[half][0]), fp4::hmul2_hi(a[1], s2[half][1]),
                                            fp4::hmul2_hi(a[2], s2[half][2]), fp4::hmul2_hi(a[3], s2[half][3]));
                         }
                     }
                 }
+            };
+            // tile i from x, with tile i + 1 fetched to y; false at the end or when a wait was abandoned
+            auto step = [&](int i, const Record &x, Record &y) {
+                bool ok = true;
+                if (i + 1 < n_tiles) {
+                    ok = load(i + 1, y);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&stg_empty[(i + 1) % NSG]);
+                }
+                // the ring slot's previous tile has been consumed
+                if (ok && i >= NR) ok = mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    flags[0] = 1;
+                    return false;
+                }
+                widen(i, x);
                 tc::fence_async_smem();  // the tensor core reads the widened tile
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ring_full[i % NR]);
-                    mbar_arrive(&stg_empty[i % NSG]);
-                }
-            }
+                if (lane == 0) mbar_arrive(&ring_full[i % NR]);
+                return i + 1 < n_tiles;
+            };
+            Record x, y;
+            bool ok = load(0, x);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) flags[0] = 1;
+            if (ok && lane == 0) mbar_arrive(&stg_empty[0]);
+            for (int i = 0; ok && step(i, x, y); i += 2)
+                if (!step(i + 1, y, x)) break;
         } else if constexpr (F8) {
             // ---------------- fp8: widen staged e4m3 tiles into the K (warps 6, 7) / V (8, 9) ring ----------------
             const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
             constexpr int NR0 = NK, NR1 = NV;
             const int NR = tensor == 0 ? NR0 : NR1;
-            uint64_t *ring_full = tensor == 0 ? k_full : v_full;
+            uint64_t *ring_full = tensor == 0 ? k_full : p_full;
             uint64_t *ring_empty = tensor == 0 ? k_empty : v_empty;
             uint64_t *stg_full = tensor == 0 ? kst_full : vst_full;
             uint64_t *stg_empty = tensor == 0 ? kst_empty : vst_empty;
@@ -974,9 +1056,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         [[maybe_unused]] float o_far[FAR ? D : 1];  // (indexed at run time: local memory)
         [[maybe_unused]] float m_far = -INFINITY;   // the reference max that o_far stands for
         bool ok = true;
-        // O += P_k V_k of tile k is waited for in order per barrier (tile k +
-        // NSB, where it is long finished), so no wait ever tests a phase parity
-        // two phases behind the barrier.
+        // O += P_k V_k of tile k.  S_i being there says that tile i - NSB's
+        // product is done (the tensor core ran it first), so a wait for tile
+        // i - 1 never tests a phase parity two phases behind the barrier.
         auto wait_pv = [&](int k) {
             return __all_sync(0xffffffffu, mbar_wait(&o_done[k % NSB], (k / NSB) & 1, &flags[0]));
         };
@@ -1015,7 +1097,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             // for 128 keys would not fit the registers, and the two-pass form
             // makes the fp8 variants spill).
             if (idle_warp) {
-                mbar_arrive(&p_full[j]);
+                if (lane == 0) mbar_arrive(&p_full[i % C::NP]);
                 continue;
             }
             if constexpr (VPK == 1) {
@@ -1029,11 +1111,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
 #pragma unroll
                     for (int c = 0; c < TT; ++c) sv[c] = __uint_as_float(r[c / 16][c % 16]);
                 }
-                if (i >= NSB && !wait_pv(i - NSB)) {
-                    ok = false;
-                    break;
-                }
-
                 const int t0 = (c_begin + i * CPT) * kChunk;
                 float mx = -INFINITY;
                 // the exponent is 2^(sv * mul - m): raw scores with mul = scale when
@@ -1166,10 +1243,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     load_half(h2);
                     mx = fmaxf(mx, half_max());
                 }
-                if (i >= NSB && !wait_pv(i - NSB)) {
-                    ok = false;
-                    break;
-                }
                 // lazy rescale: only when the max grows by more than 2^kLazy, and
                 // then only after the previous tile's P.V product has finished
                 const bool raise = mx > m_ref + kLazy;
@@ -1242,7 +1315,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 tc::wait_st();
                 tc::fence_before();
             }
-            mbar_arrive(&p_full[j]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[i % C::NP]);
         }
         // Epilogue: wait for the last P.V MMA, normalise and write this row.
         if (ok && !wait_pv(n_tiles - 1)) ok = false;
