@@ -82,6 +82,13 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &h
         : "r"(w));
 }
 
+// The two scale codes in the low half.
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
 __device__ __forceinline__ float e4m3_f32(uint32_t code) {
     uint32_t lo, hi;
     e4m3x4_f16(code, lo, hi);

@@ -269,7 +269,7 @@ struct VerifyTcCfg {
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
     // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NSB], p_full[NP], o_done[NSB], mma_fin,
     // then (fp8, fp4) kst_full[NSG], kst_empty[NSG], vst_full[NSG], vst_empty[NSG]
-    static constexpr int CW = F4 ? 4 : 2;              // fp8, fp4: widening warps per tensor
+    static constexpr int CW = F4 ? 8 : 2;              // fp8, fp4: widening warps per tensor
     static constexpr int NP = F8 ? NV : NSB;           // P barriers (fp8, fp4: the V slot's too)
     static constexpr int OFF_TMEM = OFF_BAR + (2 * NK + 2 * NV + 2 * NSB + NP + 1 + 4 * NSG) * 8;
     static constexpr int OFF_FLAGS = OFF_TMEM + 16;
@@ -288,7 +288,12 @@ struct VerifyTcCfg {
     static constexpr int SBUF(int j) { return S_COL + j * TK; }
     static constexpr int SROW = D * 4 + 16;            // epilogue: output rows staged in the K/V rings
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
-    static constexpr int THREADS = (F4 ? 7 + 2 * CW : F8 ? 6 + 2 * CW : 6) * 32;
+    static constexpr int W0 = F4 ? 8 : 6;              // first widening warp
+    static constexpr int THREADS = (F8 ? W0 + 2 * CW : 6) * 32;
+    // fp4: registers of the softmax warpgroup and of the others (setmaxnreg).  Their sum draws on what the block
+    // was launched with, which the launch checks.
+    static constexpr int REGS_SM = 152, REGS_OTHER = 64;
+    static constexpr int REGS_LAUNCH = (128 * REGS_SM + (THREADS - 128) * REGS_OTHER + THREADS - 1) / THREADS;
     static_assert(D == 256 || D == 128, "head_dim 256 or 128");
     static_assert(Q_COL + Q_TCOLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(TK == 64 || (TK == 128 && !F8), "128-key score tiles: bf16 cache only");
@@ -496,12 +501,12 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         __syncwarp();
     };
     static_assert(CPK * (F8 ? D / 128 : C::DB) <= 32, "a lane per box of a tile");
-    // fp4: warp 5 copies K, the last warp V (a copy's issue takes one lane 0.15
+    // fp4: warp 5 copies K, warp 6 V (a copy's issue takes one lane 0.15
     // us: both tensors' would fill one warp's time).  A lane keeps the page and
     // the place in it of its chunk of the next tile.
     [[maybe_unused]] const int f4_tensor = warp == 5 ? 0 : 1, f4_cpp = p.block_size / kChunk;
     [[maybe_unused]] int f4_lp = 0, f4_in = 0, f4_next = 0;
-    if (F4 && (warp == 5 || warp == C::THREADS / 32 - 1)) {
+    if (F4 && (warp == 5 || warp == 6)) {
         f4_lp = (c_begin + lane) / f4_cpp;
         f4_in = c_begin + lane - f4_lp * f4_cpp;
     }
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     if (p.early_kv) {
         __syncthreads();  // barrier initialisation and the page table are visible to the producer warp
         if constexpr (F4) {
-            if (warp == 5 || warp == C::THREADS / 32 - 1)
+            if (warp == 5 || warp == 6)
                 while (f4_next < min(NSG, n_tiles) && before_new_rows(f4_next, CPT)) issue_f4(l2_policy_evict_first());
         } else if (warp == 5) {
             // first use of each slot: tiles that end before the new rows
@@ -554,15 +559,16 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
 
     // Q rows: each softmax thread loads its row (D / 8 16-byte words, one
     // round of loads) right after the dependency wait, so the loads are in
-    // flight while tensor memory is allocated.
+    // flight while tensor memory is allocated (fp4: once it has its registers).
     constexpr int NQ = D / 8;
     uint4 qv[NQ];
-    if (warp < 4) {
+    auto load_q = [&]() {
         const bool qlive = (int)threadIdx.x < R;
 #pragma unroll
         for (int v = 0; v < NQ; ++v)
             qv[v] = qlive ? *reinterpret_cast<const uint4 *>(qrow + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    };
+    if (!F4 && warp < 4) load_q();
     if (warp == 4) {
         tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
         tc::tmem_relinquish();
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     // enters scaled by q_pre, the power of two that brings its largest element
     // into [2^14, 2^15) (f16_prescale).
     float q_pre = 1.f;
-    if (warp < 4) {
+    auto store_q = [&]() {
         if constexpr (F8) {  // the products run in f16: Q too
             uint32_t amax = 0;
 #pragma unroll
@@ -637,13 +643,22 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         }
         tc::fence_before();
         asm volatile("bar.arrive 1, 160;" ::: "memory");
-    } else if (warp == 4) {
+    };
+    auto wait_q = [&]() {  // (warp 4)
         asm volatile("bar.sync 1, 160;" ::: "memory");
         tc::fence_after();
+    };
+    if (!F4) {
+        if (warp < 4)
+            store_q();
+        else if (warp == 4)
+            wait_q();
     }
 
-    if (F4 && (warp == 5 || warp == C::THREADS / 32 - 1)) {
-        // ---------------- fp4 producers: records of K (warp 5) and V (the last warp) ----------------
+    if (warp >= 4) {
+    if constexpr (F4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if (F4 && (warp == 5 || warp == 6)) {
+        // ---------------- fp4 producers: records of K (warp 5) and V (warp 6) ----------------
         const uint64_t policy = l2_policy_evict_first();
         constexpr int NS = NSG > 0 ? NSG : 1;
         uint64_t *full = f4_tensor == 0 ? kst_full : vst_full, *empty = f4_tensor == 0 ? kst_empty : vst_empty;
@@ -717,6 +732,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // branch of one lane, the 16 products of S_i took 720 clocks and more,
         // not the tensor core's 517.
         {
+            if (F4) wait_q();
             constexpr uint32_t kIdQK = tc::idesc_bf16(128, TK, 0, F8);
             constexpr uint32_t kIdPV = tc::idesc_bf16(128, D, 1, F8);
             const bool leader = tc::elect_one();
@@ -804,180 +820,124 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             }
             __syncwarp();
         }
-    } else if (warp >= 6) {
+    } else if (warp >= C::W0) {
         if constexpr (F4) {
-            // ---------------- fp4: widen staged records into the K (warps 6-9) / V (10-13) ring ----------------
-            // A warp takes one record of the tile.  Its bytes come to registers a
-            // tile ahead: the loads' latency, and the wait for the next record,
-            // pass while the current one is widened.
-            static_assert(C::CW == C::CPT, "a widening warp per record of a tile");
+            // ---------------- fp4: widen staged records into the K (warps 8-15) / V (16-23) ring ----------------
+            // A warp takes half a record of the tile: 8 tokens.
+            static_assert(C::CW == 2 * C::CPT, "two widening warps per record of a tile");
             constexpr int REC = fp4::rec_bytes(D), NBL = D / 16;
-            const int tensor = (warp - 6) / C::CW, rc = (warp - 6) % C::CW;
+            const int tensor = (warp - C::W0) / C::CW, rc = (warp - C::W0) % C::CW / 2, half = warp & 1;
             const int NR = tensor == 0 ? NK : NV;
             uint64_t *ring_full = tensor == 0 ? k_full : p_full;
             uint64_t *ring_empty = tensor == 0 ? k_empty : v_empty;
             uint64_t *stg_full = tensor == 0 ? kst_full : vst_full;
             uint64_t *stg_empty = tensor == 0 ? kst_empty : vst_empty;
-            uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V) + rc * kChunk * 128;
+            uint8_t *ring = smem + (tensor == 0 ? 0 : C::OFF_V) + (rc * kChunk + 8 * half) * 128;
             uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES + rc * REC;
             const int t_end = min(k_last + 1, (c_begin + n_my) * kChunk);
             // every row sees the tokens [w_last, f_last]
             const int f_last = L - p.q_len + row0 / G, w_last = p.window > 0 ? k_last - p.window + 1 : 0;
-            // K: lane = token r of a half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so that
+            // K: lane = token r of the half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so that
             // its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups
             // V: lane = token pair c, dims 2 r, 2 r + 1 of every block
             const int c = lane & 3, r = tensor == 0 ? (lane >> 3) ^ (lane & 4 ? 5 : 0) : lane >> 2;
-            struct Record {
-                uint32_t code[4][NBL / 4];  // K: [2 j + half]; V: [u], tokens 8 (u / 2) + 2 c + u % 2
-                uint32_t sc[NBL / 4][4];    // K: [q] of 8-byte halves; V: [w]
-            };
-            auto load = [&](int i, Record &x) {  // the staged record of tile i, once it has landed
-                if (!mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0])) return false;
-                uint8_t *rec = stg + (i % NSG) * C::STG_BYTES;
-                const int t0 = (c_begin + i * CPT + rc) * kChunk;
-                // NaN scales of V's tokens hidden from some rows: noted, and 0 in the staged record
-                if (tensor == 1 && (t0 + kChunk - 1 > f_last || t0 < w_last)) {
-                    constexpr int WB = D / 32;  // scale bytes of a lane
-                    uint8_t *sb = rec + 8 * D + lane * WB;
-                    uint32_t found = 0;
-#pragma unroll
-                    for (int o = 0; o < WB; o += 4)
-                        found |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(sb + o) & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    if (found != 0) {
-#pragma unroll 1
-                        for (int o = 0; o < WB; ++o) {
-                            const int at = lane * WB + o, blk = (at >> 6) * 4 + ((at >> 2) & 3);
-                            const int t = t0 + ((at >> 3) & 6) + (at & 1) + ((at & 2) << 2);
-                            if ((sb[o] & 0x7f) != 0x7f || t > k_last || t < k_first || (t <= f_last && t >= w_last))
-                                continue;
-                            const int bit = t > f_last ? t - f_last - 1 : 128 + t - k_first;
-                            atomicOr(&nan_bits[blk * 8 + (bit >> 5)], 1u << (bit & 31));
-                            flags[2] = 1;
-                            sb[o] = 0;
-                        }
-                        tc::fence_async_smem();  // before the slot's next copy
-                    }
-                    __syncwarp();
+            for (int i = 0; i < n_tiles; ++i) {
+                // the staged records have landed, and the ring slot's previous tile has been consumed
+                bool ok = mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]);
+                if (ok && i >= NR) ok = mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    flags[0] = 1;
+                    break;
                 }
-                if (tensor == 0) {
-#pragma unroll
-                    for (int g = 0; g < NBL / 4; ++g) {  // 2 j + half
-                        const uint4 w = *reinterpret_cast<const uint4 *>(rec + g * 512 + (4 * r + c) * 16);
-                        x.code[0][g] = w.x, x.code[1][g] = w.y, x.code[2][g] = w.z, x.code[3][g] = w.w;
-                    }
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int j = 0; j < NBL / 8; ++j) {
-                            const uint2 w =
-                                *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * half + r) * NBL + 8 * j);
-                            x.sc[2 * j + half][0] = w.x, x.sc[2 * j + half][1] = w.y;
-                        }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint8_t *src = rec + u * 2 * D + lane * NBL;
-                        if constexpr (NBL == 16) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(src);
-                            x.code[u][0] = w.x, x.code[u][1] = w.y, x.code[u][2] = w.z, x.code[u][3] = w.w;
-                        } else {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                            x.code[u][0] = w.x, x.code[u][1] = w.y;
-                        }
-                    }
-#pragma unroll
-                    for (int w = 0; w < NBL / 4; ++w) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
-                        x.sc[w][0] = v.x, x.sc[w][1] = v.y, x.sc[w][2] = v.z, x.sc[w][3] = v.w;
-                    }
-                }
-                return true;
-            };
-            auto widen = [&](int i, const Record &x) {  // into the ring slot
-                uint8_t *ring_rows = ring + (i % NR) * C::TILE_BYTES;
-                const int t0 = (c_begin + i * CPT + rc) * kChunk;
+                uint8_t *rec = stg + (i % NSG) * C::STG_BYTES, *ring_rows = ring + (i % NR) * C::TILE_BYTES;
+                const int t0 = (c_begin + i * CPT + rc) * kChunk + 8 * half;
                 if (tensor == 0) {  // (rows past the tile's end may hold anything: their scores are masked)
+                    uint8_t *dst = ring_rows + r * 128;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint8_t *dst = ring_rows + (8 * half + r) * 128;
+                    for (int j = 0; j < NBL / 8; ++j) {
+                        const uint4 kw = *reinterpret_cast<const uint4 *>(rec + (2 * j + half) * 512 + (4 * r + c) * 16);
+                        const uint2 sc = *reinterpret_cast<const uint2 *>(rec + 8 * D + (8 * half + r) * NBL + 8 * j);
+                        const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-                        for (int j = 0; j < NBL / 8; ++j) {
+                        for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1
+                            uint32_t a[4], s2[2];
+                            fp4::e2m1x8_f16(wd[q], a);
+                            fp4::e4m3x4_f16(q < 2 ? sc.x : sc.y, s2[0], s2[1]);
+                            const uint32_t sv2 = s2[q & 1];
+                            const uint4 o = make_uint4(fp4::hmul2_lo(a[0], sv2), fp4::hmul2_lo(a[1], sv2),
+                                                       fp4::hmul2_hi(a[2], sv2), fp4::hmul2_hi(a[3], sv2));
+                            const int ch = 4 * (4 * j + q) + c;
+                            *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (TT * 128) + (((ch & 7) ^ r) << 4)) = o;
+                        }
+                    }
+                } else {
+                    // NaN scales of tokens hidden from some rows: noted, and 0 in the staged record
+                    if (t0 + 7 > f_last || t0 < w_last) {
+                        constexpr int WB = D / 32;  // scale bytes of a lane, both halves'
+                        uint8_t *sb = rec + 8 * D + lane * WB;
+                        uint32_t found = 0;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {  // blocks 8 j + 2 q, + 1
-                                const int g = 4 * j + q;
-                                uint32_t a[4], s2[2];
-                                fp4::e2m1x8_f16(x.code[q][2 * j + half], a);
-                                fp4::e4m3x4_f16(x.sc[2 * j + half][q / 2], s2[0], s2[1]);
-                                const uint32_t sv2 = s2[q & 1];
-                                const uint4 o = make_uint4(fp4::hmul2_lo(a[0], sv2), fp4::hmul2_lo(a[1], sv2),
-                                                           fp4::hmul2_hi(a[2], sv2), fp4::hmul2_hi(a[3], sv2));
-                                const int ch = 4 * g + c;
-                                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (TT * 128) + (((ch & 7) ^ r) << 4)) = o;
+                        for (int o = 0; o < WB; o += 4)
+                            found |= __vcmpeq4(*reinterpret_cast<const uint32_t *>(sb + o) & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        if ((found & (half ? 0xffff0000u : 0x0000ffffu)) != 0) {
+#pragma unroll 1
+                            for (int o = 0; o < WB; ++o) {
+                                const int at = lane * WB + o, blk = (at >> 6) * 4 + ((at >> 2) & 3);
+                                const int t = t0 + ((at >> 3) & 6) + (at & 1);
+                                if ((at >> 1 & 1) != half || (sb[o] & 0x7f) != 0x7f || t > k_last || t < k_first ||
+                                    (t <= f_last && t >= w_last))
+                                    continue;
+                                const int bit = t > f_last ? t - f_last - 1 : 128 + t - k_first;
+                                atomicOr(&nan_bits[blk * 8 + (bit >> 5)], 1u << (bit & 31));
+                                flags[2] = 1;
+                                sb[o] = 0;
                             }
                         }
+                        __syncwarp();
                     }
-                } else {
-                    // rows outside the block's visible keys may hold anything: their scales become 0
-                    uint32_t vm[2];
+                    uint32_t wd[2][NBL / 4];  // codes of the lane's tokens 2 c, 2 c + 1
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int tg = t0 + 8 * half + 2 * c;
-                        vm[half] = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
-                                   (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint8_t *src = rec + (2 * half + u) * 2 * D + lane * NBL;
+                        if constexpr (NBL == 16) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                            wd[u][0] = w.x, wd[u][1] = w.y, wd[u][2] = w.z, wd[u][3] = w.w;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                            wd[u][0] = w.x, wd[u][1] = w.y;
+                        }
                     }
+                    // rows outside the block's visible keys may hold anything: their scales become 0
+                    const int tg = t0 + 2 * c;
+                    const uint32_t vm = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
+                                        (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
                     uint8_t *dst = ring_rows + 2 * c * 128;
                     const int p0 = (r ^ (2 * c)) << 4, p1 = (r ^ (2 * c + 1)) << 4;
 #pragma unroll
                     for (int w = 0; w < NBL / 4; ++w) {
-                        uint32_t s2[2][4];  // [half]: scale pairs of its two tokens, blocks 4 w .. 4 w + 3
+                        const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
+                        const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
+                        uint32_t s2[4];  // scale pairs of the two tokens, blocks 4 w .. 4 w + 3
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            fp4::e4m3x4_f16(x.sc[w][q], s2[0][q], s2[1][q]);
-                            s2[0][q] &= vm[0];
-                            s2[1][q] &= vm[1];
-                        }
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t a[4];
-                            fp4::e2m1x8_f16(x.code[2 * half][w], a);
-                            *reinterpret_cast<uint4 *>(dst + half * 1024 + w * (TT * 128) + p0) =
-                                make_uint4(fp4::hmul2_lo(a[0], s2[half][0]), fp4::hmul2_lo(a[1], s2[half][1]),
-                                           fp4::hmul2_lo(a[2], s2[half][2]), fp4::hmul2_lo(a[3], s2[half][3]));
-                            fp4::e2m1x8_f16(x.code[2 * half + 1][w], a);
-                            *reinterpret_cast<uint4 *>(dst + half * 1024 + 128 + w * (TT * 128) + p1) =
-                                make_uint4(fp4::hmul2_hi(a[0], s2[half][0]), fp4::hmul2_hi(a[1], s2[half][1]),
-                                           fp4::hmul2_hi(a[2], s2[half][2]), fp4::hmul2_hi(a[3], s2[half][3]));
-                        }
+                        for (int q = 0; q < 4; ++q) s2[q] = fp4::e4m3x2_f16(half ? sb[q] >> 16 : sb[q]) & vm;
+                        uint32_t a[4];
+                        fp4::e2m1x8_f16(wd[0][w], a);
+                        *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + p0) =
+                            make_uint4(fp4::hmul2_lo(a[0], s2[0]), fp4::hmul2_lo(a[1], s2[1]),
+                                       fp4::hmul2_lo(a[2], s2[2]), fp4::hmul2_lo(a[3], s2[3]));
+                        fp4::e2m1x8_f16(wd[1][w], a);
+                        *reinterpret_cast<uint4 *>(dst + 128 + w * (TT * 128) + p1) =
+                            make_uint4(fp4::hmul2_hi(a[0], s2[0]), fp4::hmul2_hi(a[1], s2[1]),
+                                       fp4::hmul2_hi(a[2], s2[2]), fp4::hmul2_hi(a[3], s2[3]));
                     }
                 }
-            };
-            // tile i from x, with tile i + 1 fetched to y; false at the end or when a wait was abandoned
-            auto step = [&](int i, const Record &x, Record &y) {
-                bool ok = true;
-                if (i + 1 < n_tiles) {
-                    ok = load(i + 1, y);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&stg_empty[(i + 1) % NSG]);
-                }
-                // the ring slot's previous tile has been consumed
-                if (ok && i >= NR) ok = mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    flags[0] = 1;
-                    return false;
-                }
-                widen(i, x);
-                tc::fence_async_smem();  // the tensor core reads the widened tile
+                tc::fence_async_smem();  // the tensor core reads the widened tile; the copy engine refills the slot
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ring_full[i % NR]);
-                return i + 1 < n_tiles;
-            };
-            Record x, y;
-            bool ok = load(0, x);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) flags[0] = 1;
-            if (ok && lane == 0) mbar_arrive(&stg_empty[0]);
-            for (int i = 0; ok && step(i, x, y); i += 2)
-                if (!step(i + 1, y, x)) break;
+                if (lane == 0) {
+                    mbar_arrive(&ring_full[i % NR]);
+                    mbar_arrive(&stg_empty[i % NSG]);
+                }
+            }
         } else if constexpr (F8) {
             // ---------------- fp8: widen staged e4m3 tiles into the K (warps 6, 7) / V (8, 9) ring ----------------
             const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
@@ -1035,8 +995,14 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 }
             }
         }
+    }
     } else {
         // ---------------- softmax: thread = query row = tensor-memory lane ----------------
+        if constexpr (F4) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SM));
+            load_q();
+            store_q();
+        }
         const int rho = row0 + threadIdx.x;  // this thread's row (tensor-memory lane threadIdx.x)
         const bool live = (int)threadIdx.x < R;
         // last visible key: the causal limit of the row, and never past this
