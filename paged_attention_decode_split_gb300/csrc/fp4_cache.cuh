@@ -82,10 +82,14 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t &lo, uint32_t &h
         : "r"(w));
 }
 
-// The two scale codes in the low half.
+// The two scale codes in the low or the high half.
+template <bool HIGH>
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
     uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+    if (HIGH)
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
     return r;
 }
 

@@ -63,6 +63,8 @@
 // undone by a renaming of registers in the epilogue).
 #pragma once
 
+#include <climits>
+
 #include "decode_split.cuh"
 #include "fp4_cache.cuh"
 
@@ -286,6 +288,9 @@ struct VerifyTcCfg {
     static constexpr int Q_COL = D + NSB * TK;
     static constexpr int Q_TCOLS = QSM ? 0 : D / 2;
     static constexpr int SBUF(int j) { return S_COL + j * TK; }
+    static constexpr int QROW = D * 2 + 16;            // fp4: rows of Q in f16, staged in the V ring
+    static constexpr int OFF_QPRE = OFF_V + M * QROW;  // and their pre-scales
+    static_assert(!F4 || M * (QROW + 4) <= NV * TILE_BYTES, "the staged Q rows fit in the V ring");
     static constexpr int SROW = D * 4 + 16;            // epilogue: output rows staged in the K/V rings
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
     static constexpr int W0 = F4 ? 8 : 6;              // first widening warp
@@ -404,15 +409,43 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     const int rho_q = row0 + (int)threadIdx.x;  // the softmax threads' rows (rows past R are zero padding)
     const __nv_bfloat16 *qrow =
         p.q + (((size_t)b * p.q_len + rho_q / G) * p.num_q_heads + kvh * G + rho_q % G) * D;
-    if (warp < 4 && (int)threadIdx.x < R) {
+    if (!F4 && warp < 4 && (int)threadIdx.x < R) {
 #pragma unroll
         for (int o = 0; o < D * 2; o += 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(qrow) + o));
     }
+    // fp4: the widening warps, idle until the first records land, fetch and
+    // convert Q, 8 rows each, a row's 16-byte pieces by neighbouring lanes.
+    // (A row per softmax thread is 1000 instructions that run once, at the pace
+    // they come from memory: 4 us until the first product.)
+    constexpr int QL = D / 8;              // lanes of a row
+    constexpr int QN = F4 ? QL / 4 : 1;    // loads of a lane: 8 rows, 32 / QL at a time
+    [[maybe_unused]] uint4 qx[QN];
+    [[maybe_unused]] auto fetch_q = [&]() {
+        int rl = 8 * (warp - C::W0) + lane / QL;
+        const int rho = row0 + rl, qi = rho / G;
+        int g = rho - qi * G;
+        const __nv_bfloat16 *row =
+            p.q + (((size_t)b * p.q_len + qi) * p.num_q_heads + kvh * G + g) * D + 8 * (lane % QL);
+#pragma unroll
+        for (int k = 0; k < QN; ++k) {
+            qx[k] = rl < R ? *reinterpret_cast<const uint4 *>(row) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int m = 0; m < 32 / QL; ++m) {  // the next row: the next head, or the next query's first
+                const bool wrap = ++g == G;
+                g = wrap ? 0 : g;
+                row += wrap ? (p.num_q_heads - G + 1) * D : D;
+            }
+            rl += 32 / QL;
+        }
+    };
     // Every global access waits for the work before this call on the stream,
     // except with early_kv: then the block table, seq_lens and the tiles that
     // end before the new rows are read first (see the producer below).
-    if (!p.early_kv) pdl_wait_primary();
+    if (!p.early_kv) {
+        pdl_wait_primary();
+        if (F4 && warp >= C::W0) fetch_q();
+    }
 
     int L = p.seq_lens[b];
     const bool bad_len = L < 0 || L > p.max_seq_len || L < p.q_len;
@@ -555,20 +588,20 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             while (issued_v < min(FV, n_vtiles) && before_new_rows(issued_v, CPT)) issue_tile(issued_v++, 1, policy);
         }
         pdl_wait_primary();
+        if (F4 && warp >= C::W0) fetch_q();
     }
 
     // Q rows: each softmax thread loads its row (D / 8 16-byte words, one
     // round of loads) right after the dependency wait, so the loads are in
-    // flight while tensor memory is allocated (fp4: once it has its registers).
+    // flight while tensor memory is allocated.
     constexpr int NQ = D / 8;
-    uint4 qv[NQ];
-    auto load_q = [&]() {
+    [[maybe_unused]] uint4 qv[NQ];
+    if (!F4 && warp < 4) {
         const bool qlive = (int)threadIdx.x < R;
 #pragma unroll
         for (int v = 0; v < NQ; ++v)
             qv[v] = qlive ? *reinterpret_cast<const uint4 *>(qrow + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    if (!F4 && warp < 4) load_q();
+    }
     if (warp == 4) {
         tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
         tc::tmem_relinquish();
@@ -594,7 +627,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     // enters scaled by q_pre, the power of two that brings its largest element
     // into [2^14, 2^15) (f16_prescale).
     float q_pre = 1.f;
-    auto store_q = [&]() {
+    if (!F4 && warp < 4) {
         if constexpr (F8) {  // the products run in f16: Q too
             uint32_t amax = 0;
 #pragma unroll
@@ -606,16 +639,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             for (int v = 0; v < NQ; ++v)
                 qv[v] = make_uint4(bf16x2_to_f16x2_scaled(qv[v].x, q_pre), bf16x2_to_f16x2_scaled(qv[v].y, q_pre),
                                    bf16x2_to_f16x2_scaled(qv[v].z, q_pre), bf16x2_to_f16x2_scaled(qv[v].w, q_pre));
-        }
-        if constexpr (F4) {  // the dim order of the widened K tiles
-#pragma unroll
-            for (int v = 0; v < NQ; v += 4) {
-                const uint4 a = qv[v], b2 = qv[v + 1], c2 = qv[v + 2], d2 = qv[v + 3];
-                qv[v] = make_uint4(a.x, a.y, c2.x, c2.y);
-                qv[v + 1] = make_uint4(a.z, a.w, c2.z, c2.w);
-                qv[v + 2] = make_uint4(b2.x, b2.y, d2.x, d2.y);
-                qv[v + 3] = make_uint4(b2.z, b2.w, d2.z, d2.w);
-            }
         }
         if constexpr (QSM) {
             // row rho of the block at [D/64 column blocks][M rows][128 B], 16-byte unit u of a
@@ -643,16 +666,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         }
         tc::fence_before();
         asm volatile("bar.arrive 1, 160;" ::: "memory");
-    };
-    auto wait_q = [&]() {  // (warp 4)
+    } else if (!F4 && warp == 4) {
         asm volatile("bar.sync 1, 160;" ::: "memory");
         tc::fence_after();
-    };
-    if (!F4) {
-        if (warp < 4)
-            store_q();
-        else if (warp == 4)
-            wait_q();
     }
 
     if (warp >= 4) {
@@ -732,7 +748,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // branch of one lane, the 16 products of S_i took 720 clocks and more,
         // not the tensor core's 517.
         {
-            if (F4) wait_q();
+            if constexpr (F4) {  // (Q stands in tensor memory)
+                asm volatile("bar.sync 1, 160;" ::: "memory");
+                tc::fence_after();
+            }
             constexpr uint32_t kIdQK = tc::idesc_bf16(128, TK, 0, F8);
             constexpr uint32_t kIdPV = tc::idesc_bf16(128, D, 1, F8);
             const bool leader = tc::elect_one();
@@ -841,10 +860,35 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             // its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups
             // V: lane = token pair c, dims 2 r, 2 r + 1 of every block
             const int c = lane & 3, r = tensor == 0 ? (lane >> 3) ^ (lane & 4 ? 5 : 0) : lane >> 2;
+            // Q first: as f16 with the row's pre-scale, dims in the order of the widened K tiles (of a 16-byte piece's
+            // two halves, dims 4 c .. + 3 of a block, the first goes to an even, the second to the next odd place)
+            {
+                const int first = 8 * (warp - C::W0) + (QL == 32 ? 0 : lane / QL), piece = lane % QL;
+                uint8_t *dst = smem + C::OFF_V + (piece >> 2) * 64 + (piece & 1) * 32 + (piece >> 1 & 1) * 8;
+#pragma unroll
+                for (int k = 0; k < QN; ++k) {
+                    const uint4 x = qx[k];
+                    uint32_t amax = max(max(bf16x2_absmax(x.x), bf16x2_absmax(x.y)),
+                                        max(bf16x2_absmax(x.z), bf16x2_absmax(x.w)));
+#pragma unroll
+                    for (int o = QL / 2; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    const float pre = f16_prescale(amax);
+                    const int rl = first + k * (32 / QL);
+                    uint2 *d = reinterpret_cast<uint2 *>(dst + rl * C::QROW);
+                    d[0] = make_uint2(bf16x2_to_f16x2_scaled(x.x, pre), bf16x2_to_f16x2_scaled(x.y, pre));
+                    d[2] = make_uint2(bf16x2_to_f16x2_scaled(x.z, pre), bf16x2_to_f16x2_scaled(x.w, pre));
+                    if (piece == 0) reinterpret_cast<float *>(smem + C::OFF_QPRE)[rl] = pre;
+                }
+                asm volatile("bar.arrive 3, 640;" ::: "memory");
+                if (tensor == 1) asm volatile("bar.sync 4, 384;" ::: "memory");
+            }
             for (int i = 0; i < n_tiles; ++i) {
                 // the staged records have landed, and the ring slot's previous tile has been consumed
-                bool ok = mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]);
-                if (ok && i >= NR) ok = mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]);
+                // (both asked at once first: an answer takes its time while shared memory is busy)
+                const bool landed = mbar_test_wait(&stg_full[i % NSG], (i / NSG) & 1);
+                const bool free = i < NR || mbar_test_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1);
+                bool ok = landed || mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]);
+                ok = ok && (free || mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]));
                 if (!__all_sync(0xffffffffu, ok)) {
                     flags[0] = 1;
                     break;
@@ -907,29 +951,42 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                             wd[u][0] = w.x, wd[u][1] = w.y;
                         }
                     }
+                    uint4 sw[NBL / 4];  // scales of blocks 4 w .. 4 w + 3, a word each: tokens 2 c, 2 c + 1 of both halves
+#pragma unroll
+                    for (int w = 0; w < NBL / 4; ++w)
+                        sw[w] = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
                     // rows outside the block's visible keys may hold anything: their scales become 0
-                    const int tg = t0 + 2 * c;
-                    const uint32_t vm = (tg < t_end && tg >= k_first ? 0x0000ffffu : 0u) |
-                                        (tg + 1 < t_end && tg + 1 >= k_first ? 0xffff0000u : 0u);
+                    if (t0 < k_first || t0 + 8 > t_end) {
+                        const int tg = t0 + 2 * c;
+                        const uint32_t vm = (tg < t_end && tg >= k_first ? 0x00ff00ffu : 0u) |
+                                            (tg + 1 < t_end && tg + 1 >= k_first ? 0xff00ff00u : 0u);
+#pragma unroll
+                        for (int w = 0; w < NBL / 4; ++w)
+                            sw[w] = make_uint4(sw[w].x & vm, sw[w].y & vm, sw[w].z & vm, sw[w].w & vm);
+                    }
                     uint8_t *dst = ring_rows + 2 * c * 128;
                     const int p0 = (r ^ (2 * c)) << 4, p1 = (r ^ (2 * c + 1)) << 4;
+                    auto store = [&](auto second) {
 #pragma unroll
-                    for (int w = 0; w < NBL / 4; ++w) {
-                        const uint4 sw = *reinterpret_cast<const uint4 *>(rec + 8 * D + w * 64 + c * 16);
-                        const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
-                        uint32_t s2[4];  // scale pairs of the two tokens, blocks 4 w .. 4 w + 3
+                        for (int w = 0; w < NBL / 4; ++w) {
+                            const uint32_t sb[4] = {sw[w].x, sw[w].y, sw[w].z, sw[w].w};
+                            uint32_t a[4], s2[4];  // s2: scale pairs of the two tokens
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) s2[q] = fp4::e4m3x2_f16(half ? sb[q] >> 16 : sb[q]) & vm;
-                        uint32_t a[4];
-                        fp4::e2m1x8_f16(wd[0][w], a);
-                        *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + p0) =
-                            make_uint4(fp4::hmul2_lo(a[0], s2[0]), fp4::hmul2_lo(a[1], s2[1]),
-                                       fp4::hmul2_lo(a[2], s2[2]), fp4::hmul2_lo(a[3], s2[3]));
-                        fp4::e2m1x8_f16(wd[1][w], a);
-                        *reinterpret_cast<uint4 *>(dst + 128 + w * (TT * 128) + p1) =
-                            make_uint4(fp4::hmul2_hi(a[0], s2[0]), fp4::hmul2_hi(a[1], s2[1]),
-                                       fp4::hmul2_hi(a[2], s2[2]), fp4::hmul2_hi(a[3], s2[3]));
-                    }
+                            for (int q = 0; q < 4; ++q) s2[q] = fp4::e4m3x2_f16<decltype(second)::value>(sb[q]);
+                            fp4::e2m1x8_f16(wd[0][w], a);
+                            *reinterpret_cast<uint4 *>(dst + w * (TT * 128) + p0) =
+                                make_uint4(fp4::hmul2_lo(a[0], s2[0]), fp4::hmul2_lo(a[1], s2[1]),
+                                           fp4::hmul2_lo(a[2], s2[2]), fp4::hmul2_lo(a[3], s2[3]));
+                            fp4::e2m1x8_f16(wd[1][w], a);
+                            *reinterpret_cast<uint4 *>(dst + 128 + w * (TT * 128) + p1) =
+                                make_uint4(fp4::hmul2_hi(a[0], s2[0]), fp4::hmul2_hi(a[1], s2[1]),
+                                           fp4::hmul2_hi(a[2], s2[2]), fp4::hmul2_hi(a[3], s2[3]));
+                        }
+                    };
+                    if (half)
+                        store(std::true_type{});
+                    else
+                        store(std::false_type{});
                 }
                 tc::fence_async_smem();  // the tensor core reads the widened tile; the copy engine refills the slot
                 __syncwarp();
@@ -1000,18 +1057,35 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // ---------------- softmax: thread = query row = tensor-memory lane ----------------
         if constexpr (F4) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SM));
-            load_q();
-            store_q();
+            // Q, staged by the widening warps (barrier 3), to tensor memory; then the V ring is theirs (barrier 4)
+            asm volatile("bar.sync 3, 640;" ::: "memory");
+            const uint8_t *qs = smem + C::OFF_V + threadIdx.x * C::QROW;
+#pragma unroll 1
+            for (int c = 0; c < NQ / 8; ++c) {
+                uint32_t r[32];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(qs + 128 * c + 16 * v);
+                    r[4 * v] = w.x, r[4 * v + 1] = w.y, r[4 * v + 2] = w.z, r[4 * v + 3] = w.w;
+                }
+                tc::st32(lane_base + C::Q_COL + 32 * c, r);
+            }
+            q_pre = reinterpret_cast<const float *>(smem + C::OFF_QPRE)[threadIdx.x];
+            tc::wait_st();
+            tc::fence_before();
+            asm volatile("bar.arrive 1, 160;" ::: "memory");
+            asm volatile("bar.arrive 4, 384;" ::: "memory");
         }
         const int rho = row0 + threadIdx.x;  // this thread's row (tensor-memory lane threadIdx.x)
         const bool live = (int)threadIdx.x < R;
         // last visible key: the causal limit of the row, and never past this
         // split's last chunk (a tile may reach into the next split's tokens)
         const int t_end = min(L, (c_begin + n_my) * kChunk);
-        const int lim = live ? min(L - p.q_len + rho / G, t_end - 1) : -1;
+        // (dead rows of a live warp, all zeros, see everything: a mask of their own would send the warp both ways)
+        const int lim = live ? min(L - p.q_len + rho / G, t_end - 1) : INT_MAX;
         // a warp without live rows only keeps the phases (its rows of S come from zeros of Q, its rows of O go nowhere)
         const bool idle_warp = F4 && warp * 32 >= R;
-        const int lo = p.window > 0 ? L - p.q_len + rho / G - p.window + 1 : 0;  // first key of the row's window
+        const int lo = p.window > 0 && live ? L - p.q_len + rho / G - p.window + 1 : 0;  // first key of the row's window
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
