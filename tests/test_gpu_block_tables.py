@@ -104,6 +104,18 @@ def test_extend_matches_the_model(B, width, bs, longest):
     same(run_extend(lens, new, table, free, n, bs, rows), extend_model(lens, new, table, free, n, bs, rows))
 
 
+@pytest.mark.parametrize("B,width,bs,longest", [(128, 7, 16, 40), (129, 7, 16, 40), (256, 4, 32, 3), (257, 4, 32, 3),
+                                                (512, 5, 16, 60), (60, 500, 16, 7900), (300, 90, 48, 4000),
+                                                (600, 60, 48, 2500)])
+def test_extend_at_the_sizes_where_the_launch_changes(B, width, bs, longest):
+    """Threads per CTA change at 128, 256 and 512 requests, slots per thread with
+    their number: half a million slots and more."""
+    rng = np.random.default_rng(B)
+    lens, new, table, free, n = state(rng, B, width, bs, longest, 1)
+    rows = int(new.sum())
+    same(run_extend(lens, new, table, free, n, bs, rows), extend_model(lens, new, table, free, n, bs, rows))
+
+
 @pytest.mark.parametrize("B", [7, 600])
 def test_extend_refuses_in_order(B):
     """A pool that runs out, packed rows that run out, lengths that make no sense."""
@@ -164,6 +176,33 @@ def test_release_refuses_what_the_pool_cannot_hold():
     # two pages fit, the next two would pass the five of the pool; a negative length
     assert free.tolist() == [4, 5, 0, 1, -1] and left.item() == 4 and out.tolist() == [0, 32, 16, 0]
     assert status.item() == pa.PA_DEV_BAD_PAGE | pa.PA_DEV_BAD_SEQLEN
+
+
+def test_tables_on_another_stream():
+    """Inputs made, and outputs read, on the stream the calls are given."""
+    rng = np.random.default_rng(4)
+    lens, new, table, free, n = state(rng, 40, 9, 16, 60, 2)
+    rows = int(new.sum())
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")  # noqa: E731
+    host = [i32(x) for x in (lens, new, table, free, [n], np.zeros(40))]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(2000000)  # the inputs are late
+        t_lens, t_new, t, f, left, zero = (x.clone() for x in host)
+    out, done = torch.empty_like(t_lens), torch.empty_like(t_lens)
+    slots = torch.empty(rows, dtype=torch.int64, device="cuda")
+    after, back, status = i32([0]), i32([0]), i32([0])
+    ones = torch.ones_like(t_lens)
+    stream.wait_stream(torch.cuda.current_stream())
+    pa.extend_block_tables(t_lens, t_new, t, f, left, 16, out, slots, after, status, stream=stream)
+    pa.release_block_tables(out, ones, t, f, after, 16, done, back, status, stream=stream)
+    stream.synchronize()
+    want = extend_model(lens, new, table, free, n, 16, rows)
+    same((t.cpu().numpy(), out.cpu().numpy(), slots.cpu().numpy(), int(after), int(status)), want)
+    # every page is back
+    assert int(back) == n + int(pages_of(lens, 16).sum()) and (done == 0).all()
+    assert sorted(f[:int(back)].tolist()) == sorted(set(f[:int(back)].tolist()))
 
 
 # -- a serving loop --------------------------------------------------------------------------------

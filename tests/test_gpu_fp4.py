@@ -176,7 +176,7 @@ class Problem:
 LENS = [0, 1, 15, 16, 17, 63, 64, 65, 200]
 
 
-@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (6, 2), (4, 1), (10, 2), (24, 4), (16, 2), (24, 2), (32, 2)])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (4, 2), (6, 2), (4, 1), (10, 2), (18, 3), (16, 2), (36, 3), (32, 2)])
 @pytest.mark.parametrize("d", [128, 256])
 def test_decode_groups_and_tails(hq, hkv, d):
     p = Problem(hq * 100 + d, LENS, hq, hkv, d, 48)
@@ -199,7 +199,7 @@ def test_decode_page_sizes_and_output_types(bs, bf):
 @pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 5000])
 @pytest.mark.parametrize("d", [128, 256])
 def test_decode_window_with_nan_before_it(window, d):
-    p = Problem(window, [5, 16, 100, 333, 0], 12, 2, d, 16)
+    p = Problem(window, [5, 16, 100, 333, 0], 18, 3, d, 16)
     for b, n in enumerate(p.lens):  # rows before the window: NaN scales, as in a page given away
         for t in range(max(0, n - window)):
             page, pos = p.table[b, t // 16], t % 16
@@ -240,7 +240,7 @@ def test_append_is_the_write_then_the_decode(d, splits, flags):
     (24, 4, 256, 16, [16, 17, 80, 333]),     # one 96-row block
     (8, 8, 128, 2, [2, 3, 64, 65, 129]),     # two live rows
     (14, 2, 128, 5, [5, 70, 200]),           # 7 heads per KV head
-    (12, 1, 256, 11, [11, 64, 127]),         # 132 rows: a second block of 4
+    (24, 2, 256, 11, [11, 64, 127]),         # 132 rows: a second block of 4
     (6, 1, 128, 60, [60, 100, 190]),         # three blocks
 ])
 def test_verify_shapes(hq, hkv, d, q_len, lens):
@@ -342,7 +342,7 @@ def test_verify_rows_that_do_not_see_a_nan_stay_finite(what, d, q_len, hq, hkv, 
 
 
 @pytest.mark.parametrize("hq,hkv,d,q_len,length", [
-    (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (12, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
+    (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (11, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
     (16, 1, 128, 1, 40000), (6, 1, 256, 4, 20011), (8, 1, 128, 16, 40000)])
 def test_fp32_outputs_of_long_unsplit_contexts(hq, hkv, d, q_len, length):
     """Against float64 over the rows read back.  The tensor core cuts additions
@@ -421,3 +421,63 @@ def test_calls_on_another_stream_and_two_at_once():
     torch.cuda.synchronize()
     for x, _, _, out, _, _ in jobs:
         x.check(out.double().cpu().numpy())
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different shapes over one workspace, replayed in turn."""
+    jobs = []
+    for p in (Problem(41, [900, 77, 400], 8, 2, 128, 16), Problem(42, [700, 300], 24, 4, 256, 16, q_len=5)):
+        jobs.append([p, p.desc(num_splits=4), p.tensors(), torch.empty(p.q.shape, device="cuda")])
+    ws = torch.empty(max(pa.workspace_bytes(j[1]) for j in jobs), dtype=torch.uint8, device="cuda")
+    for j in jobs:
+        p, desc, t, out = j
+        call = pa.paged_attention_decode_fp4 if p.q_len == 1 else pa.paged_attention_verify_fp4
+        call(*t, desc, out, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(*t, desc, out, ws)
+        j.append(g)
+    for _ in range(3):
+        for j in jobs:
+            j[3].fill_(float("nan"))
+        for j in jobs + jobs[::-1]:
+            j[4].replay()
+        torch.cuda.synchronize()
+        for p, _, _, out, _ in jobs:
+            p.check(out.double().cpu().numpy())
+
+
+def test_rows_on_another_stream():
+    """Write and gather on a given stream, with inputs made there."""
+    rng = np.random.default_rng(8)
+    x = [bf16_rows(rng, 100, 4, 128).cuda() for _ in range(2)]
+    g = [ref.cuda(v) for v in ref.head_scales(4)]
+    cache = [torch.zeros(pa.fp4_cache_shape(9, 16, 4, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    slots = torch.randperm(144, device="cuda")[:100].contiguous()
+    out = [torch.empty((100, 4, 128), device="cuda") for _ in range(2)]
+    want = [torch.empty_like(o) for o in out]
+    other = [c.clone() for c in cache]
+    pa.reshape_and_cache_fp4(*x, *other, slots, *g)
+    pa.gather_cache_fp4(*other, slots, *g, *want)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(2000000)  # the rows are late
+        late = [v.clone() for v in x]
+    pa.reshape_and_cache_fp4(*late, *cache, slots, *g, stream=stream)
+    pa.gather_cache_fp4(*cache, slots, *g, *out, stream=stream)
+    stream.synchronize()
+    for a, b in zip(out + cache, want + other):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_one_token_and_nothing(q_len):
+    """The smallest calls: contexts of nothing but the new rows, beside an empty one."""
+    p = Problem(61, [q_len, 0, q_len], 4, 1, 128, 16, q_len=q_len)
+    for splits in (1, 2):
+        for bf in (False, True):
+            out, status = p.run(num_splits=splits, out_dtype=pa.PA_OUT_BF16 if bf else pa.PA_OUT_F32)
+            assert status == (0 if q_len == 1 else pa.PA_DEV_BAD_SEQLEN)  # a sequence shorter than its rows
+            p.check(out, bf=bf)
