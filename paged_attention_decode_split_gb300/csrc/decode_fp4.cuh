@@ -109,7 +109,7 @@ __device__ __forceinline__ void append_new_row_fp4(const DecodeParams &p, int b,
 // product (columns 4-7 repeat Q, and carry the residuals into P.V).
 // FAR: the accumulators are moved to a second sum every kFp4FarPairs of a
 // warp's pairs (splits that give a warp kFp4FarMin pairs or more, fp32 output).
-constexpr int kFp4FarPairs = 64, kFp4FarMin = 96;
+constexpr int kFp4FarPairs = 8, kFp4FarMin = 12;
 template <int D, int NT, int NW, int SPW, bool RES, bool PACK, bool FAR>
 __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const Fp4Params fp) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
 
     // The tensor core cuts each addition to an accumulator off towards zero: the
     // accumulators lose 2.4e-9 of themselves per key.  FAR moves them to a sum in
-    // local memory every kFar pairs (2048 keys: 5e-6), unless fewer than half as
+    // local memory every kFar pairs (256 keys: 6e-7), unless fewer than half as
     // many follow.  A kernel of its own: it costs the other one 0.5 us of 16.5.
     constexpr int kFar = kFp4FarPairs;
     static_assert(!FAR || (RES && !PACK), "a second sum of O: fp32 output");

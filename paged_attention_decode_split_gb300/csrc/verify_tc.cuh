@@ -313,9 +313,15 @@ struct VerifyTcCfg {
 // RES: the residual of P is multiplied too (F4 with bf16 output goes without:
 // a weight is then off by at most 2^-12, an eighth of the half step that the
 // output is rounded by).
-// FAR: O is moved to a second sum every kVerifyFarTiles tiles (splits of
-// kVerifyFarMin tiles and more with fp32 output).
-constexpr int kVerifyFarTiles = 32, kVerifyFarMin = 48;
+// FAR: O is moved to a second sum every few tiles (verify_far_tiles), unless a
+// single tile follows (splits of kVerifyFarMin tiles and more with fp32 output).
+// The tensor core cuts each addition to an accumulator off towards zero: O loses
+// 2.4e-9 of itself per key (measured; half a step, 2^-24, for each of the eight
+// products of a tile, on a sum that grows).  So few tiles that the loss stays
+// below what binary32 sums and exponentials over the whole context are off by
+// anyway, 1.8e-8 sqrt(keys): 7e-7, 1.3e-6 and 2.5e-6.
+__device__ __forceinline__ int verify_far_tiles(int keys) { return keys <= 4096 ? 4 : keys <= 16384 ? 8 : 16; }
+constexpr int kVerifyFarMin = 4 + 2;
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
           bool FAR = false>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
@@ -327,7 +333,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     static_assert(RES || (F4 && C::VPK == 1), "the residual is left out over an fp4 cache only");
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
     static_assert(!FAR || (F4 && RES), "a second sum of O: fp4 cache with fp32 output");
-    constexpr int kFar = kVerifyFarTiles;
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -482,6 +487,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     }
     const int n_tiles = (n_my + CPK - 1) / CPK;   // score tiles (K tiles)
     const int n_vtiles = (n_my + CPT - 1) / CPT;  // V tiles (VPK per score tile)
+    // tile i starts O anew: what the tiles before it summed goes to the second sum
+    [[maybe_unused]] const int far_tiles = verify_far_tiles(p.window > 0 ? min(L, p.window + p.q_len) : L);
+    auto far_at = [&](int i) { return FAR && i > 0 && (i & (far_tiles - 1)) == 0 && n_tiles - i >= 2; };
 
     // The split's block-table entries, staged in shared memory by all threads
     // (visible to the producer after the next __syncthreads); splits spanning
@@ -792,7 +800,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                                     // P (head, then residual) of this 64-key half: 16 tokens = 8 columns per step
                                     const uint32_t a_tm = tm + C::SBUF(j) + h2 * TT + h * (TT / 2) + ks * 8;
                                     tc::mma_bf16_ta(tm + C::O_COL, a_tm, v_desc + (ks * 16 * 128 >> 4), kIdPV,
-                                                    (i > 0 || h2 > 0 || ks > 0 || h > 0) ? 1u : 0u);
+                                                    ((i > 0 && !far_at(i)) || h2 > 0 || ks > 0 || h > 0) ? 1u : 0u);
                                 }
                             }
                             tc::commit(&v_empty[vt % NV]);
@@ -1089,12 +1097,72 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
-        // The tensor core cuts each addition to the accumulator off towards
-        // zero: O loses 2.2e-9 of itself per key.  FAR moves O to this row's sum
-        // every kFar tiles (2048 keys: 5e-6), unless fewer than half as many
-        // follow.  A kernel of its own: it costs the other one 4 us of 74.
-        [[maybe_unused]] float o_far[FAR ? D : 1];  // (indexed at run time: local memory)
-        [[maybe_unused]] float m_far = -INFINITY;   // the reference max that o_far stands for
+        // The second sum stands in the warp's own rows of the output, in an order
+        // of its own (a lane's float4 j at float4 j * live rows + lane: whole
+        // lines per access), and is added to by red while the row's reference max
+        // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 64 us
+        // with it and 51 without.
+        [[maybe_unused]] float m_far = -INFINITY;  // the reference max that the second sum stands for
+        [[maybe_unused]] const uint32_t my_row =
+            live ? (uint32_t)((((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split)
+                 : 0u;
+        [[maybe_unused]] const int n_live = min(32, R - warp * 32);
+        [[maybe_unused]] float *far_base = p.num_splits == 1 ? static_cast<float *>(p.out) : p.part_o;
+        [[maybe_unused]] auto far_place = [&](int j) {  // (the whole warp) the lane's float4 j of the second sum
+            const int at = j * n_live + min(lane, n_live - 1);
+            const uint32_t row = __shfl_sync(0xffffffffu, my_row, at / (D / 4));
+            return reinterpret_cast<float4 *>(far_base + (size_t)row * D) + at % (D / 4);
+        };
+        // O, relative to m_win, joins the second sum.  (Predicated accesses, one loop per kind: branches around every
+        // access cost six times the accesses.)
+        [[maybe_unused]] auto far_add = [&](float m_win, bool first) {
+            const float alpha = m_far == m_win ? 1.f : fast_exp2(m_far - m_win);
+            const uint32_t mine = lane < n_live;
+            const bool moved = __any_sync(0xffffffffu, mine && m_far != m_win);
+            auto add = [&](auto kind) {
+                constexpr int KIND = decltype(kind)::value;  // 0: store, 1: red, 2: read, scale, add, store
+#pragma unroll 1
+                for (int c1 = 0; c1 < D; c1 += 64) {
+                    uint32_t r[4][16];
+                    [[maybe_unused]] float4 f[KIND == 2 ? 16 : 1];
+                    if constexpr (KIND == 2) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[j] = __ldcg(far_place(c1 / 4 + j));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc::ld16_nowait(lane_base + C::O_COL + c1 + 16 * k, r[k]);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float4 *at = far_place(c1 / 4 + j);
+                        float4 v =
+                            make_float4(__uint_as_float(r[j / 4][j % 4 * 4]), __uint_as_float(r[j / 4][j % 4 * 4 + 1]),
+                                        __uint_as_float(r[j / 4][j % 4 * 4 + 2]), __uint_as_float(r[j / 4][j % 4 * 4 + 3]));
+                        if constexpr (KIND == 1) {
+                            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                                         "@p red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(at),
+                                         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mine)
+                                         : "memory");
+                        } else {
+                            if constexpr (KIND == 2)
+                                v = make_float4(fmaf(f[j].x, alpha, v.x), fmaf(f[j].y, alpha, v.y),
+                                                fmaf(f[j].z, alpha, v.z), fmaf(f[j].w, alpha, v.w));
+                            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                                         "@p st.global.cg.v4.f32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(at),
+                                         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mine)
+                                         : "memory");
+                        }
+                    }
+                }
+            };
+            if (first)
+                add(std::integral_constant<int, 0>{});
+            else if (!moved)
+                add(std::integral_constant<int, 1>{});
+            else
+                add(std::integral_constant<int, 2>{});
+            m_far = m_win;
+        };
         bool ok = true;
         // O += P_k V_k of tile k.  S_i being there says that tile i - NSB's
         // product is done (the tensor core ran it first), so a wait for tile
@@ -1104,28 +1172,6 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         };
         for (int i = 0; i < n_tiles; ++i) {
             const int j = i % NSB;
-            if constexpr (FAR) {
-                if (i > 0 && i % kFar == 0 && n_tiles - i >= kVerifyFarMin - kFar) {
-                    if (!wait_pv(i - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const float alpha = m_far == -INFINITY ? 0.f : fast_exp2(m_far - m_ref);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        float ov[16];
-                        tc::ld16(lane_base + C::O_COL + c0, ov);
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            o_far[c0 + c] = i == kFar ? ov[c] : fmaf(o_far[c0 + c], alpha, ov[c]);
-                            ov[c] = 0.f;
-                        }
-                        tc::st16(lane_base + C::O_COL + c0, ov);
-                    }
-                    m_far = m_ref;
-                }
-            }
             // waits ahead of a warp-collective tensor-memory access end the same way for the whole warp
             if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j], (i / NSB) & 1, &flags[0]))) {
                 ok = false;
@@ -1179,7 +1225,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 // then only after the previous tile's P.V product has finished
                 const bool raise = mx > m_ref + kLazy;
                 const bool need_rescale = raise && m_ref != -INFINITY;
-                if (__any_sync(0xffffffffu, need_rescale)) {
+                [[maybe_unused]] const float m_win = m_ref;  // (a window's end: what O stands for)
+                if (far_at(i)) {
+                    if (need_rescale) l_sum *= fast_exp2(m_ref - mx);
+                } else if (__any_sync(0xffffffffu, need_rescale)) {
                     if (!wait_pv(i - 1)) {
                         ok = false;
                         break;
@@ -1237,6 +1286,16 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 tc::st32(lane_base + C::SBUF(j), hw);
                 if constexpr (RES) tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
                 tc::wait_st();
+                if constexpr (FAR) {
+                    if (far_at(i)) {  // (O is free for P_i V_i once it has been read)
+                        if (!wait_pv(i - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        far_add(m_win, i == far_tiles);
+                    }
+                }
                 tc::fence_before();
             } else {
                 tc::fence_after();
@@ -1378,6 +1437,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             return hit;
         };
         const bool direct = p.num_splits == 1;  // the final output, else this split's record
+        if (FAR && !ok) {  // (other lanes' parts of the second sum may be on their way to this row)
+            __threadfence();
+            __syncwarp();
+        }
         if (ok) {
             // Every tile has been consumed by the tensor core, so the K/V rings
             // are free: the row is staged there (rows SROW bytes apart, so the
@@ -1386,7 +1449,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             // rows going out as 32 separate segments per store.
             const bool bf = direct && p.out_bf16;
             uint8_t *srow = smem + threadIdx.x * C::SROW;
-            const float far_w = m_far == -INFINITY ? 0.f : fast_exp2(m_far - m_ref);
+            [[maybe_unused]] const float far_w = m_far == m_ref ? 1.f : fast_exp2(m_far - m_ref);
             [[maybe_unused]] const bool some_nan = F4 && flags[2] != 0;
 #pragma unroll 1
             for (int c1 = 0; c1 < D; c1 += 64) {
@@ -1394,6 +1457,21 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tc::ld16_nowait(lane_base + C::O_COL + c1 + 16 * k, r[k]);
                 tc::wait_ld();
+                if constexpr (FAR) {
+                    if (n_tiles >= far_tiles + 2 && !idle_warp) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 *at = far_place(c1 / 4 + j);
+                            const float4 f = __ldcg(at);
+                            const float fv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t &o = r[j / 4][j % 4 * 4 + e];
+                                o = __float_as_uint(fmaf(fv[e], far_w, __uint_as_float(o)));
+                            }
+                        }
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int c0 = c1 + 16 * k;
@@ -1402,10 +1480,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     for (int c = 0; c < 16; ++c) {
                         if constexpr (F4) {  // column 8 r' + 2 q + e of a 64-dim group holds dim 16 q + 2 r' + e
                             const int col = (c >> 1) * 8 + 2 * k + (c & 1);
-                            float o = __uint_as_float(r[col >> 4][col & 15]);
-                            if constexpr (FAR) {
-                                if (n_tiles >= kVerifyFarMin) o = fmaf(o_far[c1 + col], far_w, o);
-                            }
+                            const float o = __uint_as_float(r[col >> 4][col & 15]);
                             // (a bad page's stand-in may hold NaN)
                             ov[c] = poisoned ? 0.f : o * inv;
                         } else {
@@ -1431,6 +1506,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                                 make_float4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
                     }
                 }
+            }
+            if constexpr (FAR) {  // the second sum has been read by the whole warp, before any of its rows is written
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                __syncwarp();
             }
             if (live) {
                 tc::fence_async_smem();  // the staged row is read by the copy engine

@@ -342,14 +342,14 @@ def test_verify_rows_that_do_not_see_a_nan_stay_finite(what, d, q_len, hq, hkv, 
 
 
 @pytest.mark.parametrize("hq,hkv,d,q_len,length", [
-    (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (11, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
+    (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (16, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
     (16, 1, 128, 1, 40000), (6, 1, 256, 4, 20011), (8, 1, 128, 16, 40000)])
 def test_fp32_outputs_of_long_unsplit_contexts(hq, hkv, d, q_len, length):
     """Against float64 over the rows read back.  The tensor core cuts additions
-    off towards zero: half a step, 2^-24 of at most 2048 / 16 x 2 growing sums
-    before they move to another sum, is a loss of 5.5e-6 at most on the
+    off towards zero: half a step, 2^-24 of at most 17 x 64 / 16 x 2 growing
+    sums before they move to another sum, is a loss of 2.9e-6 at most on the
     average (the mean of 1 / mantissa is 0.72, of a growing sum half its end);
-    what rounds both ways averages out below that.  1e-5 overall."""
+    what rounds both ways averages out below that.  4e-6 overall."""
     rng = np.random.default_rng(length)
     bs, pages = 784, -(-length // 784)
     g = [ref.cuda(x) for x in ref.head_scales(hkv)]
@@ -370,7 +370,7 @@ def test_fp32_outputs_of_long_unsplit_contexts(hq, hkv, d, q_len, length):
     x = torch.einsum("qhd,td->qht", q.double(), k[:, 0].double()) * d ** -0.5
     hidden = torch.arange(length, device="cuda") > length - q_len + torch.arange(q_len, device="cuda")[:, None]
     want = x.masked_fill(hidden[:, None], -math.inf).softmax(-1) @ v[:, 0].double()
-    assert ((out.double() - want).norm() / want.norm()).item() <= 1e-5
+    assert ((out.double() - want).norm() / want.norm()).item() <= 4e-6
 
 
 def test_offsets_past_32_bits():
