@@ -37,7 +37,7 @@ cudaError_t launch_res(const VerifyParams &p, dim3 grid, cudaStream_t stream, in
 template <int D, int NK, int NV, int NSG>
 cudaError_t launch_t(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
     if (p.out_bf16) return launch_res<D, NK, NV, NSG, false, false>(p, grid, stream, slot);
-    if (p.chunks_per_split > (kVerifyFarMin - 1) * 4)
+    if (p.chunks_per_split > kVerifyFarTiles * 4)
         return launch_res<D, NK, NV, NSG, true, true>(p, grid, stream, slot + 1);
     return launch_res<D, NK, NV, NSG, true, false>(p, grid, stream, slot + 2);
 }

@@ -313,15 +313,12 @@ struct VerifyTcCfg {
 // RES: the residual of P is multiplied too (F4 with bf16 output goes without:
 // a weight is then off by at most 2^-12, an eighth of the half step that the
 // output is rounded by).
-// FAR: O is moved to a second sum every few tiles (verify_far_tiles), unless a
-// single tile follows (splits of kVerifyFarMin tiles and more with fp32 output).
-// The tensor core cuts each addition to an accumulator off towards zero: O loses
-// 2.4e-9 of itself per key (measured; half a step, 2^-24, for each of the eight
-// products of a tile, on a sum that grows).  So few tiles that the loss stays
-// below what binary32 sums and exponentials over the whole context are off by
-// anyway, 1.8e-8 sqrt(keys): 7e-7, 1.3e-6 and 2.5e-6.
-__device__ __forceinline__ int verify_far_tiles(int keys) { return keys <= 4096 ? 4 : keys <= 16384 ? 8 : 16; }
-constexpr int kVerifyFarMin = 4 + 2;
+// FAR: O is moved to a second sum every kVerifyFarTiles tiles (splits of more
+// tiles with fp32 output).  The tensor core cuts each addition to an accumulator
+// off towards zero: O loses 2.4e-9 of itself per key (measured; half a step,
+// 2^-24, for each of the eight products of a tile, on a sum that grows), 7e-7 in
+// 4 tiles -- what binary32 sums over a thousand keys are off by.
+constexpr int kVerifyFarTiles = 4;
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
           bool FAR = false>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
@@ -488,8 +485,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     const int n_tiles = (n_my + CPK - 1) / CPK;   // score tiles (K tiles)
     const int n_vtiles = (n_my + CPT - 1) / CPT;  // V tiles (VPK per score tile)
     // tile i starts O anew: what the tiles before it summed goes to the second sum
-    [[maybe_unused]] const int far_tiles = verify_far_tiles(p.window > 0 ? min(L, p.window + p.q_len) : L);
-    auto far_at = [&](int i) { return FAR && i > 0 && (i & (far_tiles - 1)) == 0 && n_tiles - i >= 2; };
+    auto far_at = [&](int i) { return FAR && i > 0 && i % kVerifyFarTiles == 0; };
 
     // The split's block-table entries, staged in shared memory by all threads
     // (visible to the producer after the next __syncthreads); splits spanning
@@ -1097,6 +1093,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
+        [[maybe_unused]] float l_low = 0.f;
         // The second sum stands in the warp's own rows of the output, in an order
         // of its own (a lane's float4 j at float4 j * live rows + lane: whole
         // lines per access), and is added to by red while the row's reference max
@@ -1227,7 +1224,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 const bool need_rescale = raise && m_ref != -INFINITY;
                 [[maybe_unused]] const float m_win = m_ref;  // (a window's end: what O stands for)
                 if (far_at(i)) {
-                    if (need_rescale) l_sum *= fast_exp2(m_ref - mx);
+                    if (need_rescale) {
+                        const float alpha = fast_exp2(m_ref - mx);
+                        l_sum *= alpha;
+                        l_low *= alpha;
+                    }
                 } else if (__any_sync(0xffffffffu, need_rescale)) {
                     if (!wait_pv(i - 1)) {
                         ok = false;
@@ -1243,7 +1244,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                         for (int c = 0; c < 16; ++c) ov[c] *= alpha;
                         tc::st16(lane_base + C::O_COL + c0, ov);
                     }
-                    if (need_rescale) l_sum *= alpha;
+                    if (need_rescale) {
+                        l_sum *= alpha;
+                        l_low *= alpha;
+                    }
                 }
                 if (raise) m_ref = mx;
                 // The tile may be short or end in a partial chunk: V rows past the
@@ -1282,7 +1286,13 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     else
                         split_bf16(p0, p1, hw[c], lw[c]);
                 }
-                l_sum += ps2.x + ps2.y;
+                if constexpr (FAR) {  // with what the sum's rounding leaves over
+                    const float t = ps2.x + ps2.y + l_low, sum = l_sum + t;
+                    l_low = t - (sum - l_sum);
+                    l_sum = sum;
+                } else {
+                    l_sum += ps2.x + ps2.y;
+                }
                 tc::st32(lane_base + C::SBUF(j), hw);
                 if constexpr (RES) tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
                 tc::wait_st();
@@ -1293,7 +1303,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                             break;
                         }
                         tc::fence_after();
-                        far_add(m_win, i == far_tiles);
+                        far_add(m_win, i == kVerifyFarTiles);
                     }
                 }
                 tc::fence_before();
@@ -1458,7 +1468,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 for (int k = 0; k < 4; ++k) tc::ld16_nowait(lane_base + C::O_COL + c1 + 16 * k, r[k]);
                 tc::wait_ld();
                 if constexpr (FAR) {
-                    if (n_tiles >= far_tiles + 2 && !idle_warp) {
+                    if (n_tiles > kVerifyFarTiles && !idle_warp) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float4 *at = far_place(c1 / 4 + j);
