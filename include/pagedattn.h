@@ -354,10 +354,13 @@ pa_status pa_gather_cache_fp4(const void *k_cache, const void *v_cache, const in
 /* paged_attention_decode over an fp4 cache: out as pa_paged_attention_decode
  * with K_t = code * S * k_scale[kv head], V_t likewise.  Same plan, workspace,
  * limits, window and flags as pa_paged_attention_decode.  The products run on
- * code * S in f16 (exact; q enters scaled by a power of two, softmax weights as
- * an f16 head and residual) with binary32 sums.  Slots past a sequence's end or
+ * code * S in f16 (exact; q enters scaled by a power of two) with binary32 sums.
+ * For fp32 outputs a softmax weight enters as an f16 head and an f16 residual,
+ * and the sums are split so that they lose about 1e-6 of themselves at most; for
+ * bf16 outputs it enters as one f16 (off by 2^-12 at most, twice in decode,
+ * where it is multiplied by V's scale first).  Slots past a sequence's end or
  * before its window may hold any bytes.  A NaN in a visible row (a NaN scale)
- * or in q makes the outputs that depend on it NaN. */
+ * or in q makes the outputs that depend on it NaN, and no others. */
 pa_status pa_paged_attention_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
                                         const float *k_scale, const float *v_scale,
                                         const int32_t *block_table, const int32_t *seq_lens,
@@ -375,8 +378,9 @@ pa_status pa_paged_attention_decode_append_fp4(const void *q, const void *k_new,
                                                size_t workspace_bytes, int32_t *device_status, void *stream);
 
 /* paged_attention_verify over an fp4 cache: out as pa_paged_attention_verify
- * with K and V as for pa_paged_attention_decode_fp4.  Same plan, workspace,
- * limits and errors as pa_paged_attention_verify. */
+ * with K and V as for pa_paged_attention_decode_fp4, whose rules on rounding
+ * and NaN hold row by row (a NaN in a new row reaches the rows that see it).
+ * Same plan, workspace, limits and errors as pa_paged_attention_verify. */
 pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, const void *v_cache,
                                         const float *k_scale, const float *v_scale,
                                         const int32_t *block_table, const int32_t *seq_lens,

@@ -17,8 +17,9 @@
 // keeps one request and its prefix in shared memory, and a thread writes a run
 // of consecutive slots from one search, searching again only where a page or a
 // request ends: runs of two, which fill the GPU up to 311,000 tokens, and of
-// eight beyond that (a step of 32 single tokens: 3.6 us against 7.3 with runs
-// of eight; 1M slots: 8.0 against 9.7 us).  CTAs of their own write the table
+// eight beyond that (a step of 32 single tokens: 3.0 us; 1M slots of 509
+// requests: 8.1 us against 9.7 with four slot pairs per search; release and
+// admission of 256 requests: 6.4 us in two calls).  CTAs of their own write the table
 // entries.  Beyond 512 requests the prefix is kept per group of requests and
 // the group is walked.
 #include <algorithm>

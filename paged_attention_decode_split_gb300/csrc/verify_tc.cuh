@@ -54,13 +54,23 @@
 //
 // fp4 cache (F4; fp4_cache.cuh): as over an e4m3 cache, but the staging slots
 // hold the tile's four records per tensor, copied by untiled bulk copies (one
-// per run of chunks in a page), and the widening applies each 16-dim block's
-// scale: code * S in f16 (exact).  The dims of a row are left in an order that
+// per run of chunks in a page) that a warp per tensor issues (5: K, 6: V), and
+// sixteen warps (8-15: K, 16-23: V; half a record each) apply each 16-dim
+// block's scale: code * S in f16 (exact).  At the start they fetch and convert
+// Q.  The softmax warps take registers from the others (setmaxnreg).  The dims of a row are left in an order that
 // makes every ring write a whole 16-byte chunk of what one lane holds: K chunk
 // 4 g + c holds dims 4 c .. 4 c + 3 of blocks 2 g and 2 g + 1 (Q is stored in
 // the same order, a renaming of registers), V chunk 8 w + r of a row holds dims
 // 2 r, 2 r + 1 of blocks 4 w .. 4 w + 3 (so O's columns stand in that order,
-// undone by a renaming of registers in the epilogue).
+// undone by a renaming of registers in the epilogue).  bf16 outputs leave the
+// residual of P out; fp32 outputs of long splits keep a second sum (FAR).
+// What bounds it: shared memory.  A tile of 64 keys is 64 KiB widened and
+// written, 64 KiB (96 with the residual) read by the tensor core and 18 KiB
+// copied and read, 1450 (1700) clocks of its 128 bytes per clock, at a tile time
+// of 1750 (2250); the products take 1030 (1540).  2048 rows over 16K (24 heads on
+// 4, D = 256): 720 us; 32 x 5 rows over 700-2048 (48 on 4): 39 us.  With 8
+// widening warps the prefill took 748 us, with one producer warp for both
+// tensors 790, with products issued from a branch of one lane 900.
 #pragma once
 
 #include <climits>
@@ -1097,8 +1107,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // The second sum stands in the warp's own rows of the output, in an order
         // of its own (a lane's float4 j at float4 j * live rows + lane: whole
         // lines per access), and is added to by red while the row's reference max
-        // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 64 us
-        // with it and 51 without.
+        // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 78 us
+        // with it and 51 without; the bytes of the second sum are what it costs
+        // (moved by four other warps, or read, added and stored without red: no
+        // less).
         [[maybe_unused]] float m_far = -INFINITY;  // the reference max that the second sum stands for
         [[maybe_unused]] const uint32_t my_row =
             live ? (uint32_t)((((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split)
