@@ -127,10 +127,11 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     float *q_mul = reinterpret_cast<float *>(smem + C::OFF_QSC);
 
     // The reference max of a head is kept kAbove over the largest score it was
-    // raised for, and raised again when a score passes it by kRaise: without
-    // the residual P is multiplied by the V scales (up to 448) in f16, so it
-    // stays below 2^6.
-    constexpr float kAbove = RES ? 0.f : 2.f, kRaise = kLazyLog2 - kAbove;
+    // raised for, and raised again when a score passes it by kRaise.  With the
+    // residual it is kept below, so that P in f16, at most 2^15, holds weights
+    // down to 2^-32 of the largest (f16 ends at 2^-25); without, P is multiplied
+    // by the V scales (up to 448) in f16 and stays below 2^6.
+    constexpr float kAbove = RES ? -7.f : 2.f, kRaise = kLazyLog2 - kAbove;
 
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -341,6 +341,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
     static_assert(!FAR || (F4 && RES), "a second sum of O: fp4 cache with fp32 output");
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
+    // fp4: the reference is kept 2^7 below the max, so that P in f16, at most 2^15,
+    // holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
+    constexpr float kBelow = F4 ? 7.f : 0.f;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     // K and V tiles have their own rings: a K slot is free again as soon as
@@ -1232,6 +1235,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 }
                 // lazy rescale: only when the max grows by more than 2^kLazy, and
                 // then only after the previous tile's P.V product has finished
+                mx -= kBelow;
                 const bool raise = mx > m_ref + kLazy;
                 const bool need_rescale = raise && m_ref != -INFINITY;
                 [[maybe_unused]] const float m_win = m_ref;  // (a window's end: what O stands for)

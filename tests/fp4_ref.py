@@ -160,6 +160,30 @@ def tolerance(mag, reach, d, keys, out_bf16, ref):
     return tol + (np.abs(ref) * 2.0 ** -8 if out_bf16 else 0.0)
 
 
+def vanished(q, k_cache, v_cache, g, table, lens, scale, q_len=1, window=0):
+    """What small weights may lose, element by element.  A weight enters the
+    product as two f16 numbers, relative to a reference that gives the largest
+    weight of its split 2^7 or more, so its error ends at half the smallest f16,
+    2^-25, or at itself: at most min(w, 2^-32 of the largest w) |v|, summed."""
+    rows, hq, d = q.shape
+    hkv, bs = k_cache.shape[1], k_cache.shape[2] * 16
+    off = np.zeros((rows, hq, d))
+    q = np.asarray(q, np.float64)
+    for b, n in enumerate(lens):
+        if n < max(1, q_len):
+            continue
+        s = slots_of(table[b], n, bs)
+        k, v = read_rows("k", k_cache, s, g[0]), np.abs(read_rows("v", v_cache, s, g[1]))
+        for i in range(q_len):
+            pos = n - q_len + i
+            lo = max(0, pos - window + 1) if window else 0
+            for h in range(hq):
+                x = k[lo:pos + 1, h * hkv // hq] @ q[b * q_len + i, h] * scale
+                w = np.exp(x - x.max())
+                off[b * q_len + i, h] = np.minimum(w, 2.0 ** -32) @ v[lo:pos + 1, h * hkv // hq] / w.sum()
+    return off
+
+
 def head_scales(hkv):
     """Scales that are no powers of two, one per KV head."""
     h = np.arange(hkv, dtype=np.float32)

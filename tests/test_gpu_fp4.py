@@ -341,6 +341,29 @@ def test_verify_rows_that_do_not_see_a_nan_stay_finite(what, d, q_len, hq, hkv, 
         assert (np.abs(out - want) <= tol)[np.isfinite(want)].all()
 
 
+@pytest.mark.parametrize("hq,hkv,d,q_len,lens,window", [
+    (6, 1, 256, 4, [1500, 700, 4], 0),    # 24 rows: one warp, not all of it live
+    (24, 2, 256, 11, [900, 11], 0),       # 132 rows: a full block and one of 4 rows
+    (8, 8, 128, 3, [1100, 333], 500),
+    (12, 2, 128, 16, [1303], 0),          # 96 rows
+    (6, 1, 256, 1, [4600, 3100], 0), (8, 1, 128, 1, [6000], 0), (16, 1, 128, 1, [4000], 3900)])
+def test_second_sum_with_growing_scores(hq, hkv, d, q_len, lens, window):
+    """fp32 outputs whose accumulators move to a second sum, with keys that grow
+    along the sequence, so that the reference max rises again and again."""
+    p = Problem(q_len + window, lens, hq, hkv, d, 16, q_len=q_len)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            p.k[p.table[b, t // 16]][:, 0, ref.byte_places("k", t % 16, d)[1]] = 0x30 + t * 64 // n
+    args = (p.q.float().numpy(), p.k, p.v, p.g, p.table, p.lens, p.scale, q_len, window)
+    want, mag, reach = ref.attention(*args)
+    tol = ref.tolerance(mag, reach, d, max(lens), False, want) + ref.vanished(*args)
+    for kw in (dict(num_splits=1), dict(num_splits=2, flags=pa.PA_FLAG_EARLY_KV_READ)):
+        out, status = p.run(window=window, **kw)
+        assert status == 0
+        assert (np.abs(out - want) <= tol).all()
+        assert np.linalg.norm(out - want) <= 2.0 ** -18 * np.linalg.norm(want)
+
+
 @pytest.mark.parametrize("hq,hkv,d,q_len,length", [
     (6, 1, 256, 1, 49189), (4, 1, 256, 1, 33000), (16, 1, 256, 1, 40000), (8, 1, 128, 1, 60000),
     (16, 1, 128, 1, 40000), (6, 1, 256, 4, 20011), (8, 1, 128, 16, 40000)])
