@@ -66,8 +66,9 @@
 // residual of P out; fp32 outputs of long splits keep a second sum (FAR).
 // What bounds it: shared memory.  A tile of 64 keys is 64 KiB widened and
 // written, 64 KiB (96 with the residual) read by the tensor core and 18 KiB
-// copied and read, 1450 (1700) clocks of its 128 bytes per clock, at a tile time
-// of 1750 (2250); the products take 1030 (1540).  2048 rows over 16K (24 heads on
+// copied and read, 1450 (1700) clocks of its 128 bytes per clock and more with
+// scales and barriers, at a tile time of 1750 (2250); the products take 1030
+// (1540), the issue slots are two thirds full.  2048 rows over 16K (24 heads on
 // 4, D = 256): 720 us; 32 x 5 rows over 700-2048 (48 on 4): 39 us.  With 8
 // widening warps the prefill took 748 us, with one producer warp for both
 // tensors 790, with products issued from a branch of one lane 900.
