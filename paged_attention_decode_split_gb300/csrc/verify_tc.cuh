@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     uint64_t *vst_full = kst_empty + NSG;
     uint64_t *vst_empty = vst_full + NSG;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page, [2] nan_bits holds something
+    // [0] abort, [1] bad page, [2] nan_bits holds something
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
     // F4: a V block with a NaN scale whose token only some of the rows see
     // enters the product as zeros (0 * NaN would reach every row) and is noted
@@ -689,6 +690,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         tc::fence_after();
     }
 
+    // (a branch for setmaxnreg: what either side may use is known only where the sides are apart)
     if (warp >= 4) {
     if constexpr (F4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (F4 && (warp == 5 || warp == 6)) {
