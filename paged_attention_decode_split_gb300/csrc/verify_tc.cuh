@@ -69,7 +69,7 @@
 // copied and read, 1450 (1700) clocks of its 128 bytes per clock and more with
 // scales and barriers, at a tile time of 1750 (2250); the products take 1030
 // (1540), the issue slots are two thirds full.  2048 rows over 16K (24 heads on
-// 4, D = 256): 720 us; 32 x 5 rows over 700-2048 (48 on 4): 39 us.  With 8
+// 4, D = 256): 701 us; 32 x 5 rows over 700-2048 (48 on 4): 38 us.  With 8
 // widening warps the prefill took 748 us, with one producer warp for both
 // tensors 790, with products issued from a branch of one lane 900.
 #pragma once
@@ -904,11 +904,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             }
             for (int i = 0; i < n_tiles; ++i) {
                 // the staged records have landed, and the ring slot's previous tile has been consumed
-                // (both asked at once first: an answer takes its time while shared memory is busy)
-                const bool landed = mbar_test_wait(&stg_full[i % NSG], (i / NSG) & 1);
-                const bool free = i < NR || mbar_test_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1);
-                bool ok = landed || mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]);
-                ok = ok && (free || mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]));
+                bool ok = mbar_wait(&stg_full[i % NSG], (i / NSG) & 1, &flags[0]);
+                ok = ok && (i < NR || mbar_wait(&ring_empty[i % NR], ((i / NR) - 1) & 1, &flags[0]));
                 if (!__all_sync(0xffffffffu, ok)) {
                     flags[0] = 1;
                     break;
@@ -956,6 +953,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                                 flags[2] = 1;
                                 sb[o] = 0;
                             }
+                            tc::fence_async_smem();  // before the slot's next copy
                         }
                         __syncwarp();
                     }
@@ -1008,12 +1006,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     else
                         store(std::false_type{});
                 }
-                tc::fence_async_smem();  // the tensor core reads the widened tile; the copy engine refills the slot
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ring_full[i % NR]);
-                    mbar_arrive(&stg_empty[i % NSG]);
-                }
+                if (lane == 0) mbar_arrive(&stg_empty[i % NSG]);
+                tc::fence_async_smem();  // the tensor core reads the widened tile
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ring_full[i % NR]);
             }
         } else if constexpr (F8) {
             // ---------------- fp8: widen staged e4m3 tiles into the K (warps 6, 7) / V (8, 9) ring ----------------
@@ -1113,7 +1110,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // The second sum stands in the warp's own rows of the output, in an order
         // of its own (a lane's float4 j at float4 j * live rows + lane: whole
         // lines per access), and is added to by red while the row's reference max
-        // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 78 us
+        // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 77 us
         // with it and 51 without; the bytes of the second sum are what it costs
         // (moved by four other warps, or read, added and stored without red: no
         // less).
