@@ -685,11 +685,12 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 lsum = fmaf(ml[st].y, ml[st].y != 0.f ? fast_exp2(ml[st].x - M) : 0.f, lsum);
             const float fac = l_run[nt][j] != 0.f && lsum != 0.f ? fast_exp2(m_run[nt][j] - M) * (v_scale / lsum) : 0.f;
             if (h < G && warp < n_act) {
-                // a NaN sum (a NaN in a visible key or in q) goes on as a NaN output with
-                // a weight of its own: the reduce takes a sum that is not > 0 for an empty split
+                // a NaN sum (a NaN in a visible key or in q) goes on as a NaN output with a
+                // record of its own, max 0 and sum 1: the reduce takes a sum that is not > 0
+                // for an empty split, and the max of such a split may be infinite
                 if (warp == 0 && r == 0 && p.num_splits > 1)
                     p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + split] =
-                        make_float2(M, poisoned ? -1.f : lsum == lsum ? lsum : 1.f);
+                        poisoned ? make_float2(M, -1.f) : lsum == lsum ? make_float2(M, lsum) : make_float2(0.f, 1.f);
                 float *row = macc + (warp * G + h) * HS + 2 * r;
 #pragma unroll
                 for (int mt = 0; mt < NB; ++mt)

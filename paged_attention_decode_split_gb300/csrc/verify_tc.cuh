@@ -1556,9 +1556,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             }
         }
         if (live && !direct)
-            // (F4: a NaN sum goes on as a NaN row with a weight, which the reduce does not take for an empty split)
-            p.part_ml[orow * p.num_splits + split] =
-                make_float2(m_ref, poisoned ? -1.f : F4 && l_sum != l_sum ? 1.f : l_sum);
+            // (F4: a NaN sum goes on as a NaN row with max 0 and sum 1: the reduce takes a sum that is not > 0 for
+            // an empty split, and the max may be infinite)
+            p.part_ml[orow * p.num_splits + split] = poisoned                  ? make_float2(m_ref, -1.f)
+                                                     : F4 && l_sum != l_sum ? make_float2(0.f, 1.f)
+                                                                            : make_float2(m_ref, l_sum);
     }
 
     tc::fence_before();
