@@ -357,10 +357,13 @@ pa_status pa_gather_cache_fp4(const void *k_cache, const void *v_cache, const in
  * code * S in f16 (exact; q enters scaled by a power of two) with binary32 sums.
  * For fp32 outputs a softmax weight enters as an f16 head and an f16 residual,
  * and the sums are split so that they lose about 1e-6 of themselves at most; for
- * bf16 outputs it enters as one f16 (off by 2^-12 at most, twice in decode,
- * where it is multiplied by V's scale first).  Slots past a sequence's end or
- * before its window may hold any bytes.  A NaN in a visible row (a NaN scale)
- * or in q makes the outputs that depend on it NaN, and no others. */
+ * bf16 outputs it enters as one f16, off by half a step, 2^-11 of itself.  Both
+ * are relative to a reference 2^7 or more below the split's largest weight, so
+ * that either form is off by 2^-32 of that weight at most where f16 ends (bf16
+ * outputs: weights below 2^-21 of the largest).  V's scales take no part in it.
+ * Slots past a sequence's end or before its window may hold any bytes.  A NaN
+ * in a visible row (a NaN scale) or in q makes the outputs that depend on it
+ * NaN, and no others. */
 pa_status pa_paged_attention_decode_fp4(const void *q, const void *k_cache, const void *v_cache,
                                         const float *k_scale, const float *v_scale,
                                         const int32_t *block_table, const int32_t *seq_lens,

@@ -11,10 +11,13 @@
 // q enters as f16 scaled by a power of two per head (f16_prescale), P as an
 // f16 head plus an f16 residual (22 significant bits): what is rounded to
 // fewer than 32 bits is rounded below the sums' own error.  For bf16 outputs
-// the residual is left out and the V scales are multiplied to P rather than to
-// V: two roundings of a weight by 2^-12 each, together a quarter of the half
-// step that the output itself is rounded by, and the errors of many keys
-// average out.
+// the residual is left out: a weight is off by half a step of f16, 2^-11 of
+// itself, an eighth of the half step that the output is rounded by, and the
+// errors of many keys average out.  (Multiplying the V scales to P, which is
+// half as many multiplies, rounded a second time and lost small weights to
+// f16's end where the scales are small, for 1 % of the time.)  Either way a
+// weight is off by 2^-32 of the split's largest at most where it is smaller
+// than 2^-21 of it.
 //
 // Layout on sm_103a:
 //  * A chunk is two records (K, V) of 9 D contiguous bytes; a warp works on two
@@ -39,10 +42,11 @@
 // In the loop HBM and the instruction issue are about even (a chunk pair takes
 // 400 clocks either way); 8 warps of 230 registers measured faster than 10 or 12
 // of 168 (which spill) and than 16 of 128 whose pairs share the work on a chunk
-// and exchange P (32 x 1K-32K batch, 24 heads on 4, D = 256: 143 us, 4.4 TB/s of
-// records, against 163, 150 and 151).  Outside it a CTA spends 5 us on its page
-// table, first copies and merge, which bounds the short calls: 32K in one
-// sequence takes 16.5 us, 512 tokens with the append 9.2 us, both with the reduce.
+// and exchange P (32 x 1K-32K batch, 24 heads on 4, D = 256: 143 us against 163,
+// 150 and 151; 145 us, 4.3 TB/s of records, since the V scales meet V).  Outside
+// it a CTA spends 5 us on its page table, first copies and merge, which bounds
+// the short calls: 32K in one sequence takes 16.5 us, 512 tokens with the append
+// 9.2 us, both with the reduce.
 #pragma once
 
 #include "decode_mma.cuh"
@@ -126,12 +130,10 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     uint4 *q_frag = reinterpret_cast<uint4 *>(smem + C::OFF_Q);
     float *q_mul = reinterpret_cast<float *>(smem + C::OFF_QSC);
 
-    // The reference max of a head is kept kAbove over the largest score it was
-    // raised for, and raised again when a score passes it by kRaise.  With the
-    // residual it is kept below, so that P in f16, at most 2^15, holds weights
-    // down to 2^-32 of the largest (f16 ends at 2^-25); without, P is multiplied
-    // by the V scales (up to 448) in f16 and stays below 2^6.
-    constexpr float kAbove = RES ? -7.f : 2.f, kRaise = kLazyLog2 - kAbove;
+    // The reference max of a head is kept 2^7 below the largest score it was
+    // raised for, and raised again when a score passes it by kRaise: P in f16, at
+    // most 2^15, holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
+    constexpr float kBelow = 7.f, kRaise = kLazyLog2 + kBelow;
 
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
                     if (m > m_run[nt][j] + kRaise) {
-                        m += kAbove;
+                        m -= kBelow;
                         const float alpha = fast_exp2(m_run[nt][j] - m);  // 0 on the first pair
                         m_run[nt][j] = m;
                         l_run[nt][j] *= alpha;
@@ -556,36 +558,26 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                     fp4::e2m1x8_f16(((vw[0][w] >> 4) & LO) | (vw[1][w] & HI), a1);  // dims 16 blk + 2r + 1
                     fp4::e2m1x8_f16((vw[2][w] & LO) | ((vw[3][w] << 4) & HI), a2);  // tokens 8 + 2c, 9 + 2c
                     fp4::e2m1x8_f16(((vw[2][w] >> 4) & LO) | (vw[3][w] & HI), a3);
-                    if constexpr (RES) {
-                        // V = code * S (exact); four tiles' heads, then their residuals: no product waits for
-                        // the one before it
+                    // V = code * S (exact); four tiles' heads, then their residuals: no product waits for
+                    // the one before it
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            a0[q] = fp4::hmul2(a0[q], slo[q]);
-                            a1[q] = fp4::hmul2(a1[q], slo[q]);
-                            a2[q] = fp4::hmul2(a2[q], shi[q]);
-                            a3[q] = fp4::hmul2(a3[q], shi[q]);
-                        }
+                    for (int q = 0; q < 4; ++q) {
+                        a0[q] = fp4::hmul2(a0[q], slo[q]);
+                        a1[q] = fp4::hmul2(a1[q], slo[q]);
+                        a2[q] = fp4::hmul2(a2[q], shi[q]);
+                        a3[q] = fp4::hmul2(a3[q], shi[q]);
+                    }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bh[ch][nt][0], bh[ch][nt][1]);
-                            if constexpr (!PACK) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bl[ch][nt][0],
-                                                  bl[ch][nt][1]);
-                            }
-                        }
-                    } else {
-                        // the scales go to P instead (half the multiplies): P S rounds once more, by 2^-12
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int q = 0; q < 4; ++q)
+                            mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bh[ch][nt][0], bh[ch][nt][1]);
+                        if constexpr (RES && !PACK) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q],
-                                              fp4::hmul2(bh[ch][nt][0], slo[q]), fp4::hmul2(bh[ch][nt][1], shi[q]));
+                                mm::mma<true>(oacc[4 * w + q][nt], a0[q], a1[q], a2[q], a3[q], bl[ch][nt][0],
+                                              bl[ch][nt][1]);
+                        }
                     }
                 }
             }

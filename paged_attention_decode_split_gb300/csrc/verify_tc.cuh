@@ -322,8 +322,8 @@ struct VerifyTcCfg {
 // swizzle).
 // tm_k64: 5-D boxes of a whole K tile of TK keys (64, or 128 with TK = 128).
 // RES: the residual of P is multiplied too (F4 with bf16 output goes without:
-// a weight is then off by at most 2^-12, an eighth of the half step that the
-// output is rounded by).
+// a weight is then off by half a step of f16, 2^-11 of itself, an eighth of the
+// half step that the output is rounded by).
 // FAR: O is moved to a second sum every kVerifyFarTiles tiles (splits of more
 // tiles with fp32 output).  The tensor core cuts each addition to an accumulator
 // off towards zero: O loses 2.4e-9 of itself per key (measured; half a step,
