@@ -402,7 +402,7 @@ def _plain_tables(s):
     p = lens[r] + i - (end - new)[r]
     slot = table[r, (p // bs).clamp(max=width - 1)] * bs + p % bs
     slots = torch.where((i < end[-1]) & served[r], slot, -1)
-    left = n_free - torch.where(served, upto, 0).amax()
+    left = n_free - torch.where(served & (need > 0), upto, 0).amax()  # (upto counts refused requests' pages too)
     return dict(table=table.int(), lens=torch.where(served, lens + new, lens).int(), slots=slots, num_free=left.int(),
                 free=free.int())
 
