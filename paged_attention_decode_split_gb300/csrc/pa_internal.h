@@ -38,5 +38,8 @@ cudaError_t launch_verify_fp4(int head_dim, const VerifyParams &p, dim3 grid, cu
 
 // Sets the dynamic shared-memory limit of `fn` once per device.
 cudaError_t ensure_smem_limit(const void *fn, int bytes, int slot);
+// Whether `fn` is launched with at least `regs` registers per thread, asked
+// once per device (cudaErrorInvalidConfiguration if not).
+cudaError_t ensure_launch_regs(const void *fn, int regs, int slot);
 
 }  // namespace pa

@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "../../include/pagedattn.h"
+#include "device_once.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -286,18 +287,24 @@ pa_status check_workspace(const Plan &pl, void *workspace, size_t ws_bytes) {
 }  // namespace
 
 cudaError_t ensure_smem_limit(const void *fn, int bytes, int slot) {
-    static bool done[kMaxDevices][kKernelSlots] = {};
-    static std::mutex mu;
+    static DeviceOnce<kMaxDevices, kKernelSlots> once;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices || slot < 0 || slot >= kKernelSlots)
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[dev][slot]) return cudaSuccess;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done[dev][slot] = true;
-    return e;
+    return once.run(dev, slot,
+                    [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
+
+cudaError_t ensure_launch_regs(const void *fn, int regs, int slot) {
+    static DeviceOnce<kMaxDevices, kKernelSlots> once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return once.run(dev, slot, [&] {
+        cudaFuncAttributes attr;
+        const cudaError_t err = cudaFuncGetAttributes(&attr, fn);
+        return err != cudaSuccess ? err : attr.numRegs >= regs ? cudaSuccess : cudaErrorInvalidConfiguration;
+    });
 }
 
 // ---- reshape_and_cache kernel ------------------------------------------------

@@ -10,14 +10,11 @@ template <int D, int NK, int NV, int NSG, bool RES, bool FAR>
 cudaError_t launch_res(const VerifyParams &p, dim3 grid, cudaStream_t stream, int slot) {
     using C = VerifyTcCfg<D, NK, NV, NSG, 2, 64, true>;
     auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, 2, 64, true, RES, FAR>;
-    const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // the warpgroups' register shares draw on the launch's registers: with fewer, setmaxnreg would wait forever
-    static const bool enough = [&] {
-        cudaFuncAttributes attr;
-        return cudaFuncGetAttributes(&attr, kern) == cudaSuccess && attr.numRegs >= C::REGS_LAUNCH;
-    }();
-    if (!enough) return cudaErrorInvalidConfiguration;
+    e = ensure_launch_regs(reinterpret_cast<const void *>(kern), C::REGS_LAUNCH, slot);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(C::THREADS);
