@@ -396,7 +396,7 @@ pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, cons
  * lengths to the host and can be captured into a graph.  The pool of free pages
  * is a stack: free_pages[0 .. num_free) lists them.  A page belongs to one
  * request.  Inputs and outputs are separate buffers (PA_ERR_INVALID_ARG where
- * seq_lens or num_free_out is an input's address): a step hands the outputs of
+ * one that is written shares bytes with another): a step hands the outputs of
  * one call to the next, and a replayed call gives the same result again.
  *
  * Both calls write the block table, which PA_FLAG_EARLY_KV_READ reads ahead of

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kTabThreads) pa_release_block_tables_kernel(co
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-pa_status check_tables(const TableParams &p, const void *slots_needed) {
+pa_status check_tables(const TableParams &p, bool release, const void *slots_needed) {
     if (p.B < 0 || p.width < 0 || p.block_size < 1 || p.num_pages < 1 || p.num_tokens < 0) return PA_ERR_INVALID_ARG;
     if (p.num_pages > INT32_MAX || p.B > 65535) return PA_ERR_UNSUPPORTED;
     if ((int64_t)p.width * p.block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;  // lengths are 32-bit
@@ -468,9 +468,25 @@ pa_status check_tables(const TableParams &p, const void *slots_needed) {
     if (!aligned(p.lens, 4) || !aligned(p.count, 4) || !aligned(p.table, 4) || !aligned(p.free_pages, 4) ||
         !aligned(p.num_free, 4) || !aligned(p.lens_out, 4) || !aligned(p.num_free_out, 4) || !aligned(p.slots, 8))
         return PA_ERR_INVALID_ARG;
-    // every CTA reads the inputs while one writes these
-    if (p.num_free_out == p.num_free || (p.B > 0 && (p.lens_out == p.lens || p.lens_out == p.count)))
-        return PA_ERR_INVALID_ARG;
+    // every CTA reads the inputs while others write: no buffer that is written shares bytes with another
+    const struct {
+        const void *at;
+        int64_t bytes;
+        bool written;
+    } buf[] = {{p.lens, 4ll * p.B, false},
+               {p.count, 4ll * p.B, false},
+               {p.table, 4ll * p.B * p.width, !release},
+               {p.free_pages, 4 * p.num_pages, release},
+               {p.num_free, 4, false},
+               {p.lens_out, 4ll * p.B, true},
+               {p.slots, 8ll * p.num_tokens, true},
+               {p.num_free_out, 4, true}};
+    for (const auto &a : buf)
+        for (const auto &b : buf) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+            if (&a != &b && a.written && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes)
+                return PA_ERR_INVALID_ARG;
+        }
     return PA_OK;
 }
 
@@ -507,7 +523,7 @@ pa_status pa_extend_block_tables(const int32_t *context_lens, const int32_t *num
     TableParams p{context_lens, num_new, block_table, const_cast<int32_t *>(free_pages), num_free, seq_lens,
                   slot_mapping, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size,
                   num_tokens, 0};
-    const pa_status st = check_tables(p, num_tokens > 0 ? static_cast<const void *>(slot_mapping) : free_pages);
+    const pa_status st = check_tables(p, false, num_tokens > 0 ? static_cast<const void *>(slot_mapping) : free_pages);
     if (st != PA_OK) return st;
     if (num_seqs > kTabThreads)
         return launch_tables(pa_extend_block_tables_kernel, p, std::min(kMost, ctas_for(num_tokens, 4, kTabThreads)),
@@ -531,7 +547,7 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
                                   int32_t *seq_lens_out, int32_t *num_free_out, int32_t *device_status, void *stream) {
     const TableParams p{seq_lens, finished, const_cast<int32_t *>(block_table), free_pages, num_free, seq_lens_out,
                         nullptr, num_free_out, device_status, num_pages, num_seqs, max_pages_per_seq, block_size, 0, 0};
-    const pa_status st = check_tables(p, free_pages);
+    const pa_status st = check_tables(p, true, free_pages);
     if (st != PA_OK) return st;
     const int64_t items = (int64_t)num_seqs * max_pages_per_seq;
     const int T = num_seqs > 256 ? 512 : num_seqs > 128 ? 256 : 128;
