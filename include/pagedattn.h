@@ -399,10 +399,10 @@ pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, cons
  * one that is written shares bytes with another): a step hands the outputs of
  * one call to the next, and a replayed call gives the same result again.
  *
- * Both calls write the block table, which PA_FLAG_EARLY_KV_READ reads ahead of
- * the stream order: the attention calls of a step that runs them on the same
- * stream are given no such flag, unless work of another kind (not a kernel of
- * this library) lies between. */
+ * The calls write block tables and lengths, which PA_FLAG_EARLY_KV_READ reads
+ * ahead of the stream order: the attention calls of a step that runs them on
+ * the same stream are given no such flag, unless work of another kind (not a
+ * kernel of this library) lies between. */
 
 /* extend_block_tables -- request b holds context_lens[b] tokens and gets
  * num_new[b] more.  It takes the pages that context_lens[b] + num_new[b] tokens
@@ -411,11 +411,12 @@ pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, cons
  * free_pages[num_free - 1]), and they are entered in its block-table row.  The
  * new tokens are packed request by request (row i of k_new is the i-th of
  * them); slot_mapping[i] is token i's slot, -1 for i past the last one.
- * A request is refused -- seq_lens[b] = context_lens[b], slots -1, no pages --
- * if its lengths are negative or exceed max_pages_per_seq * block_size
- * (PA_DEV_BAD_SEQLEN), if the packed rows up to its last one exceed num_tokens
- * (PA_DEV_BAD_SLOT), or if the pages wanted by all requests up to and including
- * it exceed num_free (PA_DEV_NO_PAGES; it must want at least one itself).
+ * A request is refused -- seq_lens[b] = context_lens[b] (0 if that is
+ * negative), slots -1, no pages -- if its lengths are negative or exceed
+ * max_pages_per_seq * block_size (PA_DEV_BAD_SEQLEN), if the packed rows up to
+ * its last one exceed num_tokens (PA_DEV_BAD_SLOT), or if the pages wanted by
+ * all requests up to and including it exceed num_free (PA_DEV_NO_PAGES; it must
+ * want at least one itself).
  *   context_lens, num_new  device int32 [num_seqs]
  *   block_table            device int32 [num_seqs, max_pages_per_seq]; the entries of
  *                          the pages taken are written, the others left as they are
@@ -437,11 +438,12 @@ pa_status pa_extend_block_tables(const int32_t *context_lens, const int32_t *num
 /* release_block_tables -- the pages of every request with finished[b] != 0
  * (those of its seq_lens[b] tokens) go back to the pool, requests in order,
  * pages in order of position, above free_pages[num_free - 1];
- * seq_lens_out[b] = 0 for them and seq_lens[b] for the others.  The block
- * table is not written (entries of an empty request are never read).  A
- * request whose pages would not fit under num_pages keeps them
- * (PA_DEV_BAD_PAGE: more pages than the pool has; the same status reports an
- * entry outside [0, num_pages), which is returned as it is).
+ * seq_lens_out[b] = 0 for them and seq_lens[b] (0 if negative) for the others;
+ * a length that is negative or exceeds max_pages_per_seq * block_size stands
+ * for no pages (PA_DEV_BAD_SEQLEN).  The block table is not written (entries of
+ * an empty request are never read).  A request whose pages would not fit under
+ * num_pages keeps them (PA_DEV_BAD_PAGE: more pages than the pool has; the same
+ * status reports an entry outside [0, num_pages), which is returned as it is).
  *   free_pages  device int32 [num_pages], written from num_free on
  * Other arguments and limits as for pa_extend_block_tables. */
 pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,

@@ -18,10 +18,11 @@
 // of consecutive slots from one search, searching again only where a page or a
 // request ends: runs of two, which fill the GPU up to 311,000 tokens, and of
 // eight beyond that (a step of 32 single tokens: 3.0 us; 1M slots of 509
-// requests: 8.1 us against 9.7 with four slot pairs per search; release and
+// requests: 8.1-8.4 us against 9.7 with four slot pairs per search; release and
 // admission of 256 requests: 6.4 us in two calls).  CTAs of their own write the table
 // entries.  Beyond 512 requests the prefix is kept per group of requests and
-// the group is walked.
+// the group is walked: 1M slots of 1000 requests take 18.4 us (8.4 us for 509),
+// a step of one token each 7.2 us for 1000 requests and 317 for 65535.
 #include <algorithm>
 
 #include "pa_device.cuh"

@@ -22,9 +22,9 @@
 // Layout on sm_103a:
 //  * A chunk is two records (K, V) of 9 D contiguous bytes; a warp works on two
 //    chunks (32 tokens) at a time.  Every warp owns a ring of SPW stages of one
-//    chunk pair and fills it itself: lane k issues the copies of the warp's
-//    k-th pair up front, lane 0 refills a stage when the warp has read it.  No
-//    producer warp and no empty barriers; the first NW * SPW pairs of a split
+//    chunk pair and fills it itself: lanes 2 s and 2 s + 1 issue the copies of K
+//    and of V into stage s, up front and again whenever the warp has read it.
+//    No producer warp and no empty barriers; the first NW * SPW pairs of a split
 //    are in flight at once.  The chunks left after the last whole round of NW
 //    pairs are spread over the warps one by one.
 //  * Fragments come from shared memory by 16-byte loads at lane * 16 (the
@@ -39,14 +39,16 @@
 //  * Q^T's fragments stand in shared memory, one 16-byte load per two k-steps,
 //    used for both chunks; a pair's scales are widened to f16 once, into shared
 //    memory (each is used by four lanes of K, by eight of V).
-// In the loop HBM and the instruction issue are about even (a chunk pair takes
-// 400 clocks either way); 8 warps of 230 registers measured faster than 10 or 12
-// of 168 (which spill) and than 16 of 128 whose pairs share the work on a chunk
-// and exchange P (32 x 1K-32K batch, 24 heads on 4, D = 256: 143 us against 163,
-// 150 and 151; 145 us, 4.3 TB/s of records, since the V scales meet V).  Outside
-// it a CTA spends 5 us on its page table, first copies and merge, which bounds
-// the short calls: 32K in one sequence takes 16.5 us, 512 tokens with the append
-// 9.2 us, both with the reduce.
+// What bounds the loop is the chain of dependent instructions with two warps per
+// scheduler (8 x 20K-32K tokens: a warp issues every 4.3 clocks, 1.3 of them
+// fixed latencies, 0.5 waits for shared memory and copies; 47 % of the issue
+// slots and 44 % of the HBM's peak are used).  8 warps of 230 registers measured
+// faster all the same than 10 or 12 of 168 (which spill) and than 16 of 128 whose
+// pairs share the work on a chunk and exchange P (32 x 1K-32K batch, 24 heads on
+// 4, D = 256: 143 us against 163, 150 and 151; 145 us, 4.3 TB/s of records, since
+// the V scales meet V).  Outside the loop a CTA spends 5 us on its page table,
+// first copies and merge, which bounds the short calls: 32K in one sequence takes
+// 16.6 us, 512 tokens with the append 7.5 us, both with the reduce.
 #pragma once
 
 #include "decode_mma.cuh"

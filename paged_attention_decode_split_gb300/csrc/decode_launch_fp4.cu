@@ -47,6 +47,13 @@ cudaError_t launch_t(int group, const DecodeParams &p, dim3 grid, cudaStream_t s
 
 // One kernel per head_dim and 8-head n-tile count; the group and the window
 // are run-time values (they change a handful of instructions per chunk).
+// Warps x stages, D = 256: decode_fp4.cuh.  D = 128, up to 8 heads (32 heads on
+// 8, 16-token pages; 32 x 1K-32K with bf16 / fp32 output, one 32K sequence):
+// 12 x 3 195 / 231 / 15.7 us, 12 x 2 195 / 231 / 15.9, 8 x 4 249 / 275 / 16.2,
+// 10 x 4 224 / 264 / 16.9, 16 x 2 187 / 225 / 16.7: the single sequence decides
+// against 16.  Up to 16 heads (32 on 2; the sequence: 64 on 4): 8 x 4 69.6 /
+// 86.1 / 15.0, 8 x 3 70.1 / 85.2 / 15.1, 10 x 3 77.0 / 92.8 / 16.3, 12 x 3
+// 70.4 / 78.1 / 16.0.
 cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     if (head_dim == 256)
         return group <= 8 ? launch_t<256, 1, 8, 2>(group, p, grid, stream, 146)

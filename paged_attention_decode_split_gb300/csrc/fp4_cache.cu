@@ -12,10 +12,13 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // 16-dim block of a row of K and of V, NB lanes a row, so every value is loaded
 // and quantised once with 16-byte accesses; a row's code bytes go through
 // shared memory into (or out of) the order of the record, whose 16-byte pieces
-// then move with one access each.  Bytes bound the large calls, launch latency
-// the single token: 16411 tokens of 8 heads x 128 are written in 18.5 us (86 MB,
-// 4.6 TB/s) and read back in 17.8 us (4.8 TB/s), one token of 4 x 256 takes 1.8 us
-// each way.  With a byte per access they took 23.3 and 21.0 us.
+// then move with one access each.  16411 tokens of 8 heads x 128 are written in
+// 18.5 us (86 MB, 4.6 TB/s) and read back in 17.8 us (4.8 TB/s); one token of 4 x
+// 256 takes 1.7 us each way, a launch.  Beside the bytes, the instruction issue
+// bounds the write (77 % of the slots, the ALU 70 %: the quantiser and the
+// packing of bytes), the load/store path the read (the largest stalls; issue 62
+// %): the pieces of a row are 8 and 16 bytes, 32 and 64 bytes apart, the scales
+// single bytes.  With a byte per access the two took 23.3 and 21.0 us.
 template <int D>
 struct RowCfg {
     static constexpr int NB = D / 16;        // lanes per row

@@ -121,8 +121,6 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map) {
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 2^x with the hardware approximation instruction (ex2.approx, relative error
-// about 2^-22); exp2(-inf) = +0.
 // max(a, b, c) in one instruction (three-input max.f32, sm_100 family).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
@@ -130,6 +128,8 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
+// 2^x with the hardware approximation instruction (ex2.approx, relative error
+// about 2^-22); exp2(-inf) = +0.
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

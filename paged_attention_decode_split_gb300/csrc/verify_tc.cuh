@@ -329,6 +329,9 @@ struct VerifyTcCfg {
 // off towards zero: O loses 2.4e-9 of itself per key (measured; half a step,
 // 2^-24, for each of the eight products of a tile, on a sum that grows), 7e-7 in
 // 4 tiles -- what binary32 sums over a thousand keys are off by.
+// (8 x 16 rows over 8K, error against float64 and time: 4 tiles 9.4e-7 and 77 us,
+// 8 tiles 1.3e-6 and 64, 16 tiles 2.5e-6 and 57, none 51; a 32-bit product and
+// softmax in torch is off by 1.7e-6.  Four keeps below that at any length.)
 constexpr int kVerifyFarTiles = 4;
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
           bool FAR = false>
@@ -1111,9 +1114,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // of its own (a lane's float4 j at float4 j * live rows + lane: whole
         // lines per access), and is added to by red while the row's reference max
         // stays.  A kernel of its own: 8 sequences x 16 rows over 8K take 77 us
-        // with it and 51 without; the bytes of the second sum are what it costs
-        // (moved by four other warps, or read, added and stored without red: no
-        // less).
+        // with it and 51 without, 2048 rows over 16K 1344 us (701 with bf16 output);
+        // the bytes of the second sum are what it costs (moved by four other warps,
+        // or read, added and stored without red: no less).
         [[maybe_unused]] float m_far = -INFINITY;  // the reference max that the second sum stands for
         [[maybe_unused]] const uint32_t my_row =
             live ? (uint32_t)((((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split)
