@@ -59,7 +59,7 @@ typedef enum { PA_OUT_F32 = 0, PA_OUT_BF16 = 1 } pa_out_dtype;
 #define PA_DEV_BAD_PAGE 2    /* a block_table entry that is read lies outside [0, num_pages) */
 #define PA_DEV_BAD_SLOT 4    /* reshape_and_cache: slot >= num_pages * block_size */
 #define PA_DEV_TIMEOUT 8     /* a bounded wait inside a kernel gave up (never expected) */
-#define PA_DEV_NO_PAGES 16   /* extend_block_tables: the pool ran out before a request's new pages */
+#define PA_DEV_NO_PAGES 16   /* extend_block_tables, fork_block_tables: the pool ran out before a request's new pages */
 
 /* Shape and launch description of one attention call.
  *   num_seqs          B, number of sequences (>= 0; 0 is a no-op)
@@ -451,6 +451,209 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
                                   int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
                                   int32_t *seq_lens_out, int32_t *num_free_out, int32_t *device_status,
                                   void *stream);
+
+/* ---- pages that several requests hold ------------------------------------------
+ * Requests forked from a common prompt hold its full pages together:
+ * share_counts[p] is the number of holders of page p beyond the first, so a
+ * page of one request counts 0, pa_extend_block_tables (whose pages have one
+ * holder) needs no counts, and an array of zeros is what a pool starts with.
+ * Inputs and outputs are separate buffers (PA_ERR_INVALID_ARG where one that is
+ * written shares bytes with another), except for the block table and the stack
+ * of free pages, which are changed in place; a replayed call gives the same
+ * result again.  PA_FLAG_EARLY_KV_READ: as for the block tables above, and for
+ * pages that pa_copy_cache_pages writes. */
+
+/* fork_block_tables -- request b with parent[b] = a >= 0 becomes a child of
+ * request a: its block-table row begins with a's full pages (each gets one more
+ * holder), and where a's last page is only partly filled, the child gets a page
+ * of its own from the top of the stack, children in order, to which the caller
+ * copies those tokens:
+ *     copy_src[b], copy_dst[b], copy_tokens[b] = a's last page, the new page,
+ *         seq_lens[a] % block_size            (-1, -1, 0 where nothing is copied)
+ * as pa_copy_cache_pages takes them; seq_lens_out[b] = seq_lens[a].  Requests
+ * with parent[b] < 0 are left as they are.  A child is refused -- seq_lens_out[b]
+ * = seq_lens[b] (0 if negative), no pages -- if a is out of range or itself a
+ * child in this call, if request b still holds tokens (seq_lens[b] != 0), or if
+ * a's length is negative or exceeds max_pages_per_seq * block_size
+ * (PA_DEV_BAD_SEQLEN); or if the pages wanted by the children up to and
+ * including it exceed num_free (PA_DEV_NO_PAGES; it must want one itself).
+ *   seq_lens, parent   device int32 [num_seqs]
+ *   block_table        device int32 [num_seqs, max_pages_per_seq]; the children's
+ *                      entries are written, the others left as they are
+ *   free_pages         device int32 [num_pages], read; an entry outside [0, num_pages)
+ *                      sets PA_DEV_BAD_PAGE and is entered as it is, as is a
+ *                      parent's (which gets no holder)
+ *   num_free           device int32 [1]; outside [0, num_pages]: clamped, PA_DEV_BAD_PAGE
+ *   share_counts       device int32 [num_pages]
+ *   seq_lens_out, copy_src, copy_dst, copy_tokens   device int32 [num_seqs], out
+ *   share_counts_out   device int32 [num_pages], out (all of it)
+ *   num_free_out       device int32 [1], out
+ * num_seqs <= 65535, max_pages_per_seq * block_size < 2^31 (PA_ERR_UNSUPPORTED). */
+pa_status pa_fork_block_tables(const int32_t *seq_lens, const int32_t *parent, int32_t *block_table,
+                               const int32_t *free_pages, const int32_t *num_free, const int32_t *share_counts,
+                               int32_t num_seqs, int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
+                               int32_t *seq_lens_out, int32_t *share_counts_out, int32_t *copy_src, int32_t *copy_dst,
+                               int32_t *copy_tokens, int32_t *num_free_out, int32_t *device_status, void *stream);
+
+/* release_shared_block_tables -- pa_release_block_tables for pages with several
+ * holders: every request with finished[b] != 0 lets go of the pages of its
+ * seq_lens[b] tokens, and those that nobody holds any more go back to the pool,
+ * in ascending order of the page, above free_pages[num_free - 1] (the order does
+ * not tell who held them).  A page let go of more often than it was held is
+ * returned once (PA_DEV_BAD_PAGE); an entry outside [0, num_pages) is skipped
+ * (PA_DEV_BAD_PAGE), as are pages past the end of the pool.  A length that is
+ * negative or exceeds max_pages_per_seq * block_size stands for no pages
+ * (PA_DEV_BAD_SEQLEN).  Arguments and limits as for pa_release_block_tables and
+ * pa_fork_block_tables. */
+pa_status pa_release_shared_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,
+                                         int32_t *free_pages, const int32_t *num_free, const int32_t *share_counts,
+                                         int32_t num_seqs, int32_t max_pages_per_seq, int32_t block_size,
+                                         int64_t num_pages, int32_t *seq_lens_out, int32_t *share_counts_out,
+                                         int32_t *num_free_out, int32_t *device_status, void *stream);
+
+/* compact_block_tables -- moves pages in use to the low end of the pool, so
+ * that its high end can be given back or used otherwise.  A page is in use if
+ * it is not on the list of free pages.  With n of them, those at n and above move
+ * into free pages below n, the highest into the lowest, at most max_moves:
+ *     copy_src[k], copy_dst[k]  the k-th move, as pa_copy_cache_pages takes
+ *                               them (-1 past the last)
+ *     page_map[p]               where the contents of page p are from now on
+ * The block tables (the entries of the pages that hold seq_lens[b] tokens) and
+ * the share counts follow; a holder of pages outside the tables follows by
+ * page_map.  free_pages_out lists the free pages, the lowest on top (-1 past
+ * num_free_out); extent = 1 + the highest page in use.  Copies of a call do not
+ * depend on each other's order.
+ *   seq_lens          device int32 [num_seqs]; negative or too long:
+ *                     PA_DEV_BAD_SEQLEN, the row is left as it is
+ *   block_table       device int32 [num_seqs, max_pages_per_seq], rewritten in place
+ *   free_pages, num_free, share_counts   as for pa_fork_block_tables; a free
+ *                     page that is listed twice counts once
+ *   free_pages_out, share_counts_out, page_map   device int32 [num_pages], out
+ *   copy_src, copy_dst   device int32 [max_moves], out
+ *   num_free_out, extent device int32 [1], out
+ * Limits as for pa_fork_block_tables. */
+pa_status pa_compact_block_tables(const int32_t *seq_lens, int32_t *block_table, const int32_t *free_pages,
+                                  const int32_t *num_free, const int32_t *share_counts, int32_t num_seqs,
+                                  int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages, int32_t max_moves,
+                                  int32_t *free_pages_out, int32_t *num_free_out, int32_t *share_counts_out,
+                                  int32_t *page_map, int32_t *copy_src, int32_t *copy_dst, int32_t *extent,
+                                  int32_t *device_status, void *stream);
+
+/* Caches that one pa_copy_cache_pages call takes. */
+#define PA_MAX_COPY_CACHES 128
+
+/* copy_cache_pages -- page copy_dst[i] = page copy_src[i] in every one of the
+ * caches (K and V of all layers in one call, say), bit for bit.  A pair with a
+ * negative page is skipped; one with a page >= num_pages sets PA_DEV_BAD_PAGE
+ * and is skipped.  With copy_tokens, only the 16-token chunks that hold the
+ * first copy_tokens[i] tokens are copied, the rest of the page is left as it is
+ * (outside [0, block_size]: PA_DEV_BAD_SEQLEN, skipped).  The destinations are
+ * distinct and none is another pair's source.
+ *   caches          host array of num_caches device pointers, 16-byte aligned
+ *   copy_src,
+ *   copy_dst        device int32 [num_pairs];  copy_tokens likewise, or NULL
+ *   parts_per_page,
+ *   chunk_bytes     a page is parts_per_page parts of block_size / 16 chunks of
+ *                   chunk_bytes (16 tokens):
+ *                       bf16, e4m3:  1, 16 * num_kv_heads * head_dim * (2 or 1)
+ *                       fp4:         num_kv_heads, 9 * head_dim
+ * num_caches <= PA_MAX_COPY_CACHES, block_size and chunk_bytes multiples of 16
+ * (PA_ERR_UNSUPPORTED otherwise). */
+pa_status pa_copy_cache_pages(void *const *caches, int32_t num_caches, const int32_t *copy_src,
+                              const int32_t *copy_dst, const int32_t *copy_tokens, int32_t num_pairs,
+                              int32_t parts_per_page, int64_t chunk_bytes, int32_t block_size, int64_t num_pages,
+                              int32_t *device_status, void *stream);
+
+/* ---- rotary positions ----------------------------------------------------------
+ * The rows that attention and the caches take carry their positions as
+ * rotations: of the first rotary_dim = R dims of a head, pair j = 0 .. R/2 - 1,
+ * (a, b) = dims (j, j + R/2), or (2 j, 2 j + 1) with PA_ROPE_INTERLEAVED, becomes
+ *     ((a cos t - b sin t) * factor, (b cos t + a sin t) * factor),
+ *     t = (position + position_offset) * w_j,
+ * in binary32, rounded once; the other dims are copied.  w_j is given as a
+ * fraction of a turn in 64-bit fixed point, so that t is exact modulo whole
+ * turns at any position (its error is 2^-24 of half a turn at most). */
+
+typedef enum {
+    PA_ROPE_SCALE_NONE = 0,
+    PA_ROPE_SCALE_LINEAR = 1, /* w / factor */
+    PA_ROPE_SCALE_NTK = 2,    /* base * factor^(R / (R - 2)) */
+    PA_ROPE_SCALE_YARN = 3,   /* w / factor for the slow pairs, w for the fast ones, a ramp over the pair's number between */
+    PA_ROPE_SCALE_BANDS = 4   /* the same with a ramp over the turns that a pair makes */
+} pa_rope_scale;
+
+/* How the frequencies w_j = base^(-2 j / R) are scaled for contexts longer than
+ * the original_len positions that a model was trained on.  By turns (yarn,
+ * bands): a pair that turns high_turns times or more over original_len
+ * positions is left as it is, one that turns low_turns times or less is
+ * stretched by the factor (1 and 32 are usual for yarn, 1 and 4 for bands). */
+typedef struct {
+    int32_t rotary_dim; /* R, even, >= 2 */
+    int32_t kind;       /* pa_rope_scale */
+    int32_t original_len;
+    double base;        /* > 1 */
+    double factor;      /* >= 1 */
+    double low_turns, high_turns;
+} pa_rotary_scaling;
+
+/* rotary_frequencies -- freqs[j] = w_j / 2 pi * 2^64 (host, [R / 2]) and the
+ * factor on the rotated rows (0.1 ln(factor) + 1 for yarn, else 1).  Host only. */
+pa_status pa_rotary_frequencies(const pa_rotary_scaling *scaling, int64_t *freqs, float *factor);
+
+#define PA_ROPE_INTERLEAVED 1 /* pairs (2 j, 2 j + 1) instead of (j, j + R / 2) */
+#define PA_ROPE_INVERSE 2     /* rotate back: the gradient of a rotation, or its undoing (pa_rotary only) */
+
+/* One rotary call: num_tokens rows of num_q_heads (and num_kv_heads) heads of
+ * head_dim; heads are dense, rows are *_stride elements apart (a multiple of
+ * 8), so that q, k and v may be read in place from one projection's rows. */
+typedef struct {
+    int32_t num_tokens;
+    int32_t num_q_heads;
+    int32_t num_kv_heads;
+    int32_t head_dim;    /* a multiple of 16, 32 .. 1024 */
+    int32_t rotary_dim;  /* R <= head_dim, a multiple of 16 */
+    int32_t flags;       /* PA_ROPE_* */
+    int32_t position_offset;
+    float factor;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+} pa_rotary_desc;
+
+/* rotary -- q_out = rotated q, k_out = rotated k.  An output may be its own
+ * input (the same pointer and stride); apart from that what is written shares
+ * no byte with another argument (PA_ERR_INVALID_ARG).  num_kv_heads may be 0 (k
+ * and k_out are not used then).
+ *   q, q_out     device bf16 [num_tokens, num_q_heads, head_dim]
+ *   k, k_out     device bf16 [num_tokens, num_kv_heads, head_dim]
+ *   positions    device int32 [num_tokens], any values
+ *   freqs        device int64 [rotary_dim / 2] */
+pa_status pa_rotary(const void *q, const void *k, const int32_t *positions, const int64_t *freqs, void *q_out,
+                    void *k_out, const pa_rotary_desc *desc, void *stream);
+
+/* rotary_and_cache -- rotary of q and k, and reshape_and_cache of the rotated k
+ * (rounded to bf16) and of v, in one kernel: q_out and the caches equal, bit for
+ * bit, those of pa_rotary followed by pa_reshape_and_cache (its slot rules; q of a
+ * padding token is rotated all the same).  With a new token per request,
+ * positions = seq_lens and position_offset = -1 need no array of their own.
+ *   v            device bf16 [num_tokens, num_kv_heads, head_dim]
+ *   other arguments as for pa_rotary and pa_reshape_and_cache */
+pa_status pa_rotary_and_cache(const void *q, const void *k, const void *v, const int32_t *positions,
+                              const int64_t *freqs, void *q_out, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, const pa_rotary_desc *desc, int32_t block_size,
+                              int64_t num_pages, int32_t *device_status, void *stream);
+
+/* The same into an e4m3 cache (as pa_reshape_and_cache_fp8) and into an fp4 cache
+ * (as pa_reshape_and_cache_fp4: head_dim 128 or 256, distinct slots; and
+ * num_kv_heads * head_dim <= 10240). */
+pa_status pa_rotary_and_cache_fp8(const void *q, const void *k, const void *v, const int32_t *positions,
+                                  const int64_t *freqs, void *q_out, void *k_cache, void *v_cache,
+                                  const int64_t *slot_mapping, const float *k_scale, const float *v_scale,
+                                  const pa_rotary_desc *desc, int32_t block_size, int64_t num_pages,
+                                  int32_t *device_status, void *stream);
+pa_status pa_rotary_and_cache_fp4(const void *q, const void *k, const void *v, const int32_t *positions,
+                                  const int64_t *freqs, void *q_out, void *k_cache, void *v_cache,
+                                  const int64_t *slot_mapping, const float *k_scale, const float *v_scale,
+                                  const pa_rotary_desc *desc, int32_t block_size, int64_t num_pages,
+                                  int32_t *device_status, void *stream);
 
 /* Size of the scratch array that pa_paged_attention_decode_noalloc keeps in
  * device memory (8 MiB per GPU that loads the library, held until exit). */

@@ -14,7 +14,10 @@ Names follow the C ABI: ``reshape_and_cache``, ``paged_attention_decode``,
 ``paged_attention_decode_append``, ``paged_attention_verify``,
 ``workspace_bytes``, ``last_plan``; ``_fp8`` and ``_fp4`` forms for quantised
 caches, ``gather_cache_fp4``, ``extend_block_tables``,
-``release_block_tables``.
+``release_block_tables``; ``fork_block_tables``,
+``release_shared_block_tables``, ``compact_block_tables`` and
+``copy_cache_pages`` for pages with several holders; ``rotary``,
+``rotary_and_cache`` and ``rotary_frequencies``.
 """
 from __future__ import annotations
 
@@ -33,7 +36,10 @@ __all__ = [
     "PA_PATH_VERIFY_TCGEN05", "PA_FLAG_EARLY_KV_READ", "PA_NOALLOC_SCRATCH_BYTES", "paged_attention_decode_noalloc",
     "fp4_cache_shape", "reshape_and_cache_fp4", "gather_cache_fp4", "paged_attention_decode_fp4",
     "paged_attention_decode_append_fp4", "paged_attention_verify_fp4", "extend_block_tables",
-    "release_block_tables", "PA_DEV_NO_PAGES",
+    "release_block_tables", "PA_DEV_NO_PAGES", "RotaryScaling", "rotary_frequencies", "rotary", "rotary_and_cache",
+    "rotary_and_cache_fp8", "rotary_and_cache_fp4", "fork_block_tables", "release_shared_block_tables",
+    "compact_block_tables", "copy_cache_pages", "copy_cache_pages_fp4", "PA_ROPE_INTERLEAVED", "PA_ROPE_INVERSE",
+    "PA_MAX_COPY_CACHES",
 ]
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, 1, 2, 3, 4
@@ -42,6 +48,9 @@ PA_DEV_BAD_SEQLEN, PA_DEV_BAD_PAGE, PA_DEV_BAD_SLOT, PA_DEV_TIMEOUT, PA_DEV_NO_P
 PA_PATH_DECODE_CUDA_CORE, PA_PATH_DECODE_MMA, PA_PATH_VERIFY_TCGEN05 = 1, 2, 3
 PA_FLAG_EARLY_KV_READ = 1
 PA_NOALLOC_SCRATCH_BYTES = 8 << 20
+PA_MAX_COPY_CACHES = 128
+PA_ROPE_INTERLEAVED, PA_ROPE_INVERSE = 1, 2
+_ROPE_SCALES = ("none", "linear", "ntk", "yarn", "bands")
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libpagedattn.so")
@@ -67,6 +76,14 @@ class PlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32), ("kind", ctypes.c_int32), ("original_len", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low_turns", ctypes.c_double),
+        ("high_turns", ctypes.c_double),
+    ]
+
+
 class PagedAttnError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)}")
@@ -85,7 +102,9 @@ _BOUND_ENTRIES = ("pa_paged_attention_decode", "pa_paged_attention_verify", "pa_
                   "pa_paged_attention_decode_append_fp8", "pa_paged_attention_decode_noalloc", "pa_reshape_and_cache",
                   "pa_reshape_and_cache_fp8", "pa_reshape_and_cache_fp4", "pa_gather_cache_fp4",
                   "pa_paged_attention_decode_fp4", "pa_paged_attention_decode_append_fp4",
-                  "pa_paged_attention_verify_fp4", "pa_extend_block_tables", "pa_release_block_tables")
+                  "pa_paged_attention_verify_fp4", "pa_extend_block_tables", "pa_release_block_tables", "pa_rotary",
+                  "pa_rotary_and_cache", "pa_rotary_and_cache_fp8", "pa_rotary_and_cache_fp4", "pa_fork_block_tables",
+                  "pa_release_shared_block_tables", "pa_compact_block_tables", "pa_copy_cache_pages")
 
 
 def _load_binding(lib):
@@ -145,6 +164,26 @@ def load_library(path: str | None = None):
                                                + [_vp] * 5)
         lib.pa_release_block_tables.restype = ctypes.c_int
         lib.pa_release_block_tables.argtypes = [_vp] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_int64] + [_vp] * 4
+        lib.pa_rotary_frequencies.restype = ctypes.c_int
+        lib.pa_rotary_frequencies.argtypes = [ctypes.POINTER(RotaryScaling), _vp, ctypes.POINTER(ctypes.c_float)]
+        lib.pa_rotary.restype = ctypes.c_int
+        lib.pa_rotary.argtypes = [_vp] * 8
+        lib.pa_rotary_and_cache.restype = ctypes.c_int
+        lib.pa_rotary_and_cache.argtypes = [_vp] * 10 + [ctypes.c_int32, ctypes.c_int64, _vp, _vp]
+        for name in ("pa_rotary_and_cache_fp8", "pa_rotary_and_cache_fp4"):
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = [_vp] * 12 + [ctypes.c_int32, ctypes.c_int64, _vp, _vp]
+        lib.pa_fork_block_tables.restype = ctypes.c_int
+        lib.pa_fork_block_tables.argtypes = [_vp] * 6 + [ctypes.c_int32] * 3 + [ctypes.c_int64] + [_vp] * 8
+        lib.pa_release_shared_block_tables.restype = ctypes.c_int
+        lib.pa_release_shared_block_tables.argtypes = [_vp] * 6 + [ctypes.c_int32] * 3 + [ctypes.c_int64] + [_vp] * 5
+        lib.pa_compact_block_tables.restype = ctypes.c_int
+        lib.pa_compact_block_tables.argtypes = ([_vp] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_int64, ctypes.c_int32]
+                                                + [_vp] * 9)
+        lib.pa_copy_cache_pages.restype = ctypes.c_int
+        lib.pa_copy_cache_pages.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32,
+                                            ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _vp, _vp]
         for name in ("pa_paged_attention_decode_fp8", "pa_paged_attention_verify_fp8",
                      "pa_paged_attention_decode_fp4", "pa_paged_attention_verify_fp4"):
             fn = getattr(lib, name)
@@ -361,6 +400,117 @@ def release_block_tables(seq_lens, finished, block_table, free_pages, num_free, 
     (free_pages is written from num_free on) and set their lengths to 0."""
     _check(_bound().release_tables(seq_lens, finished, block_table, free_pages, num_free, block_size, seq_lens_out,
                                    num_free_out, status, _stream(stream)), "pa_release_block_tables")
+
+
+def fork_block_tables(seq_lens, parent, block_table, free_pages, num_free, share_counts, block_size: int, seq_lens_out,
+                      share_counts_out, copy_src, copy_dst, copy_tokens, num_free_out, status=None, stream=None) -> None:
+    """Request b with parent[b] >= 0 becomes a child of that request: it holds
+    the parent's full pages with it and gets a page for the partly filled last
+    one, listed in copy_src, copy_dst and copy_tokens (out, [B]) for
+    copy_cache_pages.  All int32; share_counts and share_counts_out [P]: holders
+    of a page beyond the first."""
+    _check(_bound().fork_tables(seq_lens, parent, block_table, free_pages, num_free, share_counts, block_size,
+                                seq_lens_out, share_counts_out, copy_src, copy_dst, copy_tokens, num_free_out, status,
+                                _stream(stream)), "pa_fork_block_tables")
+
+
+def release_shared_block_tables(seq_lens, finished, block_table, free_pages, num_free, share_counts, block_size: int,
+                                seq_lens_out, share_counts_out, num_free_out, status=None, stream=None) -> None:
+    """release_block_tables for pages with several holders: a page goes back to
+    the pool with its last one, in ascending order of the page."""
+    _check(_bound().release_shared(seq_lens, finished, block_table, free_pages, num_free, share_counts, block_size,
+                                   seq_lens_out, share_counts_out, num_free_out, status, _stream(stream)),
+           "pa_release_shared_block_tables")
+
+
+def compact_block_tables(seq_lens, block_table, free_pages, num_free, share_counts, block_size: int, free_pages_out,
+                         num_free_out, share_counts_out, page_map, copy_src, copy_dst, extent, status=None,
+                         stream=None) -> None:
+    """Move the highest pages in use into the lowest free ones, at most
+    len(copy_src) of them: block_table is rewritten in place, page_map [P] says
+    where every page is from now on, copy_src and copy_dst list the moves for
+    copy_cache_pages, extent [1] = 1 + the highest page in use."""
+    _check(_bound().compact_tables(seq_lens, block_table, free_pages, num_free, share_counts, block_size,
+                                   free_pages_out, num_free_out, share_counts_out, page_map, copy_src, copy_dst,
+                                   extent, status, _stream(stream)), "pa_compact_block_tables")
+
+
+def copy_cache_pages(caches, copy_src, copy_dst, copy_tokens=None, status=None, stream=None) -> None:
+    """Copy page copy_src[i] to page copy_dst[i] in every cache of the list
+    (bf16 or e4m3, one shape [P, BS, Hkv, D]); with copy_tokens, the 16-token
+    chunks of the first copy_tokens[i] tokens.  Negative pages are skipped."""
+    _check(_bound().copy_pages(False, list(caches), copy_src, copy_dst, copy_tokens, status, _stream(stream)),
+           "pa_copy_cache_pages")
+
+
+def copy_cache_pages_fp4(caches, copy_src, copy_dst, copy_tokens=None, status=None, stream=None) -> None:
+    """copy_cache_pages for fp4 caches (uint8 tensors of fp4_cache_shape)."""
+    _check(_bound().copy_pages(True, list(caches), copy_src, copy_dst, copy_tokens, status, _stream(stream)),
+           "pa_copy_cache_pages")
+
+
+def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_len: int = 0, low_turns: float = 1.0, high_turns: float | None = None,
+                       device="cuda") -> tuple:
+    """The frequency table of rotary (int64 [rotary_dim / 2], fractions of a turn
+    per position in 2^-64) and the factor on the rotated rows.  scaling: none,
+    linear, ntk, yarn or bands (by default up to 32 or 4 turns over
+    original_len positions are left alone)."""
+    import torch
+    if scaling not in _ROPE_SCALES:
+        raise ValueError(f"scaling: {scaling!r}; expected one of {', '.join(_ROPE_SCALES)}")
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim: an even number is required")
+    if high_turns is None:
+        high_turns = 4.0 if scaling == "bands" else 32.0
+    desc = RotaryScaling(rotary_dim, _ROPE_SCALES.index(scaling), original_len, base, factor, low_turns, high_turns)
+    freqs = torch.empty(rotary_dim // 2, dtype=torch.int64)
+    rows = ctypes.c_float()
+    _check(load_library().pa_rotary_frequencies(ctypes.byref(desc), freqs.data_ptr(), ctypes.byref(rows)),
+           "pa_rotary_frequencies")
+    return freqs.to(device), rows.value
+
+
+def rotary(q, k, positions, freqs, q_out, k_out, *, interleaved: bool = False, inverse: bool = False,
+           factor: float = 1.0, position_offset: int = 0, stream=None) -> None:
+    """Rotate the first 2 * len(freqs) dims of the heads of q and k (bf16
+    [N, heads, D], rows any multiple of 8 elements apart; k and k_out may be
+    None) by their positions (int32 [N]); inverse rotates back, which is the
+    gradient.  An output may be its own input."""
+    flags = (PA_ROPE_INTERLEAVED if interleaved else 0) | (PA_ROPE_INVERSE if inverse else 0)
+    _check(_bound().rotary(q, k, positions, freqs, q_out, k_out, flags, factor, position_offset, _stream(stream)),
+           "pa_rotary")
+
+
+def _rotary_and_cache(kind, q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                      interleaved, factor, position_offset, status, stream, what):
+    _check(_bound().rotary_and_cache(kind, q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale,
+                                     v_scale, PA_ROPE_INTERLEAVED if interleaved else 0, factor, position_offset,
+                                     status, _stream(stream)), what)
+
+
+def rotary_and_cache(q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, *, interleaved: bool = False,
+                     factor: float = 1.0, position_offset: int = 0, status=None, stream=None) -> None:
+    """rotary of q and k and reshape_and_cache of the rotated k and of v in one
+    kernel, the same result as the two calls."""
+    _rotary_and_cache(0, q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, None, None, interleaved,
+                      factor, position_offset, status, stream, "pa_rotary_and_cache")
+
+
+def rotary_and_cache_fp8(q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale, v_scale, *,
+                         interleaved: bool = False, factor: float = 1.0, position_offset: int = 0, status=None,
+                         stream=None) -> None:
+    """rotary and reshape_and_cache_fp8 in one kernel."""
+    _rotary_and_cache(1, q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                      interleaved, factor, position_offset, status, stream, "pa_rotary_and_cache_fp8")
+
+
+def rotary_and_cache_fp4(q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale, v_scale, *,
+                         interleaved: bool = False, factor: float = 1.0, position_offset: int = 0, status=None,
+                         stream=None) -> None:
+    """rotary and reshape_and_cache_fp4 in one kernel."""
+    _rotary_and_cache(2, q, k, v, positions, freqs, q_out, k_cache, v_cache, slot_mapping, k_scale, v_scale,
+                      interleaved, factor, position_offset, status, stream, "pa_rotary_and_cache_fp4")
 
 
 def last_plan() -> dict:
