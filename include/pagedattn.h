@@ -135,6 +135,7 @@ typedef struct {
 #define PA_PATH_DECODE_CUDA_CORE 1  /* retired: split-KV decode on the CUDA cores (no longer reported) */
 #define PA_PATH_DECODE_MMA 2        /* split-KV decode, both products on the tensor cores (mma.sync) */
 #define PA_PATH_VERIFY_TCGEN05 3    /* multi-row verify, tcgen05 + TMEM */
+#define PA_PATH_DECODE_SHARED 4     /* decode over shared prefixes: both of them, and the merge */
 
 /* Bytes of device workspace an attention call with this description needs
  * (split partials: out vectors, max and sum per split).  0 when the plan does
@@ -451,6 +452,81 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
                                   int32_t max_pages_per_seq, int32_t block_size, int64_t num_pages,
                                   int32_t *seq_lens_out, int32_t *num_free_out, int32_t *device_status,
                                   void *stream);
+
+/* ---- decode over shared prefixes ------------------------------------------------
+ * Sequences that begin with the same tokens (samples of one prompt, requests
+ * behind one system prompt) hold the same pages for them.  A plain decode reads
+ * those pages once per sequence; these calls read them once per group.  The
+ * groups' common part runs on the tensor cores with a row per sequence and head
+ * (as verify's rows share every K/V tile), the sequences' own parts as in
+ * decode, and one merge joins both. */
+
+/* The groups of a call: group g is the sequences group_starts[g] ..
+ * group_starts[g + 1] - 1, next to one another in the batch.
+ *   num_groups      1 .. 65535
+ *   max_group_seqs  host-side upper bound of a group's sequences (a larger one:
+ *                   PA_DEV_BAD_SEQLEN, zero rows for those past it)
+ *   max_prefix_len,
+ *   max_suffix_len  about the longest prefix and the most tokens that a sequence
+ *                   has beyond it: they plan the splits and bound nothing; 0 =
+ *                   max_seq_len of the description
+ *   prefix_splits   0 = automatic; > 0 forces the splits of the prefixes (the
+ *                   description's num_splits those of the own parts) */
+typedef struct {
+    int32_t num_groups;
+    int32_t max_group_seqs;
+    int32_t max_prefix_len;
+    int32_t max_suffix_len;
+    int32_t prefix_splits;
+} pa_prefix_desc;
+
+/* Bytes of device workspace that a shared-prefix decode needs (never 0 for a
+ * batch that is not empty); (size_t)-1 if the description is invalid.  Host
+ * only; what pa_workspace_bytes says of the workspace holds here too. */
+size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc *prefix);
+
+/* paged_attention_decode_shared -- the result of pa_paged_attention_decode (up
+ * to rounding), where the first prefix_lens[b] tokens of sequence b, rounded down
+ * to a multiple of 16, stand in the pages of its group's first sequence that is
+ * not idle: for tokens t below that, its row of the block table is read, and the
+ * other sequences' entries are not.  prefix_lens[b] is the same throughout a
+ * group, and at most seq_lens[b] (a group without a common part has 0; any length
+ * serves, also one that ends inside a page).  seq_lens[b] == 0 is an idle sequence:
+ * a zero row whatever its prefix_lens says.  A sequence whose length is out of
+ * range, or whose prefix_lens is negative, longer than it or not its group's, is
+ * PA_DEV_BAD_SEQLEN and a zero row, as is one that no group has; group_starts
+ * that do not ascend give zero rows throughout (PA_DEV_BAD_SEQLEN).  A NaN in q or
+ * in a visible key makes the outputs that depend on it NaN, and no others.
+ * PA_FLAG_EARLY_KV_READ is accepted and changes nothing; a window is refused
+ * (PA_ERR_UNSUPPORTED).
+ *   group_starts  device int32 [num_groups + 1], 0 .. num_seqs ascending
+ *   prefix_lens   device int32 [num_seqs]
+ *   workspace     device, >= pa_shared_workspace_bytes(desc, prefix) bytes
+ * Other arguments, results and errors as for pa_paged_attention_decode; head
+ * layouts and head_dim as there. */
+pa_status pa_paged_attention_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                                           const int32_t *block_table, const int32_t *seq_lens,
+                                           const int32_t *group_starts, const int32_t *prefix_lens,
+                                           const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                           void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                           void *stream);
+
+/* The same over an e4m3 cache (K and V as for pa_paged_attention_decode_fp8) and
+ * over an fp4 cache (as for pa_paged_attention_decode_fp4). */
+pa_status pa_paged_attention_decode_shared_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                               const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const int32_t *group_starts, const int32_t *prefix_lens,
+                                               const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                               void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                               void *stream);
+pa_status pa_paged_attention_decode_shared_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                               const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const int32_t *group_starts, const int32_t *prefix_lens,
+                                               const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                               void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                               void *stream);
 
 /* ---- pages that several requests hold ------------------------------------------
  * Requests forked from a common prompt hold its full pages together:

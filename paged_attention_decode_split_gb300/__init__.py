@@ -39,13 +39,14 @@ __all__ = [
     "release_block_tables", "PA_DEV_NO_PAGES", "RotaryScaling", "rotary_frequencies", "rotary", "rotary_and_cache",
     "rotary_and_cache_fp8", "rotary_and_cache_fp4", "fork_block_tables", "release_shared_block_tables",
     "compact_block_tables", "copy_cache_pages", "copy_cache_pages_fp4", "PA_ROPE_INTERLEAVED", "PA_ROPE_INVERSE",
-    "PA_MAX_COPY_CACHES",
+    "PA_MAX_COPY_CACHES", "PrefixDesc", "make_prefix", "shared_workspace_bytes", "paged_attention_decode_shared",
+    "paged_attention_decode_shared_fp8", "paged_attention_decode_shared_fp4", "PA_PATH_DECODE_SHARED",
 ]
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, 1, 2, 3, 4
 PA_OUT_F32, PA_OUT_BF16 = 0, 1
 PA_DEV_BAD_SEQLEN, PA_DEV_BAD_PAGE, PA_DEV_BAD_SLOT, PA_DEV_TIMEOUT, PA_DEV_NO_PAGES = 1, 2, 4, 8, 16
-PA_PATH_DECODE_CUDA_CORE, PA_PATH_DECODE_MMA, PA_PATH_VERIFY_TCGEN05 = 1, 2, 3
+PA_PATH_DECODE_CUDA_CORE, PA_PATH_DECODE_MMA, PA_PATH_VERIFY_TCGEN05, PA_PATH_DECODE_SHARED = 1, 2, 3, 4
 PA_FLAG_EARLY_KV_READ = 1
 PA_NOALLOC_SCRATCH_BYTES = 8 << 20
 PA_MAX_COPY_CACHES = 128
@@ -76,6 +77,11 @@ class PlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class PrefixDesc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("num_groups", "max_group_seqs", "max_prefix_len", "max_suffix_len",
+                                                    "prefix_splits")]
+
+
 class RotaryScaling(ctypes.Structure):
     _fields_ = [
         ("rotary_dim", ctypes.c_int32), ("kind", ctypes.c_int32), ("original_len", ctypes.c_int32),
@@ -104,7 +110,9 @@ _BOUND_ENTRIES = ("pa_paged_attention_decode", "pa_paged_attention_verify", "pa_
                   "pa_paged_attention_decode_fp4", "pa_paged_attention_decode_append_fp4",
                   "pa_paged_attention_verify_fp4", "pa_extend_block_tables", "pa_release_block_tables", "pa_rotary",
                   "pa_rotary_and_cache", "pa_rotary_and_cache_fp8", "pa_rotary_and_cache_fp4", "pa_fork_block_tables",
-                  "pa_release_shared_block_tables", "pa_compact_block_tables", "pa_copy_cache_pages")
+                  "pa_release_shared_block_tables", "pa_compact_block_tables", "pa_copy_cache_pages",
+                  "pa_paged_attention_decode_shared", "pa_paged_attention_decode_shared_fp8",
+                  "pa_paged_attention_decode_shared_fp4")
 
 
 def _load_binding(lib):
@@ -164,6 +172,16 @@ def load_library(path: str | None = None):
                                                + [_vp] * 5)
         lib.pa_release_block_tables.restype = ctypes.c_int
         lib.pa_release_block_tables.argtypes = [_vp] * 5 + [ctypes.c_int32] * 3 + [ctypes.c_int64] + [_vp] * 4
+        lib.pa_shared_workspace_bytes.restype = ctypes.c_size_t
+        lib.pa_shared_workspace_bytes.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(PrefixDesc)]
+        lib.pa_paged_attention_decode_shared.restype = ctypes.c_int
+        lib.pa_paged_attention_decode_shared.argtypes = [_vp] * 7 + [ctypes.POINTER(AttnDesc), ctypes.POINTER(PrefixDesc),
+                                                                     _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        for name in ("pa_paged_attention_decode_shared_fp8", "pa_paged_attention_decode_shared_fp4"):
+            fn = getattr(lib, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnDesc), ctypes.POINTER(PrefixDesc), _vp, _vp, ctypes.c_size_t,
+                                       _vp, _vp]
         lib.pa_rotary_frequencies.restype = ctypes.c_int
         lib.pa_rotary_frequencies.argtypes = [ctypes.POINTER(RotaryScaling), _vp, ctypes.POINTER(ctypes.c_float)]
         lib.pa_rotary.restype = ctypes.c_int
@@ -229,6 +247,20 @@ def workspace_bytes(desc: AttnDesc) -> int:
     return int(n)
 
 
+def make_prefix(*, num_groups: int, max_group_seqs: int, max_prefix_len: int = 0, max_suffix_len: int = 0,
+                prefix_splits: int = 0) -> PrefixDesc:
+    """The groups of a decode over shared prefixes: their number, a bound of a
+    group's sequences, and about how long prefixes and own parts get."""
+    return PrefixDesc(num_groups, max_group_seqs, max_prefix_len, max_suffix_len, prefix_splits)
+
+
+def shared_workspace_bytes(desc: AttnDesc, prefix: PrefixDesc) -> int:
+    n = load_library().pa_shared_workspace_bytes(ctypes.byref(desc), ctypes.byref(prefix))
+    if n == ctypes.c_size_t(-1).value:
+        raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_shared_workspace_bytes")
+    return int(n)
+
+
 def hybrid_page_tokens(state_page_bytes: int, attn_bytes_per_token: int, alignment_tokens: int) -> int:
     """Page length (tokens) shared by a hybrid model's attention and state caches."""
     n = load_library().pa_hybrid_page_tokens(state_page_bytes, attn_bytes_per_token, alignment_tokens)
@@ -254,7 +286,7 @@ def _check(status: int, what: str) -> None:
 
 # Call kinds of the compiled binding's attention(); each maps to one C entry point.
 (_DECODE, _DECODE_APPEND, _VERIFY, _DECODE_FP8, _DECODE_APPEND_FP8, _VERIFY_FP8, _DECODE_NOALLOC, _DECODE_FP4,
- _DECODE_APPEND_FP4, _VERIFY_FP4) = range(10)
+ _DECODE_APPEND_FP4, _VERIFY_FP4, _SHARED, _SHARED_FP8, _SHARED_FP4) = range(13)
 
 
 def _bound():
@@ -382,6 +414,34 @@ def paged_attention_verify_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     _check(_bound().attention(_VERIFY_FP4, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
                               ctypes.addressof(desc), out, workspace, status, _stream(stream)),
            "pa_paged_attention_verify_fp4")
+
+
+def paged_attention_decode_shared(q, k_cache, v_cache, block_table, seq_lens, group_starts, prefix_lens, desc: AttnDesc,
+                                  prefix: PrefixDesc, out, workspace, status=None, stream=None) -> None:
+    """paged_attention_decode where the sequences of a group (int32 group_starts
+    [groups + 1]) hold the pages of their first prefix_lens tokens (int32 [B],
+    the same throughout a group) together: those are read once per group."""
+    _check(_bound().attention(_SHARED, q, k_cache, v_cache, None, None, None, None, block_table, seq_lens,
+                              ctypes.addressof(desc), out, workspace, status, _stream(stream), group_starts, prefix_lens,
+                              ctypes.addressof(prefix)), "pa_paged_attention_decode_shared")
+
+
+def paged_attention_decode_shared_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, group_starts,
+                                      prefix_lens, desc: AttnDesc, prefix: PrefixDesc, out, workspace, status=None,
+                                      stream=None) -> None:
+    """Decode over shared prefixes in an e4m3 cache."""
+    _check(_bound().attention(_SHARED_FP8, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
+                              ctypes.addressof(desc), out, workspace, status, _stream(stream), group_starts, prefix_lens,
+                              ctypes.addressof(prefix)), "pa_paged_attention_decode_shared_fp8")
+
+
+def paged_attention_decode_shared_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, group_starts,
+                                      prefix_lens, desc: AttnDesc, prefix: PrefixDesc, out, workspace, status=None,
+                                      stream=None) -> None:
+    """Decode over shared prefixes in an fp4 cache."""
+    _check(_bound().attention(_SHARED_FP4, q, k_cache, v_cache, k_scale, v_scale, None, None, block_table, seq_lens,
+                              ctypes.addressof(desc), out, workspace, status, _stream(stream), group_starts, prefix_lens,
+                              ctypes.addressof(prefix)), "pa_paged_attention_decode_shared_fp4")
 
 
 def extend_block_tables(context_lens, num_new, block_table, free_pages, num_free, block_size: int, seq_lens,

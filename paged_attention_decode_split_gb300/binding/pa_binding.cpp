@@ -54,6 +54,13 @@ using ExtendFn = pa_status (*)(const int32_t *, const int32_t *, int32_t *, cons
 using ReleaseFn = pa_status (*)(const int32_t *, const int32_t *, const int32_t *, int32_t *, const int32_t *, int32_t,
                                 int32_t, int32_t, int64_t, int32_t *, int32_t *, int32_t *, void *);
 
+using SharedFn = pa_status (*)(const void *, const void *, const void *, const int32_t *, const int32_t *,
+                               const int32_t *, const int32_t *, const pa_attn_desc *, const pa_prefix_desc *, void *,
+                               void *, size_t, int32_t *, void *);
+using SharedQuantFn = pa_status (*)(const void *, const void *, const void *, const float *, const float *,
+                                    const int32_t *, const int32_t *, const int32_t *, const int32_t *,
+                                    const pa_attn_desc *, const pa_prefix_desc *, void *, void *, size_t, int32_t *,
+                                    void *);
 using RotaryFn = pa_status (*)(const void *, const void *, const int32_t *, const int64_t *, void *, void *,
                                const pa_rotary_desc *, void *);
 using RotaryCacheFn = pa_status (*)(const void *, const void *, const void *, const int32_t *, const int64_t *, void *,
@@ -88,6 +95,8 @@ struct Entries {
     GatherFn gather_fp4 = nullptr;
     ExtendFn extend_tables = nullptr;
     ReleaseFn release_tables = nullptr;
+    SharedFn shared = nullptr;
+    SharedQuantFn shared_fp8 = nullptr, shared_fp4 = nullptr;
     RotaryFn rotary = nullptr;
     RotaryCacheFn rotary_and_cache = nullptr;
     RotaryQuantFn rotary_and_cache_fp8 = nullptr, rotary_and_cache_fp4 = nullptr;
@@ -117,6 +126,9 @@ void set_entry(const std::string &name, int64_t addr) {
     else if (name == "pa_gather_cache_fp4") g_entries.gather_fp4 = reinterpret_cast<GatherFn>(p);
     else if (name == "pa_extend_block_tables") g_entries.extend_tables = reinterpret_cast<ExtendFn>(p);
     else if (name == "pa_release_block_tables") g_entries.release_tables = reinterpret_cast<ReleaseFn>(p);
+    else if (name == "pa_paged_attention_decode_shared") g_entries.shared = reinterpret_cast<SharedFn>(p);
+    else if (name == "pa_paged_attention_decode_shared_fp8") g_entries.shared_fp8 = reinterpret_cast<SharedQuantFn>(p);
+    else if (name == "pa_paged_attention_decode_shared_fp4") g_entries.shared_fp4 = reinterpret_cast<SharedQuantFn>(p);
     else if (name == "pa_rotary") g_entries.rotary = reinterpret_cast<RotaryFn>(p);
     else if (name == "pa_rotary_and_cache") g_entries.rotary_and_cache = reinterpret_cast<RotaryCacheFn>(p);
     else if (name == "pa_rotary_and_cache_fp8") g_entries.rotary_and_cache_fp8 = reinterpret_cast<RotaryQuantFn>(p);
@@ -164,7 +176,7 @@ T *ptr_of(const optional<Tensor> &t) {
 
 enum Kind {
     kDecode = 0, kDecodeAppend, kVerify, kDecodeFp8, kDecodeAppendFp8, kVerifyFp8, kDecodeNoAlloc, kDecodeFp4,
-    kDecodeAppendFp4, kVerifyFp4
+    kDecodeAppendFp4, kVerifyFp4, kShared, kSharedFp8, kSharedFp4
 };
 
 // One attention call of the given kind (the C entry point it maps to is in the
@@ -173,11 +185,14 @@ int64_t attention(int64_t kind, const Tensor &q, const Tensor &k_cache, const Te
                   const optional<Tensor> &k_scale, const optional<Tensor> &v_scale, const optional<Tensor> &k_new,
                   const optional<Tensor> &v_new, const Tensor &block_table, const Tensor &seq_lens,
                   int64_t desc_addr, const Tensor &out, const optional<Tensor> &workspace,
-                  const optional<Tensor> &status, int64_t stream) {
+                  const optional<Tensor> &status, int64_t stream, const optional<Tensor> &group_starts = {},
+                  const optional<Tensor> &prefix_lens = {}, int64_t prefix_addr = 0) {
     TORCH_CHECK_VALUE(desc_addr != 0, "desc: a description is required");
     const pa_attn_desc *d = reinterpret_cast<const pa_attn_desc *>(desc_addr);
-    const bool fp8 = kind == kDecodeFp8 || kind == kDecodeAppendFp8 || kind == kVerifyFp8;
-    const bool fp4 = kind == kDecodeFp4 || kind == kDecodeAppendFp4 || kind == kVerifyFp4;
+    const bool fp8 = kind == kDecodeFp8 || kind == kDecodeAppendFp8 || kind == kVerifyFp8 || kind == kSharedFp8;
+    const bool fp4 = kind == kDecodeFp4 || kind == kDecodeAppendFp4 || kind == kVerifyFp4 || kind == kSharedFp4;
+    const bool shared = kind == kShared || kind == kSharedFp8 || kind == kSharedFp4;
+    const pa_prefix_desc *x = reinterpret_cast<const pa_prefix_desc *>(prefix_addr);
     const bool append = kind == kDecodeAppend || kind == kDecodeAppendFp8 || kind == kDecodeAppendFp4;
     const int64_t rows = static_cast<int64_t>(d->num_seqs) * d->q_len;
     const std::array<int64_t, 3> row_shape{rows, d->num_q_heads, d->head_dim};
@@ -209,6 +224,14 @@ int64_t attention(int64_t kind, const Tensor &q, const Tensor &k_cache, const Te
         expect(*k_new, "k_new", k_new->scalar_type() == at::kBFloat16, "bfloat16", new_shape);
         expect(*v_new, "v_new", v_new->scalar_type() == at::kBFloat16, "bfloat16", new_shape);
     }
+    if (shared) {
+        TORCH_CHECK_VALUE(x != nullptr, "prefix: a description is required");
+        TORCH_CHECK_VALUE(group_starts.has_value() && prefix_lens.has_value(), "group_starts, prefix_lens: both are required");
+        expect(*group_starts, "group_starts", group_starts->scalar_type() == at::kInt, "int32",
+               std::array<int64_t, 1>{int64_t(x->num_groups) + 1});
+        expect(*prefix_lens, "prefix_lens", prefix_lens->scalar_type() == at::kInt, "int32",
+               std::array<int64_t, 1>{d->num_seqs});
+    }
     size_t ws_bytes = 0;
     if (workspace.has_value()) ws_bytes = workspace->numel() * workspace->element_size();
     if (status.has_value())
@@ -216,7 +239,8 @@ int64_t attention(int64_t kind, const Tensor &q, const Tensor &k_cache, const Te
                {}, false);
     placed({{&q, "q"}, {&k_cache, "k_cache"}, {&v_cache, "v_cache"}, {&block_table, "block_table"},
             {&seq_lens, "seq_lens"}, {&out, "out"}, {opt(k_scale), "k_scale"}, {opt(v_scale), "v_scale"},
-            {opt(k_new), "k_new"}, {opt(v_new), "v_new"}, {opt(workspace), "workspace"}, {opt(status), "status"}});
+            {opt(k_new), "k_new"}, {opt(v_new), "v_new"}, {opt(workspace), "workspace"}, {opt(status), "status"},
+            {opt(group_starts), "group_starts"}, {opt(prefix_lens), "prefix_lens"}});
 
     const void *qp = q.data_ptr();
     void *kc = k_cache.data_ptr(), *vc = v_cache.data_ptr(), *op = out.data_ptr(), *wp = ptr_of<void>(workspace);
@@ -256,6 +280,16 @@ int64_t attention(int64_t kind, const Tensor &q, const Tensor &k_cache, const Te
         case kDecodeNoAlloc:
             TORCH_CHECK(g_entries.decode_noalloc, "entry point not set");
             return g_entries.decode_noalloc(qp, kc, vc, bt, sl, d, op, st, s);
+    }
+    if (shared) {
+        const int32_t *gs = group_starts->data_ptr<int32_t>(), *pl = prefix_lens->data_ptr<int32_t>();
+        if (kind == kShared) {
+            TORCH_CHECK(g_entries.shared, "entry point not set");
+            return g_entries.shared(qp, kc, vc, bt, sl, gs, pl, d, x, op, wp, ws_bytes, st, s);
+        }
+        const SharedQuantFn fn = fp4 ? g_entries.shared_fp4 : g_entries.shared_fp8;
+        TORCH_CHECK(fn, "entry point not set");
+        return fn(qp, kc, vc, ks, vs, bt, sl, gs, pl, d, x, op, wp, ws_bytes, st, s);
     }
     TORCH_CHECK_VALUE(false, "unknown call kind ", kind);
     return PA_ERR_INVALID_ARG;
@@ -682,7 +716,11 @@ int64_t rotary_and_cache(int64_t kind, const Tensor &q, const Tensor &k, const T
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.def("set_entry", &set_entry);
-    m.def("attention", &attention);
+    m.def("attention", &attention, py::arg("kind"), py::arg("q"), py::arg("k_cache"), py::arg("v_cache"),
+          py::arg("k_scale"), py::arg("v_scale"), py::arg("k_new"), py::arg("v_new"), py::arg("block_table"),
+          py::arg("seq_lens"), py::arg("desc"), py::arg("out"), py::arg("workspace"), py::arg("status"),
+          py::arg("stream"), py::arg("group_starts") = py::none(), py::arg("prefix_lens") = py::none(),
+          py::arg("prefix") = 0);
     m.def("reshape", &reshape);
     m.def("reshape_fp4", &reshape_fp4);
     m.def("gather_fp4", &gather_fp4);

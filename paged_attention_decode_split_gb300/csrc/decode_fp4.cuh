@@ -119,7 +119,8 @@ __device__ __forceinline__ void append_new_row_fp4(const DecodeParams &p, int b,
 // FAR: the accumulators are moved to a second sum every kFp4FarPairs of a
 // warp's pairs (splits that give a warp kFp4FarMin pairs or more, fp32 output).
 constexpr int kFp4FarPairs = 8, kFp4FarMin = 12;
-template <int D, int NT, int NW, int SPW, bool RES, bool PACK, bool FAR>
+// SH: the own part of a decode over shared prefixes (decode_mma.cuh).
+template <int D, int NT, int NW, int SPW, bool RES, bool PACK, bool FAR, bool SH = false>
 __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeParams p, const Fp4Params fp) {
     using C = Fp4DecodeCfg<D, NT, NW, SPW>;
     constexpr int NB = C::NB, HS = C::HS, GMAX = C::GMAX, REC = C::REC;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     // Every global access waits for the work before this call, except that
     // early_kv lets the block table, seq_lens and the chunks wholly before the
     // new row go first.
-    if (!p.early_kv) pdl_wait_primary();
+    if (!SH && !p.early_kv) pdl_wait_primary();
 
     // Q^T as B fragments, in f16: n-tile nt, k-step ks -> dims 16 ks + 4c (+1)
     // and 16 ks + 4c + 2 (+3) of head 8 nt + r; warp nt lays its tile out.  Its
@@ -175,8 +176,18 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     if (!p.early_kv) load_q();
 
     int L = p.seq_lens[b];
-    int c_begin = split * p.chunks_per_split;
-    if (p.window > 0) {  // (a branch: without a window the table's loads do not wait for the length)
+    const int record = SH ? p.prefix_splits + split : split;  // of the row's num_splits
+    int cps = p.chunks_per_split;
+    int c_begin = split * cps;
+    [[maybe_unused]] bool own_ok = true;  // SH: the lengths make sense, and a prefix CTA has this sequence
+    if constexpr (SH) {
+        const bool len_ok = L >= 0 && L <= p.max_seq_len;  // (flagged below)
+        const Suffix x = suffix_of(p, b, len_ok ? L : 0);
+        own_ok = len_ok && x.ok;
+        cps = x.per;
+        c_begin = x.first + split * cps;
+    }
+    if (!SH && p.window > 0) {  // (a branch: without a window the table's loads do not wait for the length)
         if (L > p.window && L <= p.max_seq_len) c_begin += (L - p.window) / kChunk;
     }
     auto page_of_chunk = [&](int chunk, int &in_page) {
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     const int32_t *bt = p.block_table + (size_t)b * p.max_pages_per_seq;
     int unused;
     const int lp_first = page_of_chunk(c_begin, unused);
-    const int lp_last = min(page_of_chunk(c_begin + p.chunks_per_split - 1, unused), p.max_pages_per_seq - 1);
+    const int lp_last = min(page_of_chunk(c_begin + cps - 1, unused), p.max_pages_per_seq - 1);
     const int n_pt = lp_last - lp_first + 1;
     const bool staged = n_pt <= kPageTab;
     if (staged)
@@ -201,17 +212,28 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         L = 0;
     }
     const int n_chunks = (L + kChunk - 1) / kChunk;
-    const int n_my = min(n_chunks - c_begin, p.chunks_per_split);
+    int n_my = min(n_chunks - c_begin, cps);
+    if constexpr (SH) {
+        if (!own_ok) {
+            n_my = 0;
+            if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+        }
+        if (split == 0 && !prefix_covers(p, b, C::THREADS)) {
+            own_ok = false;
+            if (threadIdx.x == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+            poison_prefix_records(p, b, hq0, G, C::THREADS);
+        }
+    }
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
         // l = 0); an unsplit call owns its output rows and zeroes them
-        if (p.early_kv) pdl_wait_primary();
+        if (p.early_kv || SH) pdl_wait_primary();
         if (p.num_splits == 1) {
             for (int idx = threadIdx.x; idx < G * D; idx += C::THREADS)
                 store_out(p.out, ((size_t)b * p.num_q_heads + hq0) * D + idx, 0.f, p.out_bf16);
         } else if (threadIdx.x < G) {
-            p.part_ml[((size_t)b * p.num_q_heads + hq0 + threadIdx.x) * p.num_splits + split] =
-                make_float2(-INFINITY, 0.f);
+            p.part_ml[((size_t)b * p.num_q_heads + hq0 + threadIdx.x) * p.num_splits + record] =
+                make_float2(-INFINITY, own_ok ? 0.f : -1.f);
         }
         return;
     }
@@ -358,7 +380,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         // visible tokens [lead, nv) of the pair (the second half of a single chunk's stage holds stale bytes)
         const bool two = k < rounds || warp < twos;
         const int nv = min((two ? 2 : 1) * kChunk, L - t_pair);
-        const int lead = p.window > 0 ? max(0, L - p.window - t_pair) : 0;
+        const int lead = !SH && p.window > 0 ? max(0, L - p.window - t_pair) : 0;
         const bool partial = nv < 2 * kChunk || lead > 0;  // warp-uniform
 
         // ---- the pair's scales to f16, once (each is used by 4 lanes of K, by 8 of V) ----
@@ -660,7 +682,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 merge_ml[warp * GMAX + nt * 8 + 2 * c + j] = make_float2(m_run[nt][j], l_run[nt][j]);
     }
     __syncthreads();  // every chunk is consumed: the stages become the merge area
-    const bool poisoned = flags[0] != 0 || flags[1] != 0;
+    const bool poisoned = flags[0] != 0 || flags[1] != 0 || (SH && !own_ok);
     const int n_act = min(NW, n_my);  // warps that had a chunk
     float *macc = reinterpret_cast<float *>(smem);  // [NW][G][HS]
 #pragma unroll
@@ -683,7 +705,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 // record of its own, max 0 and sum 1: the reduce takes a sum that is not > 0
                 // for an empty split, and the max of such a split may be infinite
                 if (warp == 0 && r == 0 && p.num_splits > 1)
-                    p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + split] =
+                    p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + record] =
                         poisoned ? make_float2(M, -1.f) : lsum == lsum ? make_float2(M, lsum) : make_float2(0.f, 1.f);
                 float *row = macc + (warp * G + h) * HS + 2 * r;
 #pragma unroll
@@ -710,8 +732,9 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         if (p.num_splits == 1)
             store_out4(p.out, row * D + d, o, p.out_bf16);
         else
-            *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + split) * D + d) = o;
+            *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + record) * D + d) = o;
     }
+    if constexpr (SH) pdl_wait_primary();
 }
 
 }  // namespace pa

@@ -1,0 +1,13 @@
+// decode_launch_shared.cu -- the bf16 decode instantiations for the own
+// parts of sequences with a shared prefix, in a translation unit of their own so
+// they compile in parallel with the rest.
+#include "decode_launch.cuh"
+
+namespace pa {
+
+cudaError_t launch_decode_shared(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                 const DecodeParams &p, dim3 grid, cudaStream_t stream) {
+    return launch_decode_cfg<false, false, true>(head_dim, group, tk, tv, p, grid, stream);
+}
+
+}  // namespace pa

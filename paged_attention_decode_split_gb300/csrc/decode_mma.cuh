@@ -184,7 +184,11 @@ __device__ __forceinline__ void append_new_row(const DecodeParams &p, int b, int
 
 // PF: chunks of old context a CTA prefetches into L2, beyond its stages, ahead
 // of the dependency wait (PA_FLAG_EARLY_KV_READ).
-template <int D, int G, int NT, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, int PF = 0>
+// SH: the own part of a decode over shared prefixes (DecodeParams).  The kernel
+// in front of it is the prefix kernel, which lets it start once the work before
+// both has finished: it need not wait for its stream dependency before it reads,
+// and waits at its end, so that whoever waits for it has waited for both.
+template <int D, int G, int NT, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, int PF = 0, bool SH = false>
 __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
     pa_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const DecodeParams p) {
@@ -222,16 +226,26 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
-    if (!p.early_kv) pdl_wait_primary();
+    if (!SH && !p.early_kv) pdl_wait_primary();
 
     int L = p.seq_lens[b];
-    int c_begin = split * p.chunks_per_split;
+    const int record = SH ? p.prefix_splits + split : split;  // of the row's num_splits
+    int cps = p.chunks_per_split;
+    int c_begin = split * cps;
+    [[maybe_unused]] bool own_ok = true;  // SH: the lengths make sense, and a prefix CTA has this sequence
+    if constexpr (SH) {
+        const bool len_ok = L >= 0 && L <= p.max_seq_len;  // (flagged below)
+        const Suffix x = suffix_of(p, b, len_ok ? L : 0);
+        own_ok = len_ok && x.ok;
+        cps = x.per;
+        c_begin = x.first + split * cps;
+    }
     if constexpr (WIN) {
         if (L > p.window && L <= p.max_seq_len) c_begin += (L - p.window) / kChunk;
     }
     const int32_t *bt = p.block_table + (size_t)b * p.max_pages_per_seq;
     const int lp_first = (c_begin * kChunk) / p.block_size;
-    const int lp_last = min(((c_begin + p.chunks_per_split) * kChunk - 1) / p.block_size, p.max_pages_per_seq - 1);
+    const int lp_last = min(((c_begin + cps) * kChunk - 1) / p.block_size, p.max_pages_per_seq - 1);
     const int n_pt = lp_last - lp_first + 1;
     const bool staged = n_pt <= kPageTab;
     if (staged)
@@ -241,17 +255,28 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
         L = 0;
     }
     const int n_chunks = (L + kChunk - 1) / kChunk;
-    const int n_my = min(n_chunks - c_begin, p.chunks_per_split);
+    int n_my = min(n_chunks - c_begin, cps);
+    if constexpr (SH) {
+        if (!own_ok) {
+            n_my = 0;
+            if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+        }
+        if (split == 0 && !prefix_covers(p, b, C::THREADS)) {
+            own_ok = false;
+            if (threadIdx.x == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+            poison_prefix_records(p, b, hq0, G, C::THREADS);
+        }
+    }
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
         // l = 0); an unsplit call owns its output rows and zeroes them
-        if (p.early_kv) pdl_wait_primary();
+        if (p.early_kv || SH) pdl_wait_primary();
         if (p.num_splits == 1) {
             for (int idx = threadIdx.x; idx < G * D; idx += C::THREADS)
                 store_out(p.out, ((size_t)b * p.num_q_heads + hq0) * D + idx, 0.f, p.out_bf16);
         } else if (threadIdx.x < G) {
-            p.part_ml[((size_t)b * p.num_q_heads + hq0 + threadIdx.x) * p.num_splits + split] =
-                make_float2(-INFINITY, 0.f);
+            p.part_ml[((size_t)b * p.num_q_heads + hq0 + threadIdx.x) * p.num_splits + record] =
+                make_float2(-INFINITY, own_ok ? 0.f : -1.f);
         }
         return;
     }
@@ -643,7 +668,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
     // ---- CTA merge of the streams' states (log-sum-exp weights) ----
     named_bar_sync(1, NWC * 32);  // every chunk is consumed: the stages become the merge area
     const bool aborted = flags[0] != 0;
-    const bool poisoned = aborted || flags[1] != 0;
+    const bool poisoned = aborted || flags[1] != 0 || (SH && !own_ok);
     float *macc = reinterpret_cast<float *>(smem);  // [NST][G][HS], unnormalised sums
 #pragma unroll
     for (int mt = 0; mt < MTW; ++mt) {
@@ -677,18 +702,26 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
         float M = -INFINITY;
         for (int st = 0; st < NST; ++st) M = fmaxf(M, merge_ml[st * GMAX + h].x);
         float lsum = 0.f;
+        [[maybe_unused]] bool sum_nan = false;
         for (int st = 0; st < NST; ++st) {
             const float2 ml = merge_ml[st * GMAX + h];
+            if constexpr (SH) sum_nan |= ml.y != ml.y;
             const float e = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;  // 0 for a stream without chunks
             merge_w[st * GMAX + h] = e;
             lsum = fmaf(ml.y, e, lsum);
         }
         const bool zero = poisoned || !(lsum > 0.f);
         const float norm = zero ? 0.f : (F8 ? p.v_scale[kvh] / lsum : 1.f / lsum);
-        for (int st = 0; st < NST; ++st) merge_w[st * GMAX + h] *= norm;
+        if (SH && sum_nan) {
+            // a NaN (in q or in a visible key) goes on as a NaN row with max 0 and sum 1: the reduce takes a sum
+            // that is not > 0 for an empty split
+            for (int st = 0; st < NST; ++st) merge_w[st * GMAX + h] = NAN;
+        } else {
+            for (int st = 0; st < NST; ++st) merge_w[st * GMAX + h] *= norm;
+        }
         if (p.num_splits > 1)
-            p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + split] =
-                make_float2(M, poisoned ? -1.f : lsum);
+            p.part_ml[((size_t)b * p.num_q_heads + hq0 + h) * p.num_splits + record] =
+                poisoned ? make_float2(M, -1.f) : SH && sum_nan ? make_float2(0.f, 1.f) : make_float2(M, lsum);
     }
     named_bar_sync(1, NWC * 32);
     for (int idx = threadIdx.x; idx < G * D / 4; idx += NWC * 32) {
@@ -710,9 +743,10 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
             store_out(p.out, row * D + d + 2, o.z, p.out_bf16);
             store_out(p.out, row * D + d + 3, o.w, p.out_bf16);
         } else {
-            *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + split) * D + d) = o;
+            *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + record) * D + d) = o;
         }
     }
+    if constexpr (SH) pdl_wait_primary();
 }
 
 }  // namespace pa

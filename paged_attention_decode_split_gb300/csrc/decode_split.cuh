@@ -18,6 +18,10 @@
 namespace pa {
 
 constexpr int kChunk = 16;    // tokens per TMA copy and per pipeline stage
+// 64 tokens: at 1K tokens, 16 splits of 4 chunks take 5.12 us per hybrid call
+// against 5.63 us for 32 of 2 (500 tokens: 5.00 against 5.04 us); from 2K up
+// and for the dense shape the plan is the same either way
+constexpr int kMinChunksPerSplit = 4;
 constexpr int kPageTab = 512;  // block-table entries a CTA stages in shared memory
 constexpr float kLazyLog2 = 8.f;  // a head's reference max is raised only when it grows by more than 2^8
 
@@ -49,7 +53,55 @@ struct DecodeParams {
     const __nv_bfloat16 *v_new;
     uint8_t *k_cache;
     uint8_t *v_cache;
+    // Decode over shared prefixes (SH kernels): sequence b attends here to the
+    // tokens from prefix_lens[b], rounded down to whole chunks, on, cut into
+    // suffix_splits splits of its own length; their records stand behind the
+    // prefix_splits records of the prefix kernel.
+    const int32_t *prefix_lens;   // [B]
+    const int32_t *group_starts;  // [num_groups + 1]
+    int num_groups;
+    int prefix_splits;
+    int suffix_splits;
 };
+
+// What a sequence's own part of a shared-prefix decode is: its first chunk, and
+// whether its lengths make sense (an idle sequence, L = 0, has nothing).
+struct Suffix {
+    int first;  // chunk
+    int per;    // chunks per split
+    bool ok;
+};
+__device__ __forceinline__ Suffix suffix_of(const DecodeParams &p, int b, int L) {
+    const int P = p.prefix_lens[b];
+    Suffix s{0, 1, L == 0 || (P >= 0 && P <= L)};
+    if (L > 0 && s.ok) {
+        s.first = P / kChunk;
+        const int n = (L + kChunk - 1) / kChunk - s.first;
+        s.per = max(kMinChunksPerSplit, (n + p.suffix_splits - 1) / p.suffix_splits);
+    }
+    return s;
+}
+
+// Whether group_starts ascends and has sequence b in a group: then the prefix
+// kernel writes b's records.  Every thread of the CTA; asked by the CTAs of a
+// sequence's first split.
+__device__ __forceinline__ bool prefix_covers(const DecodeParams &p, int b, int threads) {
+    bool in = false, order = true;
+    for (int g = threadIdx.x; g < p.num_groups; g += threads) {
+        const int lo = p.group_starts[g], hi = p.group_starts[g + 1];
+        in |= lo <= b && b < hi;
+        order &= lo >= 0 && lo <= hi;
+    }
+    return (__syncthreads_or(in) != 0) & (__syncthreads_or(!order) == 0);
+}
+
+// The records of a sequence that no prefix CTA writes, or whose own lengths are
+// bad: poisoned, so that its rows become zeros.
+__device__ __forceinline__ void poison_prefix_records(const DecodeParams &p, int b, int hq0, int heads, int threads) {
+    for (int i = threadIdx.x; i < heads * p.prefix_splits; i += threads)
+        p.part_ml[((size_t)b * p.num_q_heads + hq0 + i / p.prefix_splits) * p.num_splits + i % p.prefix_splits] =
+            make_float2(-INFINITY, -1.f);
+}
 
 __device__ __forceinline__ void store_out(void *out, size_t idx, float v, int out_bf16) {
     if (out_bf16)

@@ -36,6 +36,21 @@ cudaError_t launch_verify_fp8(int head_dim, const CUtensorMap &tk, const CUtenso
 cudaError_t launch_decode_fp4(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_verify_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream);
 
+// Decode over shared prefixes: the common part (the verify kernel, a row per
+// sequence and head of a group; `rows` of the largest group), and the sequences'
+// own parts (the decode kernels).
+cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const CUtensorMap &tk64, const CUtensorMap &tv64, const CUtensorMap &tk128,
+                          const VerifyParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_prefix_fp8(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                              const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_prefix_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_shared(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                 const DecodeParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_fp8_shared(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                     const DecodeParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_fp4_shared(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream);
+
 // Sets the dynamic shared-memory limit of `fn` once per device.
 cudaError_t ensure_smem_limit(const void *fn, int bytes, int slot);
 // Whether `fn` is launched with at least `regs` registers per thread, asked

@@ -23,13 +23,11 @@ namespace pa {
 
 namespace {
 
-// 64 tokens: at 1K tokens, 16 splits of 4 chunks take 5.12 us per hybrid call
-// against 5.63 us for 32 of 2 (500 tokens: 5.00 against 5.04 us); from 2K up
-// and for the dense shape the plan is the same either way
-constexpr int kMinChunksPerSplit = 4;
 constexpr int kMaxChunksPerSplit = 256; // 4096 tokens: bounds the longest CTA for load balance
+constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tokens
+constexpr int kMaxPrefixChunksF32 = 128;  // and 2048 at most for fp32 outputs
 constexpr int kMaxDevices = 64;
-constexpr int kKernelSlots = 160;
+constexpr int kKernelSlots = 256;
 
 thread_local pa_plan_info g_last_plan;
 thread_local bool g_have_plan = false;
@@ -139,6 +137,72 @@ pa_status make_plan(const pa_attn_desc *d, bool verify, Plan *pl) {
         pl->off_part_ml = round256(rows * splits * d->head_dim * sizeof(float));
         pl->ws_bytes = pl->off_part_ml + rows * splits * sizeof(float2);
     }
+    return PA_OK;
+}
+
+// ---- decode over shared prefixes ------------------------------------------------
+
+struct SharedPlan {
+    int num_sms;
+    int prefix_splits, prefix_chunks;  // splits of a group's prefix, and the most chunks that one may have
+    int suffix_splits, suffix_chunks;  // likewise of a sequence's own part
+    int row_blocks;                    // of the largest group
+    size_t ws_bytes, off_part_ml;
+};
+
+// The hints bound nothing: a longer prefix or own part has longer splits.
+pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, SharedPlan *pl) {
+    pa_status st = check_desc(d, false);
+    if (st != PA_OK) return st;
+    if (!x || x->num_groups < 0 || x->max_group_seqs < 0 || x->max_prefix_len < 0 || x->max_suffix_len < 0 ||
+        x->prefix_splits < 0)
+        return PA_ERR_INVALID_ARG;
+    if (d->num_seqs > 0 && (x->num_groups < 1 || x->max_group_seqs < 1)) return PA_ERR_INVALID_ARG;
+    if (d->window > 0) return PA_ERR_UNSUPPORTED;
+    const int group = d->num_q_heads / d->num_kv_heads;
+    const int64_t rows = static_cast<int64_t>(std::min(x->max_group_seqs, d->num_seqs)) * group;
+    const int64_t blocks = std::max<int64_t>(1, (rows + 127) / 128);
+    if (x->num_groups > 65535 || blocks * d->num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    int sms = d->num_sms;
+    if (sms <= 0 && device_sm_count(&sms) != 0) return PA_ERR_CUDA;
+    auto chunks = [&](int hint) {
+        return (std::min(hint > 0 ? hint : d->max_seq_len, d->max_seq_len) + kChunk - 1) / kChunk;
+    };
+    const int all = (d->max_seq_len + kChunk - 1) / kChunk;
+    pl->num_sms = sms;
+    pl->row_blocks = static_cast<int>(blocks);
+    // the prefix: whole waves of CTAs, splits of whole 64-token tiles
+    const int np = chunks(x->max_prefix_len);
+    const int64_t units = std::max<int64_t>(1, x->num_groups * blocks * d->num_kv_heads);
+    int sp = x->prefix_splits;
+    if (sp == 0) {
+        sp = static_cast<int>(std::max<int64_t>(1, sms / units));
+        sp = std::min(sp, std::max(1, np / kMinPrefixChunks));
+        // the tensor core cuts each addition to an accumulator off towards zero, 2.4e-9 of the sum per key: fp32
+        // outputs keep a split's share below 5e-6
+        if (d->out_dtype == PA_OUT_F32) sp = std::max(sp, (np + kMaxPrefixChunksF32 - 1) / kMaxPrefixChunksF32);
+        const int per = (std::max(1, (np + sp - 1) / sp) + 3) & ~3;
+        sp = std::max(1, (np + per - 1) / per);
+    }
+    pl->prefix_splits = std::min(sp, std::max(1, all));
+    pl->prefix_chunks = (all + 4 * pl->prefix_splits - 1) / (4 * pl->prefix_splits) * 4;
+    // the own parts: as the decode's
+    const int ns = chunks(x->max_suffix_len);
+    const int64_t seqs = std::max<int64_t>(1, static_cast<int64_t>(d->num_seqs) * d->num_kv_heads);
+    int ss = d->num_splits;
+    if (ss == 0) {
+        ss = static_cast<int>(std::max<int64_t>(1, sms / seqs));
+        ss = std::min(ss, std::max(1, ns / kMinChunksPerSplit));
+        if (seqs < sms) ss = std::max(ss, (ns + kMaxChunksPerSplit - 1) / kMaxChunksPerSplit);
+        const int per = std::max(1, (ns + ss - 1) / ss);
+        ss = std::max(1, (ns + per - 1) / per);
+    }
+    pl->suffix_splits = std::min(ss, std::max(1, all));
+    pl->suffix_chunks = std::max(kMinChunksPerSplit, (all + pl->suffix_splits - 1) / pl->suffix_splits);
+    const size_t records =
+        static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits + pl->suffix_splits);
+    pl->off_part_ml = round256(records * d->head_dim * sizeof(float));
+    pl->ws_bytes = pl->off_part_ml + records * sizeof(float2);
     return PA_OK;
 }
 
@@ -259,6 +323,27 @@ bool encode_cache_map_blocks(CUtensorMap *map, const void *base, const pa_attn_d
                       [&](CUtensorMap *m) { return encode_cache_map_blocks_uncached(m, base, d, fp8, tokens); });
 }
 
+// The maps of the tensor-core verify: a 16-token chunk per 128-byte column block
+// (k, v), and whole tiles of one page in one 5-D box (64 tokens: k64, v64; 128 for
+// K where `rows` rows run 128-key score tiles: k128), used only where they fit.
+struct VerifyMaps {
+    CUtensorMap k, v, k64, v64, k128;
+};
+bool encode_verify_maps(VerifyMaps *m, const void *k_cache, const void *v_cache, const pa_attn_desc *d, bool fp8,
+                        int rows) {
+    const int box = fp8 ? 128 : 64;  // elements of 128 bytes
+    if (!encode_cache_map(&m->k, k_cache, d, box, true, fp8) || !encode_cache_map(&m->v, v_cache, d, box, true, fp8))
+        return false;
+    m->k64 = m->k;
+    m->v64 = m->v;
+    if (d->block_size >= 64 && (!encode_cache_map_blocks(&m->k64, k_cache, d, fp8) ||
+                                !encode_cache_map_blocks(&m->v64, v_cache, d, fp8)))
+        return false;
+    m->k128 = m->k64;
+    return fp8 || d->block_size < 128 || !verify_wide_score_tiles(d->head_dim, rows) ||
+           encode_cache_map_blocks(&m->k128, k_cache, d, false, 128);
+}
+
 void record_plan(int path, const Plan &pl, const pa_attn_desc *d, int ctas) {
     g_last_plan.path_id = path;
     g_last_plan.num_splits = pl.num_splits;
@@ -370,6 +455,12 @@ pa_status decode_call(const void *q, const void *k_cache, const void *v_cache, c
 pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
                       const pa_attn_desc *desc, void *out, void *workspace, size_t workspace_bytes,
+                      int32_t *device_status, void *stream, bool fp4 = false);
+
+pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                      const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *group_starts, const int32_t *prefix_lens, const pa_attn_desc *desc,
+                      const pa_prefix_desc *prefix, void *out, void *workspace, size_t workspace_bytes,
                       int32_t *device_status, void *stream, bool fp4 = false);
 
 // The head scales of a quantised cache: both present, aligned floats.
@@ -572,6 +663,46 @@ pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, cons
                        workspace_bytes, device_status, stream, true);
 }
 
+size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc *prefix) {
+    SharedPlan pl;
+    if (make_shared_plan(desc, prefix, &pl) != PA_OK) return static_cast<size_t>(-1);
+    return pl.ws_bytes;
+}
+
+pa_status pa_paged_attention_decode_shared(const void *q, const void *k_cache, const void *v_cache,
+                                           const int32_t *block_table, const int32_t *seq_lens,
+                                           const int32_t *group_starts, const int32_t *prefix_lens,
+                                           const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                           void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                           void *stream) {
+    return shared_call(q, k_cache, v_cache, nullptr, nullptr, block_table, seq_lens, group_starts, prefix_lens, desc,
+                       prefix, out, workspace, workspace_bytes, device_status, stream);
+}
+
+pa_status pa_paged_attention_decode_shared_fp8(const void *q, const void *k_cache, const void *v_cache,
+                                               const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const int32_t *group_starts, const int32_t *prefix_lens,
+                                               const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                               void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                               void *stream) {
+    if (!scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+    return shared_call(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, group_starts, prefix_lens, desc,
+                       prefix, out, workspace, workspace_bytes, device_status, stream);
+}
+
+pa_status pa_paged_attention_decode_shared_fp4(const void *q, const void *k_cache, const void *v_cache,
+                                               const float *k_scale, const float *v_scale,
+                                               const int32_t *block_table, const int32_t *seq_lens,
+                                               const int32_t *group_starts, const int32_t *prefix_lens,
+                                               const pa_attn_desc *desc, const pa_prefix_desc *prefix, void *out,
+                                               void *workspace, size_t workspace_bytes, int32_t *device_status,
+                                               void *stream) {
+    if (!scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+    return shared_call(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, group_starts, prefix_lens, desc,
+                       prefix, out, workspace, workspace_bytes, device_status, stream, true);
+}
+
 }  // extern "C"
 
 namespace pa {
@@ -668,38 +799,9 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
     st = check_workspace(pl, workspace, workspace_bytes);
     if (st != PA_OK) return st;
 
-    CUtensorMap tk, tv;
-    CUtensorMap tk64, tv64;  // whole-tile copies; only used where a 64-token tile fits in a page
-    if (fp4) {
-        // records: no tensor maps
-    } else if (fp8) {
-        // e4m3 in 128-code column blocks, 128-byte swizzle: a 16-token chunk
-        // per block, or a whole 64-token tile in one 5-D box
-        if (!encode_cache_map(&tk, k_cache, desc, 128, true, true) ||
-            !encode_cache_map(&tv, v_cache, desc, 128, true, true))
-            return PA_ERR_CUDA;
-        if (desc->block_size < 64) {
-            tk64 = tk;  // never used: no 64-token tile fits in a smaller page
-            tv64 = tv;
-        } else if (!encode_cache_map_blocks(&tk64, k_cache, desc, true) ||
-                   !encode_cache_map_blocks(&tv64, v_cache, desc, true)) {
-            return PA_ERR_CUDA;
-        }
-    } else if (!encode_cache_map(&tk, k_cache, desc, 64, true) || !encode_cache_map(&tv, v_cache, desc, 64, true)) {
-        return PA_ERR_CUDA;
-    } else if (desc->block_size >= 64) {
-        if (!encode_cache_map_blocks(&tk64, k_cache, desc) || !encode_cache_map_blocks(&tv64, v_cache, desc))
-            return PA_ERR_CUDA;
-    } else {
-        tk64 = tk;  // never used: no 64-token tile fits in a smaller page
-        tv64 = tv;
-    }
     const int group = desc->num_q_heads / desc->num_kv_heads;
-    // 128-token K tiles of one page, for the verify shapes that run 128-key score tiles
-    CUtensorMap tk128 = tk64;
-    if (!fp8 && !fp4 && desc->block_size >= 128 && verify_wide_score_tiles(desc->head_dim, desc->q_len * group) &&
-        !encode_cache_map_blocks(&tk128, k_cache, desc, false, 128))
-        return PA_ERR_CUDA;
+    VerifyMaps maps;
+    if (!fp4 && !encode_verify_maps(&maps, k_cache, v_cache, desc, fp8, desc->q_len * group)) return PA_ERR_CUDA;
 
     VerifyParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -732,9 +834,9 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
     const int row_blocks = (desc->q_len * group + 127) / 128;
     const dim3 grid(pl.num_splits, desc->num_kv_heads * row_blocks, desc->num_seqs);
     const cudaError_t e = fp4   ? launch_verify_fp4(desc->head_dim, p, grid, s)
-                          : fp8 ? launch_verify_fp8(desc->head_dim, tk, tv, tk64, tv64, p, grid, s)
-                                : launch_verify(desc->head_dim, desc->q_len * group, tk, tv, tk64, tv64, tk128, p,
-                                              grid, s);
+                          : fp8 ? launch_verify_fp8(desc->head_dim, maps.k, maps.v, maps.k64, maps.v64, p, grid, s)
+                                : launch_verify(desc->head_dim, desc->q_len * group, maps.k, maps.v, maps.k64, maps.v64,
+                                                maps.k128, p, grid, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
     if (pl.num_splits > 1) {
         ReduceParams r;
@@ -748,6 +850,116 @@ pa_status verify_call(const void *q, const void *k_cache, const void *v_cache, c
             return PA_ERR_CUDA;
     }
     record_plan(PA_PATH_VERIFY_TCGEN05, pl, desc, pl.num_splits * desc->num_kv_heads * row_blocks * desc->num_seqs);
+    return PA_OK;
+}
+
+// Decode over shared prefixes: the groups' common part on the tensor cores, the
+// sequences' own parts as in decode, the merge of all their records.
+pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                      const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *group_starts, const int32_t *prefix_lens, const pa_attn_desc *desc,
+                      const pa_prefix_desc *prefix, void *out, void *workspace, size_t workspace_bytes,
+                      int32_t *device_status, void *stream, bool fp4) {
+    const bool fp8 = k_scale != nullptr && !fp4;
+    SharedPlan pl;
+    pa_status st = make_shared_plan(desc, prefix, &pl);
+    if (st != PA_OK) return st;
+    if (desc->num_seqs == 0) return PA_OK;
+    st = check_common_ptrs(q, k_cache, v_cache, block_table, seq_lens, out);
+    if (st != PA_OK) return st;
+    if (!group_starts || !prefix_lens || (reinterpret_cast<uintptr_t>(group_starts) & 3u) ||
+        (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))
+        return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    const int group = desc->num_q_heads / desc->num_kv_heads;
+    const int rows = std::min(prefix->max_group_seqs, desc->num_seqs) * group;
+    CUtensorMap tk, tv;
+    VerifyMaps maps;
+    if (!fp4 && (!encode_cache_map_blocks(&tk, k_cache, desc, fp8, kChunk) ||
+                 !encode_cache_map_blocks(&tv, v_cache, desc, fp8, kChunk) ||
+                 !encode_verify_maps(&maps, k_cache, v_cache, desc, fp8, rows)))
+        return PA_ERR_CUDA;
+
+    VerifyParams p = {};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.out = out;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + pl.off_part_ml);
+    p.status = device_status;
+    p.num_pages = desc->num_pages;
+    p.num_q_heads = desc->num_q_heads;
+    p.q_len = 1;
+    p.group = group;
+    p.max_pages_per_seq = desc->max_pages_per_seq;
+    p.max_seq_len = desc->max_seq_len;
+    p.block_size = desc->block_size;
+    p.chunks_per_split = pl.prefix_chunks;
+    p.num_splits = pl.prefix_splits + pl.suffix_splits;
+    p.scale_log2 = desc->scale * 1.4426950408889634f;
+    p.out_bf16 = desc->out_dtype == PA_OUT_BF16;
+    p.num_kv_heads = desc->num_kv_heads;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.prefix_lens = prefix_lens;
+    p.group_starts = group_starts;
+    p.num_seqs = desc->num_seqs;
+    p.max_members = std::min(prefix->max_group_seqs, desc->num_seqs);
+    p.prefix_splits = pl.prefix_splits;
+
+    DecodeParams d = {};
+    d.q = p.q;
+    d.block_table = block_table;
+    d.seq_lens = seq_lens;
+    d.out = out;
+    d.part_o = p.part_o;
+    d.part_ml = p.part_ml;
+    d.status = device_status;
+    d.num_pages = desc->num_pages;
+    d.num_q_heads = desc->num_q_heads;
+    d.max_pages_per_seq = desc->max_pages_per_seq;
+    d.max_seq_len = desc->max_seq_len;
+    d.block_size = desc->block_size;
+    d.chunks_per_split = pl.suffix_chunks;
+    d.num_splits = p.num_splits;
+    d.scale_log2 = p.scale_log2;
+    d.out_bf16 = p.out_bf16;
+    d.k_scale = k_scale;
+    d.v_scale = v_scale;
+    d.k_cache = static_cast<uint8_t *>(const_cast<void *>(k_cache));
+    d.v_cache = static_cast<uint8_t *>(const_cast<void *>(v_cache));
+    d.prefix_lens = prefix_lens;
+    d.group_starts = group_starts;
+    d.num_groups = prefix->num_groups;
+    d.prefix_splits = pl.prefix_splits;
+    d.suffix_splits = pl.suffix_splits;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 pgrid(pl.prefix_splits, desc->num_kv_heads * pl.row_blocks, prefix->num_groups);
+    cudaError_t e = fp4   ? launch_prefix_fp4(desc->head_dim, p, pgrid, s)
+                    : fp8 ? launch_prefix_fp8(desc->head_dim, maps.k, maps.v, maps.k64, maps.v64, p, pgrid, s)
+                          : launch_prefix(desc->head_dim, rows, maps.k, maps.v, maps.k64, maps.v64, maps.k128, p, pgrid,
+                                          s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    const dim3 sgrid(pl.suffix_splits, desc->num_kv_heads, desc->num_seqs);
+    e = fp4   ? launch_decode_fp4_shared(desc->head_dim, group, d, sgrid, s)
+        : fp8 ? launch_decode_fp8_shared(desc->head_dim, group, tk, tv, d, sgrid, s)
+              : launch_decode_shared(desc->head_dim, group, tk, tv, d, sgrid, s);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    ReduceParams r;
+    r.part_o = p.part_o;
+    r.part_ml = p.part_ml;
+    r.out = out;
+    r.num_q_heads = desc->num_q_heads;
+    r.num_splits = p.num_splits;
+    r.out_bf16 = p.out_bf16;
+    if (launch_reduce(desc->head_dim, r, desc->num_seqs, pl.num_sms, s) != cudaSuccess) return PA_ERR_CUDA;
+    const Plan told{pl.num_sms, p.num_splits, pl.suffix_chunks, 0, 0};
+    record_plan(PA_PATH_DECODE_SHARED, told, desc,
+                static_cast<int>(pgrid.x * pgrid.y * pgrid.z + sgrid.x * sgrid.y * sgrid.z));
     return PA_OK;
 }
 

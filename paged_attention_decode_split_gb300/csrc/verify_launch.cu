@@ -1,34 +1,8 @@
 // verify_launch.cu -- instantiates the tensor-core verify kernel per head_dim
 // and launches it.
-#include "pa_internal.h"
+#include "verify_launch.cuh"
 
 namespace pa {
-
-namespace {
-
-template <int D, int NK, int NV, int NSG, int NSB, int TK = 64>
-cudaError_t launch_verify_tc(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
-                             const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream,
-                             int slot) {
-    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK>;
-    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, NSB, TK>;
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
-    if (e != cudaSuccess) return e;
-    // programmatic dependent launch: the set-up overlaps the work before it
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, tk, tv, tk64, tv64, p);
-}
-
-}  // namespace
 
 // Rows beyond 128 run as several 128-row blocks (grid y = Hkv x blocks), up
 // to q_len 4096 x G 8 = 32768 rows.

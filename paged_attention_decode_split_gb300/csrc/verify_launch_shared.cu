@@ -1,0 +1,32 @@
+// verify_launch_shared.cu -- the tensor-core kernel as the common part of a
+// decode over shared prefixes, bf16 and e4m3 caches, in a translation unit of its
+// own so it compiles in parallel with the rest.
+#include "verify_launch.cuh"
+
+namespace pa {
+
+// rows: what the largest group may have, sequences x heads of the group.  The
+// layouts are the verify's (verify_launch.cu).
+cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const CUtensorMap &tk64, const CUtensorMap &tv64, const CUtensorMap &tk128,
+                          const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    const bool wide = verify_wide_score_tiles(head_dim, rows);
+    if (head_dim == 256)
+        return wide ? launch_verify_tc<256, 1, 3, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 224)
+                    : launch_verify_tc<256, 4, 3, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 225);
+    if (head_dim == 128)
+        return wide ? launch_verify_tc<128, 3, 6, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 226)
+                    : launch_verify_tc<128, 6, 6, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 227);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefix_fp8(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                              const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (head_dim == 256)
+        return launch_verify_tc<256, 2, 3, 2, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 228);
+    if (head_dim == 128)
+        return launch_verify_tc<128, 4, 4, 4, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 229);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

@@ -107,6 +107,15 @@ struct VerifyParams {
     const float *v_scale;
     const uint8_t *k_cache;  // fp4 cache: the records (copied without a tensor map)
     const uint8_t *v_cache;
+    // The common part of a decode over shared prefixes (SH kernels): the rows of
+    // a CTA are those of the sequences of group blockIdx.z, one per sequence and
+    // head, and see the first prefix_lens tokens, rounded down to whole chunks,
+    // through the table of the group's first sequence that is not idle.
+    const int32_t *prefix_lens;   // [num_seqs]
+    const int32_t *group_starts;  // [groups + 1]
+    int num_seqs;
+    int max_members;              // sequences of a group that the grid covers
+    int prefix_splits;            // the first records of a row's num_splits
 };
 
 // Byte offset of 16-byte column chunk c of row t in a [D/64][rows][128 B]
@@ -333,8 +342,14 @@ struct VerifyTcCfg {
 // 8 tiles 1.3e-6 and 64, 16 tiles 2.5e-6 and 57, none 51; a 32-bit product and
 // softmax in torch is off by 1.7e-6.  Four keeps below that at any length.)
 constexpr int kVerifyFarTiles = 4;
+// Logits (log2 units) up to which an exponent may be formed as score * scale -
+// max in one fused step: the max is that product rounded, off by up to 2^-24 of
+// itself, which beyond this would pass through 2^x as a factor of two and more.
+constexpr float kExactLogits = 16777216.f;
+// SH: the common part of a decode over shared prefixes (VerifyParams): no causal
+// mask, a row per sequence and head.
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
-          bool FAR = false>
+          bool FAR = false, bool SH = false>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
@@ -377,17 +392,59 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     // [scale block][0-3: token - (first row's last key + 1), 4-7: token - k_first]
     uint32_t *nan_bits = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);
 
-    const int split = blockIdx.x, b = blockIdx.z;
-    const int kvh = blockIdx.y % p.num_kv_heads;
+    const int split = blockIdx.x, kvh = blockIdx.y % p.num_kv_heads;
+    [[maybe_unused]] int b = blockIdx.z;  // the sequence whose block table is read
     // Row blocks launch last-first: later blocks see more keys (causal), so the
     // longest CTAs go out in the first wave and a partial last wave holds the
     // shortest ones.
     const int n_blocks = gridDim.y / p.num_kv_heads;
     const int row0 = (n_blocks - 1 - (int)(blockIdx.y / p.num_kv_heads)) * C::M;  // first row (rho = r G + g)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.group, R = min(C::M, p.q_len * G - row0);  // rows of this block
-
-    pdl_launch_dependents();
+    const int G = p.group;
+    size_t row_base = (size_t)blockIdx.z * p.q_len;  // of the call's (sequence, new row) pairs: this CTA's first
+    int members = p.q_len;                           // pairs of this CTA's sequence (SH: sequences of its group)
+    [[maybe_unused]] int prefix = 0;                 // SH: prefix_lens of the group
+    if constexpr (SH) {
+        // The kernel behind this one, which works on the sequences' own parts,
+        // depends on the work before both, not on this one: it may start now.
+        pdl_wait_primary();
+        pdl_launch_dependents();
+        const int g = blockIdx.z;
+        const int lo = min(max(p.group_starts[g], 0), p.num_seqs);
+        const int hi = min(max(p.group_starts[g + 1], lo), p.num_seqs);
+        row_base = lo;
+        members = min(hi - lo, p.max_members);
+        // the first sequence with tokens has the table and the length of the prefix
+        int first = -1;
+        for (int i0 = 0; i0 < members && first < 0; i0 += 32) {
+            const int i = i0 + (threadIdx.x & 31);
+            const int len = i < members ? p.seq_lens[lo + i] : 0;
+            const uint32_t there = __ballot_sync(0xffffffffu, len > 0 && len <= p.max_seq_len);
+            if (there != 0) first = i0 + __ffs(there) - 1;
+        }
+        b = lo + max(first, 0);
+        if (first >= 0) prefix = p.prefix_lens[b];
+        if (prefix < 0 || (first >= 0 && prefix > p.seq_lens[b])) prefix = 0;  // (that sequence is flagged below)
+        if (row0 == 0 && members < hi - lo) {  // more than the host said: rows without a CTA
+            if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+            for (int rho = members * G + threadIdx.x; rho < (hi - lo) * G; rho += C::THREADS)
+                p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split] =
+                    make_float2(-INFINITY, -1.f);
+        }
+        if (row0 >= members * G) return;  // no row in this block
+    } else {
+        pdl_launch_dependents();
+    }
+    const int R = min(C::M, members * G - row0);  // rows of this block
+    // SH: what becomes of row rho: 0 its share of the prefix, 1 nothing (an idle
+    // sequence), 2 zeros (its lengths are bad, or not those of the group)
+    [[maybe_unused]] auto row_state = [&](int rho) {
+        const int s = (int)row_base + rho / G, len = p.seq_lens[s], pre = p.prefix_lens[s];
+        if (len == 0) return 1;
+        const bool ok = len > 0 && len <= p.max_seq_len && pre == prefix && pre <= len;
+        if (!ok && split == 0 && kvh == 0 && rho % G == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+        return ok ? 0 : 2;
+    };
     if (threadIdx.x == 0) {
         // a K/V ring slot is filled by the copy engine (one expect-tx arrival),
         // or with an fp8 cache by the CW widening warps of its tensor
@@ -427,9 +484,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     // memory is kept coherent, so a row the work before this call is still
     // writing is read in its final state after the wait all the same.
     const int rho_q = row0 + (int)threadIdx.x;  // the softmax threads' rows (rows past R are zero padding)
-    const __nv_bfloat16 *qrow =
-        p.q + (((size_t)b * p.q_len + rho_q / G) * p.num_q_heads + kvh * G + rho_q % G) * D;
-    if (!F4 && warp < 4 && (int)threadIdx.x < R) {
+    const __nv_bfloat16 *qrow = p.q + ((row_base + rho_q / G) * p.num_q_heads + kvh * G + rho_q % G) * D;
+    if (!SH && !F4 && warp < 4 && (int)threadIdx.x < R) {
 #pragma unroll
         for (int o = 0; o < D * 2; o += 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(qrow) + o));
@@ -446,7 +502,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         const int rho = row0 + rl, qi = rho / G;
         int g = rho - qi * G;
         const __nv_bfloat16 *row =
-            p.q + (((size_t)b * p.q_len + qi) * p.num_q_heads + kvh * G + g) * D + 8 * (lane % QL);
+            p.q + ((row_base + qi) * p.num_q_heads + kvh * G + g) * D + 8 * (lane % QL);
 #pragma unroll
         for (int k = 0; k < QN; ++k) {
             qx[k] = rl < R ? *reinterpret_cast<const uint4 *>(row) : make_uint4(0u, 0u, 0u, 0u);
@@ -463,24 +519,32 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
     // except with early_kv: then the block table, seq_lens and the tiles that
     // end before the new rows are read first (see the producer below).
     if (!p.early_kv) {
-        pdl_wait_primary();
+        if (!SH) pdl_wait_primary();
         if (F4 && warp >= C::W0) fetch_q();
     }
 
-    int L = p.seq_lens[b];
-    const bool bad_len = L < 0 || L > p.max_seq_len || L < p.q_len;
+    int L = SH ? prefix / kChunk * kChunk : p.seq_lens[b];
+    const bool bad_len = !SH && (L < 0 || L > p.max_seq_len || L < p.q_len);
     if (bad_len) {
         if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
         L = 0;
     }
     const int n_chunks = (L + kChunk - 1) / kChunk;
+    // SH: splits of whole 64-token tiles of the group's own prefix
+    const int cps = SH ? (n_chunks + 4 * p.prefix_splits - 1) / (4 * p.prefix_splits) * 4 : p.chunks_per_split;
     // with a sliding window the splits start at the chunk of the block's first
     // visible key (its first row's window start)
-    const int k_first = p.window > 0 ? max(0, L - p.q_len + row0 / G - p.window + 1) : 0;
-    const int c_begin = k_first / kChunk + split * p.chunks_per_split;
+    const int k_first = !SH && p.window > 0 ? max(0, L - p.q_len + row0 / G - p.window + 1) : 0;
+    const int c_begin = k_first / kChunk + split * cps;
     // keys past the block's last row's causal limit are never read
-    const int k_last = L - p.q_len + (row0 + R - 1) / G;
-    const int n_my = min(min(n_chunks, k_last / kChunk + 1) - c_begin, p.chunks_per_split);
+    const int k_last = SH ? L - 1 : L - p.q_len + (row0 + R - 1) / G;
+    const int n_my = min((SH ? n_chunks : min(n_chunks, k_last / kChunk + 1)) - c_begin, cps);
+    if (SH && n_my <= 0) {  // the row's other splits have its keys, if there are any
+        for (int rho = row0 + threadIdx.x; rho < row0 + R; rho += C::THREADS)
+            p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split] =
+                make_float2(-INFINITY, row_state(rho) == 2 ? -1.f : 0.f);
+        return;
+    }
     if (n_my <= 0) {
         // No key of this sequence in this split: an empty record (m = -inf,
         // l = 0) for the reduce, or zero rows when the call is unsplit.
@@ -488,12 +552,12 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         if (p.num_splits == 1) {
             for (int idx = threadIdx.x; idx < R * D; idx += C::THREADS) {
                 const int rho = row0 + idx / D, d = idx % D;
-                const size_t row = (size_t)b * p.q_len + rho / G;
+                const size_t row = row_base + rho / G;
                 store_out(p.out, (row * p.num_q_heads + kvh * G + rho % G) * D + d, 0.f, p.out_bf16);
             }
         } else {
             for (int rho = row0 + threadIdx.x; rho < row0 + R; rho += C::THREADS) {
-                const size_t row = (size_t)b * p.q_len + rho / G;
+                const size_t row = row_base + rho / G;
                 p.part_ml[(row * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split] =
                     make_float2(-INFINITY, 0.f);
             }
@@ -878,7 +942,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             uint8_t *stg = smem + C::OFF_STG + tensor * NSG * C::STG_BYTES + rc * REC;
             const int t_end = min(k_last + 1, (c_begin + n_my) * kChunk);
             // every row sees the tokens [w_last, f_last]
-            const int f_last = L - p.q_len + row0 / G, w_last = p.window > 0 ? k_last - p.window + 1 : 0;
+            const int f_last = SH ? L - 1 : L - p.q_len + row0 / G;
+            const int w_last = !SH && p.window > 0 ? k_last - p.window + 1 : 0;
             // K: lane = token r of the half, quarter c of every block; r and r ^ 5 in the same quarter-warp, so that
             // its eight 16-byte reads (bit 0) and ring writes (bit 2) fall in eight bank groups
             // V: lane = token pair c, dims 2 r, 2 r + 1 of every block
@@ -1102,10 +1167,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // split's last chunk (a tile may reach into the next split's tokens)
         const int t_end = min(L, (c_begin + n_my) * kChunk);
         // (dead rows of a live warp, all zeros, see everything: a mask of their own would send the warp both ways)
-        const int lim = live ? min(L - p.q_len + rho / G, t_end - 1) : INT_MAX;
+        const int lim = !live ? INT_MAX : SH ? t_end - 1 : min(L - p.q_len + rho / G, t_end - 1);
         // a warp without live rows only keeps the phases (its rows of S come from zeros of Q, its rows of O go nowhere)
         const bool idle_warp = F4 && warp * 32 >= R;
-        const int lo = p.window > 0 && live ? L - p.q_len + rho / G - p.window + 1 : 0;  // first key of the row's window
+        const int lo = !SH && p.window > 0 && live ? L - p.q_len + rho / G - p.window + 1 : 0;  // first key of the row's window
         // fp8: K's scale and the inverse of q's pre-scale (a power of two) join the softmax scale
         const float sl = F8 ? p.scale_log2 * p.k_scale[kvh] * (1.f / q_pre) : p.scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
@@ -1119,10 +1184,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         // or read, added and stored without red: no less).
         [[maybe_unused]] float m_far = -INFINITY;  // the reference max that the second sum stands for
         [[maybe_unused]] const uint32_t my_row =
-            live ? (uint32_t)((((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split)
-                 : 0u;
+            live ? (uint32_t)(((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split) : 0u;
         [[maybe_unused]] const int n_live = min(32, R - warp * 32);
-        [[maybe_unused]] float *far_base = p.num_splits == 1 ? static_cast<float *>(p.out) : p.part_o;
+        [[maybe_unused]] float *far_base = !SH && p.num_splits == 1 ? static_cast<float *>(p.out) : p.part_o;
         [[maybe_unused]] auto far_place = [&](int j) {  // (the whole warp) the lane's float4 j of the second sum
             const int at = j * n_live + min(lane, n_live - 1);
             const uint32_t row = __shfl_sync(0xffffffffu, my_row, at / (D / 4));
@@ -1230,6 +1294,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     mr[0] = fmaxf(fmax3(mr[0], sv[TT - 4], sv[TT - 3]), sv[TT - 2]);
                     mx = fmaxf(fmax3(mr[0], mr[1], mr[2]), fmaxf(mr[3], sv[TT - 1])) * sl;
                     mul = sl;
+                    if (SH && fabsf(mx) > kExactLogits) {
+#pragma unroll
+                        for (int c = 0; c < TT; ++c) sv[c] *= sl;
+                        mul = 1.f;
+                    }
                 } else {
 #pragma unroll
                     for (int c = 0; c < TT; ++c) sv[c] = (t0 + c <= lim && t0 + c >= lo) ? sv[c] * sl : -INFINITY;
@@ -1334,8 +1403,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 // every key of the tile is visible to this row (no mask, and the
                 // max of the scaled scores is the scaled max for scale > 0), else
                 // scaled and masked scores with mul = 1.
-                const bool all_visible = sl > 0.f && t0 + TK - 1 <= lim && t0 >= lo;
-                const float mul = all_visible ? sl : 1.f;
+                bool all_visible = sl > 0.f && t0 + TK - 1 <= lim && t0 >= lo;
+                float mul = all_visible ? sl : 1.f;
                 // 64 scores of half h2 (all loads in flight, one wait), masked and scaled unless all_visible
                 float sv[TT];
                 auto load_half = [&](int h2) {
@@ -1370,6 +1439,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 for (int h2 = 0; h2 < nvt; ++h2) {  // the tile's max, over every half
                     load_half(h2);
                     mx = fmaxf(mx, half_max());
+                }
+                if (SH && fabsf(mx) > kExactLogits) {
+                    all_visible = false;
+                    mul = 1.f;
                 }
                 // lazy rescale: only when the max grows by more than 2^kLazy, and
                 // then only after the previous tile's P.V product has finished
@@ -1453,7 +1526,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         tc::fence_after();
         const bool poisoned = !ok || flags[1] != 0;
         const float inv = (poisoned || !(l_sum > 0.f)) ? 0.f : (F8 ? p.v_scale[kvh] : 1.f) / l_sum;
-        const size_t orow = live ? ((size_t)b * p.q_len + rho / G) * p.num_q_heads + kvh * G + rho % G : 0;
+        const size_t orow = live ? (row_base + rho / G) * p.num_q_heads + kvh * G + rho % G : 0;
         [[maybe_unused]] auto sees_nan = [&](int blk) {  // the row sees a token of nan_bits in this scale block
             const int f_next = L - p.q_len + row0 / G + 1;
             bool hit = false;
@@ -1465,7 +1538,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
             }
             return hit;
         };
-        const bool direct = p.num_splits == 1;  // the final output, else this split's record
+        const bool direct = !SH && p.num_splits == 1;  // the final output, else this split's record
         if (FAR && !ok) {  // (other lanes' parts of the second sum may be on their way to this row)
             __threadfence();
             __syncwarp();
@@ -1558,7 +1631,13 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     p.part_o[(orow * p.num_splits + split) * D + c] = 0.f;
             }
         }
-        if (live && !direct)
+        if (SH && live) {
+            const int state = row_state(rho);
+            p.part_ml[orow * p.num_splits + split] = poisoned || state == 2 ? make_float2(m_ref, -1.f)
+                                                     : state == 1          ? make_float2(-INFINITY, 0.f)
+                                                     : l_sum != l_sum      ? make_float2(0.f, 1.f)
+                                                                           : make_float2(m_ref, l_sum);
+        } else if (live && !direct)
             // (F4: a NaN sum goes on as a NaN row with max 0 and sum 1: the reduce takes a sum that is not > 0 for
             // an empty split, and the max may be infinite)
             p.part_ml[orow * p.num_splits + split] = poisoned                  ? make_float2(m_ref, -1.f)
