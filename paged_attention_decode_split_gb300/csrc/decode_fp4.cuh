@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = fp.group, hq0 = kvh * G, hkv = gridDim.y;
+    [[maybe_unused]] const bool last_cta = split == (int)gridDim.x - 1 && kvh == hkv - 1 && b == (int)gridDim.z - 1;
 
     pdl_launch_dependents();
     uint64_t *q_full = full + NW * SPW;
@@ -227,7 +228,8 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
         // l = 0); an unsplit call owns its output rows and zeroes them
-        if (p.early_kv || SH) pdl_wait_primary();
+        if constexpr (SH) wait_prefix(last_cta);
+        if (p.early_kv) pdl_wait_primary();
         if (p.num_splits == 1) {
             for (int idx = threadIdx.x; idx < G * D; idx += C::THREADS)
                 store_out(p.out, ((size_t)b * p.num_q_heads + hq0) * D + idx, 0.f, p.out_bf16);
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
         else
             *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + record) * D + d) = o;
     }
-    if constexpr (SH) pdl_wait_primary();
+    if constexpr (SH) wait_prefix(last_cta);
 }
 
 }  // namespace pa

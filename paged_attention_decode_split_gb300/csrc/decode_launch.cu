@@ -54,6 +54,24 @@ cudaError_t launch_reduce_small_n(cudaLaunchConfig_t cfg, const ReduceParams &p,
 
 }  // namespace
 
+cudaError_t launch_reduce_rows(int head_dim, const ReduceParams &p, int rows, int num_sms, cudaStream_t stream) {
+    if (p.num_splits <= kReduceSmallMaxSplits || rows * p.num_q_heads < 2 * num_sms)
+        return launch_reduce(head_dim, p, rows, num_sms, stream);
+    const int pairs = rows * p.num_q_heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((pairs + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (head_dim == 256) return cudaLaunchKernelEx(&cfg, pa_split_reduce_rows_kernel<256>, p, pairs);
+    if (head_dim == 128) return cudaLaunchKernelEx(&cfg, pa_split_reduce_rows_kernel<128>, p, pairs);
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_reduce(int head_dim, const ReduceParams &p, int rows, int num_sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = 0;

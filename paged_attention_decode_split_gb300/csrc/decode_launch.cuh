@@ -78,7 +78,19 @@ cudaError_t launch_decode_cfg(int head_dim, int group, const CUtensorMap &tk, co
             return launch_decode_mma_t<D, 16, NST2, SPS2, DS2, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 8); \
     }                                                                                                         \
     return cudaErrorInvalidValue;
-    if constexpr (F8) {
+    if constexpr (SH && F8) {
+        if (head_dim == 256) {
+            PA_DECODE_CASES(256, 4, 3, 1, true, 4, 6, 1, slot0)
+        } else if (head_dim == 128) {
+            PA_DECODE_CASES(128, 6, 4, 1, true, 6, 8, 1, slot0 + 10)
+        }
+    } else if constexpr (SH) {
+        if (head_dim == 256) {
+            PA_DECODE_CASES(256, 2, 3, 2, false, 2, 6, 2, slot0)
+        } else if (head_dim == 128) {
+            PA_DECODE_CASES(128, 4, 3, 2, true, 8, 3, 1, slot0 + 10)
+        }
+    } else if constexpr (F8) {
         if (head_dim == 256) {
             PA_DECODE_CASES(256, 4, 6, 1, true, 4, 6, 1, slot0)
         } else if (head_dim == 128) {

@@ -186,10 +186,13 @@ __device__ __forceinline__ void append_new_row(const DecodeParams &p, int b, int
 // of the dependency wait (PA_FLAG_EARLY_KV_READ).
 // SH: the own part of a decode over shared prefixes (DecodeParams).  The kernel
 // in front of it is the prefix kernel, which lets it start once the work before
-// both has finished: it need not wait for its stream dependency before it reads,
-// and waits at its end, so that whoever waits for it has waited for both.
+// both has finished: it need not wait for its stream dependency before it reads.
+// One CTA, the last to be scheduled, waits at its end, so that whoever waits for
+// this kernel has waited for both.  Two CTAs per SM (up to 8 heads), each with
+// half a ring: own parts are short, and one CTA's table, first copies and merge
+// then pass behind the other's copies.
 template <int D, int G, int NT, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, int PF = 0, bool SH = false>
-__global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
+__global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     pa_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const DecodeParams p) {
     using C = MmaCfg<D, NT, NST, SPS, DS, F8>;
@@ -207,6 +210,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
     const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hq0 = kvh * G;
+    [[maybe_unused]] const bool last_cta = split == (int)gridDim.x - 1 && kvh == (int)gridDim.y - 1 && b == (int)gridDim.z - 1;
 
     // Programmatic dependent launch: as in the CUDA-core decode kernel, every
     // global access waits for the work before this call unless early_kv lets
@@ -270,7 +274,8 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
         // l = 0); an unsplit call owns its output rows and zeroes them
-        if (p.early_kv || SH) pdl_wait_primary();
+        if constexpr (SH) wait_prefix(last_cta);
+        if (p.early_kv) pdl_wait_primary();
         if (p.num_splits == 1) {
             for (int idx = threadIdx.x; idx < G * D; idx += C::THREADS)
                 store_out(p.out, ((size_t)b * p.num_q_heads + hq0) * D + idx, 0.f, p.out_bf16);
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, 1)
             *reinterpret_cast<float4 *>(p.part_o + (row * p.num_splits + record) * D + d) = o;
         }
     }
-    if constexpr (SH) pdl_wait_primary();
+    if constexpr (SH) wait_prefix(last_cta);
 }
 
 }  // namespace pa

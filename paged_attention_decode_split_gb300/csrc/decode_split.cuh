@@ -62,6 +62,7 @@ struct DecodeParams {
     int num_groups;
     int prefix_splits;
     int suffix_splits;
+    int suffix_chunks;  // of a split, where that makes no more than suffix_splits
 };
 
 // What a sequence's own part of a shared-prefix decode is: its first chunk, and
@@ -77,9 +78,15 @@ __device__ __forceinline__ Suffix suffix_of(const DecodeParams &p, int b, int L)
     if (L > 0 && s.ok) {
         s.first = P / kChunk;
         const int n = (L + kChunk - 1) / kChunk - s.first;
-        s.per = max(kMinChunksPerSplit, (n + p.suffix_splits - 1) / p.suffix_splits);
+        s.per = max(p.suffix_chunks, (n + p.suffix_splits - 1) / p.suffix_splits);
     }
     return s;
+}
+
+// The end of a CTA of the own parts: whoever waits for their kernel must have
+// waited for the prefix kernel too.
+__device__ __forceinline__ void wait_prefix(bool last_cta) {
+    if (last_cta) pdl_wait_primary();
 }
 
 // Whether group_starts ascends and has sequence b in a group: then the prefix
@@ -288,6 +295,70 @@ __global__ void __launch_bounds__(256, 1) pa_split_reduce_small_kernel(const Red
             store_out4(p.out, base + 128 * e, make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv),
                        p.out_bf16);
     }
+}
+
+// The same merge for many rows of more splits (decode over shared prefixes): a
+// warp merges one (row, head) pair.  Its lanes take the statistics of 32 splits at
+// a time and form their weights against the common maximum, so that no running
+// rescale is needed; the outputs of 8 splits are loaded at once.
+template <int D>
+__global__ void __launch_bounds__(128) pa_split_reduce_rows_kernel(const ReduceParams p, int pairs) {
+    constexpr int E = D / 128;  // float4 columns per lane
+    constexpr int U = 8;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const int pair = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (pair >= pairs) return;
+    const int S = p.num_splits;
+    const float2 *ml = p.part_ml + (size_t)pair * S;
+    const float *po = p.part_o + (size_t)pair * S * D + 4 * lane;
+    float M = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < S; i += 32) {
+        const float2 v = ml[i];
+        bad |= v.y < 0.f;
+        if (v.y > 0.f) M = fmaxf(M, v.x);
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    bad = __any_sync(0xffffffffu, bad);
+    float W = 0.f;
+    float4 a[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < S; i0 += 32) {
+        const float2 v = i0 + lane < S ? ml[i0 + lane] : make_float2(-INFINITY, 0.f);
+        const float w = v.y > 0.f ? fast_exp2(v.x - M) * v.y : 0.f;  // (0: an empty split, its outputs may be anything)
+        W += w;
+        for (int i1 = 0; i1 < min(32, S - i0); i1 += U) {
+            float4 o[U][E];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[u][e] = *reinterpret_cast<const float4 *>(po + (size_t)min(i0 + i1 + u, S - 1) * D + 128 * e);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float c = __shfl_sync(0xffffffffu, w, i1 + u);  // (0 past the last split)
+                if (c == 0.f) continue;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    a[e].x = fmaf(c, o[u][e].x, a[e].x); a[e].y = fmaf(c, o[u][e].y, a[e].y);
+                    a[e].z = fmaf(c, o[u][e].z, a[e].z); a[e].w = fmaf(c, o[u][e].w, a[e].w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) W += __shfl_xor_sync(0xffffffffu, W, k);
+    const bool zero = bad || !(W > 0.f);
+    const float inv = zero ? 0.f : 1.f / W;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        store_out4(p.out, (size_t)pair * D + 4 * lane + 128 * e,
+                   zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv),
+                   p.out_bf16);
 }
 
 }  // namespace pa

@@ -144,8 +144,9 @@ pa_status make_plan(const pa_attn_desc *d, bool verify, Plan *pl) {
 
 struct SharedPlan {
     int num_sms;
-    int prefix_splits, prefix_chunks;  // splits of a group's prefix, and the most chunks that one may have
-    int suffix_splits, suffix_chunks;  // likewise of a sequence's own part
+    // splits of a group's prefix, the chunks of one for the lengths that the plan was told, and the most it may have
+    int prefix_splits, prefix_chunks, prefix_most;
+    int suffix_splits, suffix_chunks, suffix_most;  // likewise of a sequence's own part
     int row_blocks;                    // of the largest group
     size_t ws_bytes, off_part_ml;
 };
@@ -184,8 +185,10 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
         const int per = (std::max(1, (np + sp - 1) / sp) + 3) & ~3;
         sp = std::max(1, (np + per - 1) / per);
     }
+    auto tiles = [](int n, int splits) { return (std::max(1, (n + splits - 1) / splits) + 3) & ~3; };
     pl->prefix_splits = std::min(sp, std::max(1, all));
-    pl->prefix_chunks = (all + 4 * pl->prefix_splits - 1) / (4 * pl->prefix_splits) * 4;
+    pl->prefix_chunks = tiles(np, pl->prefix_splits);
+    pl->prefix_most = std::max(pl->prefix_chunks, tiles(all, pl->prefix_splits));
     // the own parts: as the decode's
     const int ns = chunks(x->max_suffix_len);
     const int64_t seqs = std::max<int64_t>(1, static_cast<int64_t>(d->num_seqs) * d->num_kv_heads);
@@ -198,7 +201,8 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
         ss = std::max(1, (ns + per - 1) / per);
     }
     pl->suffix_splits = std::min(ss, std::max(1, all));
-    pl->suffix_chunks = std::max(kMinChunksPerSplit, (all + pl->suffix_splits - 1) / pl->suffix_splits);
+    pl->suffix_chunks = std::max(kMinChunksPerSplit, (ns + pl->suffix_splits - 1) / pl->suffix_splits);
+    pl->suffix_most = std::max(pl->suffix_chunks, (all + pl->suffix_splits - 1) / pl->suffix_splits);
     const size_t records =
         static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits + pl->suffix_splits);
     pl->off_part_ml = round256(records * d->head_dim * sizeof(float));
@@ -895,7 +899,8 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     p.max_pages_per_seq = desc->max_pages_per_seq;
     p.max_seq_len = desc->max_seq_len;
     p.block_size = desc->block_size;
-    p.chunks_per_split = pl.prefix_chunks;
+    p.chunks_per_split = pl.prefix_most;
+    p.prefix_chunks = pl.prefix_chunks;
     p.num_splits = pl.prefix_splits + pl.suffix_splits;
     p.scale_log2 = desc->scale * 1.4426950408889634f;
     p.out_bf16 = desc->out_dtype == PA_OUT_BF16;
@@ -923,7 +928,8 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     d.max_pages_per_seq = desc->max_pages_per_seq;
     d.max_seq_len = desc->max_seq_len;
     d.block_size = desc->block_size;
-    d.chunks_per_split = pl.suffix_chunks;
+    d.chunks_per_split = pl.suffix_most;
+    d.suffix_chunks = pl.suffix_chunks;
     d.num_splits = p.num_splits;
     d.scale_log2 = p.scale_log2;
     d.out_bf16 = p.out_bf16;
@@ -956,7 +962,7 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     r.num_q_heads = desc->num_q_heads;
     r.num_splits = p.num_splits;
     r.out_bf16 = p.out_bf16;
-    if (launch_reduce(desc->head_dim, r, desc->num_seqs, pl.num_sms, s) != cudaSuccess) return PA_ERR_CUDA;
+    if (launch_reduce_rows(desc->head_dim, r, desc->num_seqs, pl.num_sms, s) != cudaSuccess) return PA_ERR_CUDA;
     const Plan told{pl.num_sms, p.num_splits, pl.suffix_chunks, 0, 0};
     record_plan(PA_PATH_DECODE_SHARED, told, desc,
                 static_cast<int>(pgrid.x * pgrid.y * pgrid.z + sgrid.x * sgrid.y * sgrid.z));

@@ -16,7 +16,7 @@ cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const C
                     : launch_verify_tc<256, 4, 3, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 225);
     if (head_dim == 128)
         return wide ? launch_verify_tc<128, 3, 6, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 226)
-                    : launch_verify_tc<128, 6, 6, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 227);
+                    : launch_verify_tc<128, 3, 3, 0, 1, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 227);
     return cudaErrorInvalidValue;
 }
 

@@ -116,6 +116,7 @@ struct VerifyParams {
     int num_seqs;
     int max_members;              // sequences of a group that the grid covers
     int prefix_splits;            // the first records of a row's num_splits
+    int prefix_chunks;            // of a split, where that makes no more than prefix_splits
 };
 
 // Byte offset of 16-byte column chunk c of row t in a [D/64][rows][128 B]
@@ -302,7 +303,8 @@ struct VerifyTcCfg {
     // tensor-memory columns: O (fp32, D), NSB S/P buffers (TK each), Q (bf16
     // pairs, D / 2; not with QSM).  P of a score tile is written over its S
     // buffer, per 64-key half: a bf16 head in 32 columns, then the residual in 32.
-    static constexpr int TMEM_COLS = 512;
+    static constexpr int TMEM_COLS = D + NSB * TK + (QSM ? 0 : D / 2) <= 256 ? 256 : 512;
+    static constexpr int CTAS = TMEM_COLS == 256 ? 2 : 1;  // per SM
     static constexpr int O_COL = 0;
     static constexpr int S_COL = D;
     static constexpr int Q_COL = D + NSB * TK;
@@ -350,7 +352,8 @@ constexpr float kExactLogits = 16777216.f;
 // mask, a row per sequence and head.
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
           bool FAR = false, bool SH = false>
-__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS, 1)
+__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS,
+                                  VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::CTAS)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
                         const VerifyParams p) {
@@ -530,8 +533,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
         L = 0;
     }
     const int n_chunks = (L + kChunk - 1) / kChunk;
-    // SH: splits of whole 64-token tiles of the group's own prefix
-    const int cps = SH ? (n_chunks + 4 * p.prefix_splits - 1) / (4 * p.prefix_splits) * 4 : p.chunks_per_split;
+    // SH: splits of whole 64-token tiles of the group's own prefix, as long as planned or longer
+    const int cps = SH ? max(p.prefix_chunks, (n_chunks + 4 * p.prefix_splits - 1) / (4 * p.prefix_splits) * 4)
+                       : p.chunks_per_split;
     // with a sliding window the splits start at the chunk of the block's first
     // visible key (its first row's window start)
     const int k_first = !SH && p.window > 0 ? max(0, L - p.q_len + row0 / G - p.window + 1) : 0;
