@@ -470,8 +470,8 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
  *   max_suffix_len  about the longest prefix and the most tokens that a sequence
  *                   has beyond it: they plan the splits and bound nothing; 0 =
  *                   max_seq_len of the description
- *   prefix_splits   0 = automatic; > 0 forces the splits of the prefixes (the
- *                   description's num_splits those of the own parts) */
+ *   prefix_splits   0 = automatic; > 0 forces the sharing, and the splits of the
+ *                   prefixes (the description's num_splits those of the own parts) */
 typedef struct {
     int32_t num_groups;
     int32_t max_group_seqs;
@@ -480,28 +480,34 @@ typedef struct {
     int32_t prefix_splits;
 } pa_prefix_desc;
 
-/* Bytes of device workspace that a shared-prefix decode needs (never 0 for a
- * batch that is not empty); (size_t)-1 if the description is invalid.  Host
- * only; what pa_workspace_bytes says of the workspace holds here too. */
+/* Bytes of device workspace that a shared-prefix decode needs, over any kind of
+ * cache; (size_t)-1 if the description is invalid.  Host only; what
+ * pa_workspace_bytes says of the workspace holds here too. */
 size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc *prefix);
 
 /* paged_attention_decode_shared -- the result of pa_paged_attention_decode (up
- * to rounding), where the first prefix_lens[b] tokens of sequence b, rounded down
- * to a multiple of 16, stand in the pages of its group's first sequence that is
- * not idle: for tokens t below that, its row of the block table is read, and the
- * other sequences' entries are not.  prefix_lens[b] is the same throughout a
- * group, and at most seq_lens[b] (a group without a common part has 0; any length
- * serves, also one that ends inside a page).  seq_lens[b] == 0 is an idle sequence:
- * a zero row whatever its prefix_lens says.  A sequence whose length is out of
- * range, or whose prefix_lens is negative, longer than it or not its group's, is
- * PA_DEV_BAD_SEQLEN and a zero row, as is one that no group has; group_starts
- * that do not ascend give zero rows throughout (PA_DEV_BAD_SEQLEN).  A NaN in q or
- * in a visible key makes the outputs that depend on it NaN, and no others.
- * PA_FLAG_EARLY_KV_READ is accepted and changes nothing; a window is refused
- * (PA_ERR_UNSUPPORTED).
+ * to rounding) for sequences of which those of a group have the same K and V for
+ * their first prefix_lens[b] tokens, rounded down to a multiple of 16: their
+ * rows of the block table lead to the same pages for them, or to copies (as
+ * pa_fork_block_tables leaves them).  Those tokens are read once per group,
+ * through the row of its first sequence that is not idle; where that would save
+ * too little (about 12 MB of a bf16 cache by the description) every sequence
+ * reads them through its own row.
+ * prefix_lens[b] is the same throughout a group, and at most seq_lens[b]; a group
+ * without a common part has 0, and any length serves, also one that ends inside a
+ * page.  seq_lens[b] == 0 is an idle sequence: a zero row whatever its
+ * prefix_lens says.  A sequence whose length is out of range, or whose prefix_lens
+ * is negative, longer than it or not its group's, is PA_DEV_BAD_SEQLEN and a zero
+ * row, as is one that no group has; group_starts that do not ascend give zero
+ * rows throughout (PA_DEV_BAD_SEQLEN).  A bad page of a prefix zeroes the rows of
+ * those that read it.  A NaN in q or in a visible key makes the outputs that
+ * depend on it NaN, and no others.  fp32 outputs are summed so that they lose
+ * about 1e-6 of themselves at any length.  PA_FLAG_EARLY_KV_READ is accepted and
+ * changes nothing; a window is refused (PA_ERR_UNSUPPORTED).
  *   group_starts  device int32 [num_groups + 1], 0 .. num_seqs ascending
  *   prefix_lens   device int32 [num_seqs]
- *   workspace     device, >= pa_shared_workspace_bytes(desc, prefix) bytes
+ *   workspace     device, >= pa_shared_workspace_bytes(desc, prefix) bytes (may
+ *                 be NULL if 0)
  * Other arguments, results and errors as for pa_paged_attention_decode; head
  * layouts and head_dim as there. */
 pa_status pa_paged_attention_decode_shared(const void *q, const void *k_cache, const void *v_cache,

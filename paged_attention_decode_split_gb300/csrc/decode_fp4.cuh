@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 127) & ~uintptr_t(127));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page, [2] SH: no place in a group
     float2 *merge_ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
     uint4 *q_frag = reinterpret_cast<uint4 *>(smem + C::OFF_Q);
@@ -152,11 +152,12 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     if (threadIdx.x == 0) {
         flags[0] = 0;
         flags[1] = 0;
+        flags[2] = 0;
     }
     // Every global access waits for the work before this call, except that
     // early_kv lets the block table, seq_lens and the chunks wholly before the
     // new row go first.
-    if (!SH && !p.early_kv) pdl_wait_primary();
+    if (SH ? p.prefix_splits == 0 : !p.early_kv) pdl_wait_primary();
 
     // Q^T as B fragments, in f16: n-tile nt, k-step ks -> dims 16 ks + 4c (+1)
     // and 16 ks + 4c + 2 (+3) of head 8 nt + r; warp nt lays its tile out.  Its
@@ -219,11 +220,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
             n_my = 0;
             if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
         }
-        if (split == 0 && !prefix_covers(p, b, C::THREADS)) {
-            own_ok = false;
-            if (threadIdx.x == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
-            poison_prefix_records(p, b, hq0, G, C::THREADS);
-        }
+        if (n_my <= 0 && split == 0 && warp == 0 && !group_ok(p, b, L, hq0, G, kvh == 0)) own_ok = false;
     }
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
@@ -335,6 +332,9 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     }
     if (my_first && !issued) issue(lane >> 1);
 
+    if constexpr (SH) {
+        if (split == 0 && warp == NW - 1 && !group_ok(p, b, L, hq0, G, kvh == 0) && lane == 0) flags[2] = 1;
+    }
     // (an mbarrier rather than a CTA barrier: a warp whose copies the copy engine has yet to take holds no other up)
     bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, &flags[0]));
     if (!ok) flags[0] = 1;
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
                 merge_ml[warp * GMAX + nt * 8 + 2 * c + j] = make_float2(m_run[nt][j], l_run[nt][j]);
     }
     __syncthreads();  // every chunk is consumed: the stages become the merge area
-    const bool poisoned = flags[0] != 0 || flags[1] != 0 || (SH && !own_ok);
+    const bool poisoned = flags[0] != 0 || flags[1] != 0 || (SH && flags[2] != 0);
     const int n_act = min(NW, n_my);  // warps that had a chunk
     float *macc = reinterpret_cast<float *>(smem);  // [NW][G][HS]
 #pragma unroll

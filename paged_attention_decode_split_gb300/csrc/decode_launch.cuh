@@ -7,7 +7,7 @@
 
 namespace pa {
 
-template <int D, int G, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, bool SH = false>
+template <int D, int G, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, bool SH = false, int PT = 2, bool FAR = false>
 cudaError_t launch_decode_mma_t(const CUtensorMap &tk, const CUtensorMap &tv, const DecodeParams &p, dim3 grid,
                                 cudaStream_t stream, int slot) {
     constexpr int NT = G > 8 ? 2 : 1;
@@ -16,7 +16,7 @@ cudaError_t launch_decode_mma_t(const CUtensorMap &tk, const CUtensorMap &tv, co
     // (hybrid bf16 within noise, fp8 slower, and more chunks slower for all)
     constexpr int PF = (D == 128 && !F8 && !SH) ? 6 : 0;
     using C = MmaCfg<D, NT, NST, SPS, DS, F8>;
-    auto kern = pa_decode_mma_kernel<D, G, NT, NST, SPS, DS, WIN, F8, LP, PF, SH>;
+    auto kern = pa_decode_mma_kernel<D, G, NT, NST, SPS, DS, WIN, F8, LP, PF, SH, PT, FAR>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // Programmatic dependent launch: the kernel's set-up overlaps the previous
@@ -58,24 +58,24 @@ cudaError_t launch_decode_mma_t(const CUtensorMap &tk, const CUtensorMap &tv, co
 //    bytes at 255 registers.
 //  * fp8, D = 128: 4 KiB stages; 12 streams x 4 stages, a lane per stream;
 //    12 and 16 heads: 6 x 8, one warp per chunk (registers, as above).
-template <bool WIN, bool F8, bool SH = false>
+template <bool WIN, bool F8, bool SH = false, int PT = 2, bool FAR = false>
 cudaError_t launch_decode_cfg(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                               const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     // shared-memory limit bookkeeping: one slot per kernel
-    constexpr int slot0 = SH ? 160 + (F8 ? 20 : 0) : (WIN ? 20 : 0) + (F8 ? 40 : 0);
+    constexpr int slot0 = SH ? 160 + (F8 ? 20 : 0) + (FAR ? 80 : 0) : (WIN ? 20 : 0) + (F8 ? 40 : 0);
 #define PA_DECODE_CASES(D, NST, SPS, DS, LP, NST2, SPS2, DS2, S0)                                             \
     switch (group) {                                                                                          \
-        case 1: return launch_decode_mma_t<D, 1, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 0);  \
-        case 2: return launch_decode_mma_t<D, 2, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 1);  \
-        case 3: return launch_decode_mma_t<D, 3, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 2);  \
-        case 4: return launch_decode_mma_t<D, 4, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 3);  \
-        case 5: return launch_decode_mma_t<D, 5, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 4);  \
-        case 6: return launch_decode_mma_t<D, 6, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 5);  \
-        case 8: return launch_decode_mma_t<D, 8, NST, SPS, DS, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 6);  \
+        case 1: return launch_decode_mma_t<D, 1, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 0);  \
+        case 2: return launch_decode_mma_t<D, 2, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 1);  \
+        case 3: return launch_decode_mma_t<D, 3, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 2);  \
+        case 4: return launch_decode_mma_t<D, 4, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 3);  \
+        case 5: return launch_decode_mma_t<D, 5, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 4);  \
+        case 6: return launch_decode_mma_t<D, 6, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 5);  \
+        case 8: return launch_decode_mma_t<D, 8, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 6);  \
         case 12:                                                                                              \
-            return launch_decode_mma_t<D, 12, NST2, SPS2, DS2, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 7); \
+            return launch_decode_mma_t<D, 12, NST2, SPS2, DS2, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 7); \
         case 16:                                                                                              \
-            return launch_decode_mma_t<D, 16, NST2, SPS2, DS2, WIN, F8, LP, SH>(tk, tv, p, grid, stream, S0 + 8); \
+            return launch_decode_mma_t<D, 16, NST2, SPS2, DS2, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 8); \
     }                                                                                                         \
     return cudaErrorInvalidValue;
     if constexpr (SH && F8) {

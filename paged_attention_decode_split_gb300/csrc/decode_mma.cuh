@@ -191,18 +191,28 @@ __device__ __forceinline__ void append_new_row(const DecodeParams &p, int b, int
 // this kernel has waited for both.  Two CTAs per SM (up to 8 heads), each with
 // half a ring: own parts are short, and one CTA's table, first copies and merge
 // then pass behind the other's copies.
-template <int D, int G, int NT, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, int PF = 0, bool SH = false>
+// PT: the numbers a softmax weight enters the product as: 2 (head and residual),
+// over an e4m3 cache 1 for bf16 outputs (one f16: off by half a step, 2^-11 of
+// itself, an eighth of the half step that the output is rounded by), over a bf16
+// cache 3 for fp32 outputs (two residuals: 2^-26).  FAR: the accumulators, which
+// the tensor core cuts off towards zero at every addition, 2.4e-9 of the sum per
+// key, are moved to a second sum every kFarChunks chunks of a stream (fp32 outputs;
+// 128 keys: 3e-7).
+constexpr int kFarChunks = 8;
+template <int D, int G, int NT, int NST, int SPS, int DS, bool WIN, bool F8, bool LP, int PF = 0, bool SH = false, int PT = 2,
+          bool FAR = false>
 __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     pa_decode_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const DecodeParams p) {
     using C = MmaCfg<D, NT, NST, SPS, DS, F8>;
     constexpr int NS = C::NS, NWC = C::NWC, KS = C::KS, MTW = C::MTW, HS = C::HS, GMAX = C::GMAX;
     static_assert(G <= GMAX && G > GMAX - 8, "n-tiles match the group");
+    static_assert(PT == 2 || (PT == 1 && F8) || (PT == 3 && !F8), "numbers per weight");
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *empty = full + NS;
-    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page
+    volatile int *flags = reinterpret_cast<volatile int *>(smem + C::OFF_FLAGS);  // [0] abort, [1] bad page, [2] SH: no place in a group
     float2 *merge_ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     float *merge_w = reinterpret_cast<float *>(smem + C::OFF_W);
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
@@ -224,13 +234,14 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
         }
         flags[0] = 0;
         flags[1] = 0;
+        flags[2] = 0;
         fence_mbar_init();
     }
     if (warp == NWC && lane == 0) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
-    if (!SH && !p.early_kv) pdl_wait_primary();
+    if (SH ? p.prefix_splits == 0 : !p.early_kv) pdl_wait_primary();
 
     int L = p.seq_lens[b];
     const int record = SH ? p.prefix_splits + split : split;  // of the row's num_splits
@@ -265,11 +276,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
             n_my = 0;
             if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
         }
-        if (split == 0 && !prefix_covers(p, b, C::THREADS)) {
-            own_ok = false;
-            if (threadIdx.x == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
-            poison_prefix_records(p, b, hq0, G, C::THREADS);
-        }
+        if (n_my <= 0 && split == 0 && warp == 0 && !group_ok(p, b, L, hq0, G, kvh == 0)) own_ok = false;
     }
     if (n_my <= 0) {
         // no key of this sequence in this split: the record says so (m = -inf,
@@ -291,6 +298,10 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     const int r = lane >> 2, c = lane & 3;
     float m_run[NT][2], l_run[NT][2];
     float oacc[MTW][NT][4];
+    // the second sum: in registers where they hold it, else in local memory with the maxima that it stands for
+    constexpr bool FARR = FAR && !F8 && NT == 1, FARL = FAR && !FARR;
+    [[maybe_unused]] float ofar[FARR ? MTW : 1][NT][4];
+    [[maybe_unused]] volatile float lfar[FARL ? MTW * NT * 4 : 1], mfar[FARL ? NT * 2 : 1];
 
     if (warp == NWC) {
         // ---------------- producer: PL lanes issue the copies ----------------
@@ -412,6 +423,9 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     }
 
     // ---------------- consumers ----------------
+    if constexpr (SH) {
+        if (split == 0 && warp == 0 && !group_ok(p, b, L, hq0, G, kvh == 0) && lane == 0) flags[2] = 1;
+    }
     // Q^T as B fragments: n-tile nt, k-step ks -> {b0b1, b2b3} for head
     // 8 nt + r.  bf16: dims 16 ks + 2c (+1) and 16 ks + 8 + 2c (+1).  fp8 (the
     // permuted k order): dims 16 ks + 4c (+1) and 16 ks + 4c + 2 (+3), in f16.
@@ -460,8 +474,18 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
 #pragma unroll
         for (int mt = 0; mt < MTW; ++mt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) oacc[mt][nt][i] = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                oacc[mt][nt][i] = 0.f;
+                if constexpr (FARR) ofar[mt][nt][i] = 0.f;
+                if constexpr (FARL) lfar[(mt * NT + nt) * 4 + i] = 0.f;
+            }
+        if constexpr (FARL) mfar[2 * nt] = mfar[2 * nt + 1] = -INFINITY;
     }
+    // what a sum that stands for maximum m becomes relative to the present one
+    [[maybe_unused]] auto far_weight = [&](int nt, int j) {
+        const float m = mfar[2 * nt + j];
+        return m == m_run[nt][j] ? 1.f : fast_exp2(m - m_run[nt][j]);
+    };
 
     // ldmatrix row addresses (byte offsets inside a chunk), for the 16-byte
     // unit pair starting at an even unit 2j of a column block: lanes 8m..8m+7
@@ -565,12 +589,17 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
                         for (int mt = 0; mt < MTW; ++mt) {
                             oacc[mt][nt][j] *= alpha;
                             oacc[mt][nt][j + 2] *= alpha;
+                            if constexpr (FARR) {
+                                ofar[mt][nt][j] *= alpha;
+                                ofar[mt][nt][j + 2] *= alpha;
+                            }
                         }
                     }
                 }
         }
         // P^T fragments: head + residual, each transposed in registers
-        uint32_t bh[NT][2], bl[NT][2];
+        uint32_t bh[NT][2];
+        [[maybe_unused]] uint32_t bl[NT][2], bm[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float pr[4];
@@ -578,8 +607,18 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
             for (int q = 0; q < 4; ++q) pr[q] = fast_exp2(x[nt][q] - m_run[nt][q & 1]);  // 0 for masked rows
             l_run[nt][0] += pr[0] + pr[2];
             l_run[nt][1] += pr[1] + pr[3];
-            uint32_t h01, h23, r01, r23;
-            if constexpr (F8) {
+            uint32_t h01, h23;
+            [[maybe_unused]] uint32_t r01, r23;
+            if constexpr (PT == 1) {
+                h01 = pack_f16(pr[0], pr[1]);
+                h23 = pack_f16(pr[2], pr[3]);
+            } else if constexpr (PT == 3) {
+                uint32_t s01, s23;
+                split3_bf16(pr[0], pr[1], h01, r01, s01);
+                split3_bf16(pr[2], pr[3], h23, r23, s23);
+                bm[nt][0] = mm::movt(s01);
+                bm[nt][1] = mm::movt(s23);
+            } else if constexpr (F8) {
                 split_f16(pr[0], pr[1], h01, r01);
                 split_f16(pr[2], pr[3], h23, r23);
             } else {
@@ -588,8 +627,10 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
             }
             bh[nt][0] = mm::movt(h01);
             bh[nt][1] = mm::movt(h23);
-            bl[nt][0] = mm::movt(r01);
-            bl[nt][1] = mm::movt(r23);
+            if constexpr (PT > 1) {
+                bl[nt][0] = mm::movt(r01);
+                bl[nt][1] = mm::movt(r23);
+            }
         }
 
         // ---- O^T += V^T P^T over this warp's m16 tiles of d ----
@@ -623,6 +664,8 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
                     for (int nt = 0; nt < NT; ++nt) {
                         mm::mma<false>(oacc[mt][nt], a[0], a[1], a[2], a[3], bh[nt][0], bh[nt][1]);
                         mm::mma<false>(oacc[mt][nt], a[0], a[1], a[2], a[3], bl[nt][0], bl[nt][1]);
+                        if constexpr (PT == 3)
+                            mm::mma<false>(oacc[mt][nt], a[0], a[1], a[2], a[3], bm[nt][0], bm[nt][1]);
                     }
                 }
             } else {
@@ -645,7 +688,8 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mm::mma<true>(oacc[mt + u][nt], a0, a2, a4, a6, bh[nt][0], bh[nt][1]);
-                            mm::mma<true>(oacc[mt + u][nt], a0, a2, a4, a6, bl[nt][0], bl[nt][1]);
+                            if constexpr (PT > 1)
+                                mm::mma<true>(oacc[mt + u][nt], a0, a2, a4, a6, bl[nt][0], bl[nt][1]);
                         }
                     }
                 }
@@ -657,6 +701,54 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
             pv(std::false_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
+        if constexpr (FARR) {
+            if ((k + 1) % kFarChunks == 0) {
+#pragma unroll
+                for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        ofar[mt][0][q] += oacc[mt][0][q];
+                        oacc[mt][0][q] = 0.f;
+                    }
+            }
+        }
+        if constexpr (FARL) {
+            if ((k + 1) % kFarChunks == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float w[2] = {far_weight(nt, 0), far_weight(nt, 1)};
+#pragma unroll
+                    for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            volatile float &f = lfar[(mt * NT + nt) * 4 + q];
+                            f = fmaf(f, w[q & 1], oacc[mt][nt][q]);
+                            oacc[mt][nt][q] = 0.f;
+                        }
+                    mfar[2 * nt] = m_run[nt][0];
+                    mfar[2 * nt + 1] = m_run[nt][1];
+                }
+            }
+        }
+    }
+    if constexpr (FARR) {
+#pragma unroll
+        for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) oacc[mt][0][q] += ofar[mt][0][q];
+    }
+    if constexpr (FARL) {
+        if (n_my > NST * (kFarChunks - 1)) {  // (some stream of the CTA may have moved its sums)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float w[2] = {far_weight(nt, 0), far_weight(nt, 1)};
+#pragma unroll
+                for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        oacc[mt][nt][q] = fmaf(lfar[(mt * NT + nt) * 4 + q], w[q & 1], oacc[mt][nt][q]);
+            }
+        }
     }
     // exponential sums: a lane holds tokens r and r + 8; sum over r
 #pragma unroll
@@ -673,7 +765,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     // ---- CTA merge of the streams' states (log-sum-exp weights) ----
     named_bar_sync(1, NWC * 32);  // every chunk is consumed: the stages become the merge area
     const bool aborted = flags[0] != 0;
-    const bool poisoned = aborted || flags[1] != 0 || (SH && !own_ok);
+    const bool poisoned = aborted || flags[1] != 0 || (SH && flags[2] != 0);
     float *macc = reinterpret_cast<float *>(smem);  // [NST][G][HS], unnormalised sums
 #pragma unroll
     for (int mt = 0; mt < MTW; ++mt) {
@@ -717,7 +809,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
         }
         const bool zero = poisoned || !(lsum > 0.f);
         const float norm = zero ? 0.f : (F8 ? p.v_scale[kvh] / lsum : 1.f / lsum);
-        if (SH && sum_nan) {
+        if (SH && sum_nan && !poisoned) {
             // a NaN (in q or in a visible key) goes on as a NaN row with max 0 and sum 1: the reduce takes a sum
             // that is not > 0 for an empty split
             for (int st = 0; st < NST; ++st) merge_w[st * GMAX + h] = NAN;
@@ -741,6 +833,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
             o.z = fmaf(v.z, wg, o.z);
             o.w = fmaf(v.w, wg, o.w);
         }
+        if (SH && poisoned) o = make_float4(0.f, 0.f, 0.f, 0.f);  // (whatever the sums are)
         const size_t row = (size_t)b * p.num_q_heads + hq0 + h;
         if (p.num_splits == 1) {
             store_out(p.out, row * D + d, o.x, p.out_bf16);

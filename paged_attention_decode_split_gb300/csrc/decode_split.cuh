@@ -56,10 +56,12 @@ struct DecodeParams {
     // Decode over shared prefixes (SH kernels): sequence b attends here to the
     // tokens from prefix_lens[b], rounded down to whole chunks, on, cut into
     // suffix_splits splits of its own length; their records stand behind the
-    // prefix_splits records of the prefix kernel.
+    // prefix_splits records of the prefix kernel.  prefix_splits = 0: there is no
+    // prefix kernel, and all tokens are read here.
     const int32_t *prefix_lens;   // [B]
     const int32_t *group_starts;  // [num_groups + 1]
     int num_groups;
+    int max_members;
     int prefix_splits;
     int suffix_splits;
     int suffix_chunks;  // of a split, where that makes no more than suffix_splits
@@ -76,7 +78,7 @@ __device__ __forceinline__ Suffix suffix_of(const DecodeParams &p, int b, int L)
     const int P = p.prefix_lens[b];
     Suffix s{0, 1, L == 0 || (P >= 0 && P <= L)};
     if (L > 0 && s.ok) {
-        s.first = P / kChunk;
+        s.first = p.prefix_splits > 0 ? P / kChunk : 0;
         const int n = (L + kChunk - 1) / kChunk - s.first;
         s.per = max(p.suffix_chunks, (n + p.suffix_splits - 1) / p.suffix_splits);
     }
@@ -89,25 +91,41 @@ __device__ __forceinline__ void wait_prefix(bool last_cta) {
     if (last_cta) pdl_wait_primary();
 }
 
-// Whether group_starts ascends and has sequence b in a group: then the prefix
-// kernel writes b's records.  Every thread of the CTA; asked by the CTAs of a
-// sequence's first split.
-__device__ __forceinline__ bool prefix_covers(const DecodeParams &p, int b, int threads) {
-    bool in = false, order = true;
-    for (int g = threadIdx.x; g < p.num_groups; g += threads) {
-        const int lo = p.group_starts[g], hi = p.group_starts[g + 1];
-        in |= lo <= b && b < hi;
-        order &= lo >= 0 && lo <= hi;
+// Whether sequence b has a place in a group that makes sense: group_starts
+// ascends, b is among the first max_members of its group, and its prefix is that
+// of the group's first sequence that is not idle.  By one whole warp, for the CTAs
+// of a sequence's first split; otherwise (status set) the records that the prefix
+// kernel may not write are poisoned, so that b's rows become zeros.
+__device__ __forceinline__ bool group_ok(const DecodeParams &p, int b, int L, int hq0, int heads, bool report) {
+    const int lane = threadIdx.x & 31;
+    int lo = -1, hi = -1;
+    bool order = true;
+    for (int g = lane; g < p.num_groups; g += 32) {
+        const int x = p.group_starts[g], y = p.group_starts[g + 1];
+        if (x <= b && b < y) {
+            lo = x;
+            hi = y;
+        }
+        order &= x >= 0 && x <= y;
     }
-    return (__syncthreads_or(in) != 0) & (__syncthreads_or(!order) == 0);
-}
-
-// The records of a sequence that no prefix CTA writes, or whose own lengths are
-// bad: poisoned, so that its rows become zeros.
-__device__ __forceinline__ void poison_prefix_records(const DecodeParams &p, int b, int hq0, int heads, int threads) {
-    for (int i = threadIdx.x; i < heads * p.prefix_splits; i += threads)
-        p.part_ml[((size_t)b * p.num_q_heads + hq0 + i / p.prefix_splits) * p.num_splits + i % p.prefix_splits] =
-            make_float2(-INFINITY, -1.f);
+    lo = __reduce_max_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    bool ok = __all_sync(0xffffffffu, order) && lo >= 0 && b - lo < p.max_members;
+    const bool written = ok;  // by the prefix kernel
+    for (int i0 = lo; ok && L != 0 && i0 < hi; i0 += 32) {
+        const int i = i0 + lane, len = i < hi ? p.seq_lens[i] : 0;
+        const uint32_t live = __ballot_sync(0xffffffffu, len > 0 && len <= p.max_seq_len);
+        if (live != 0) {
+            ok = p.prefix_lens[i0 + __ffs(live) - 1] == p.prefix_lens[b];
+            break;
+        }
+    }
+    if (!ok && report && lane == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
+    if (!written)
+        for (int i = lane; i < heads * p.prefix_splits; i += 32)
+            p.part_ml[((size_t)b * p.num_q_heads + hq0 + i / p.prefix_splits) * p.num_splits + i % p.prefix_splits] =
+                make_float2(-INFINITY, -1.f);
+    return ok;
 }
 
 __device__ __forceinline__ void store_out(void *out, size_t idx, float v, int out_bf16) {

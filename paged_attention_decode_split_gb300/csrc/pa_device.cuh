@@ -176,6 +176,14 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t &head, uin
     resid = pack_bf16(r.x, r.y);
 }
 
+// The same with two residuals: about 25 significant bits.
+__device__ __forceinline__ void split3_bf16(float a, float b, uint32_t &head, uint32_t &resid, uint32_t &rest) {
+    head = pack_bf16(a, b);
+    const float2 h = make_float2(__uint_as_float(head << 16), __uint_as_float(head & 0xffff0000u));
+    const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), make_float2(a, b));
+    split_bf16(r.x, r.y, resid, rest);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);

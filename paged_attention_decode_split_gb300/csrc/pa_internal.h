@@ -46,11 +46,19 @@ cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const C
                           const VerifyParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_prefix_fp8(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
                               const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_prefix_f32(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                              const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_prefix_fp8_f32(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                                  const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_prefix_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_shared(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_fp8_shared(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                                      const DecodeParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_shared_f32(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                     const DecodeParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_fp8_shared_f32(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                         const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_fp4_shared(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream);
 
 // Sets the dynamic shared-memory limit of `fn` once per device.

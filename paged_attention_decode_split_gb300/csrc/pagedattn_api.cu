@@ -25,9 +25,10 @@ namespace {
 
 constexpr int kMaxChunksPerSplit = 256; // 4096 tokens: bounds the longest CTA for load balance
 constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tokens
-constexpr int kMaxPrefixChunksF32 = 128;  // and 2048 at most for fp32 outputs
+constexpr int kMaxOwnChunks = 64;         // a split of a sequence's own part, where SMs are left: 1024 tokens
+constexpr int64_t kMinShared = 6 << 20;   // elements of K that sharing must save
 constexpr int kMaxDevices = 64;
-constexpr int kKernelSlots = 256;
+constexpr int kKernelSlots = 288;
 
 thread_local pa_plan_info g_last_plan;
 thread_local bool g_have_plan = false;
@@ -172,39 +173,40 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
     const int all = (d->max_seq_len + kChunk - 1) / kChunk;
     pl->num_sms = sms;
     pl->row_blocks = static_cast<int>(blocks);
+    const int np = chunks(x->max_prefix_len), ns = chunks(x->max_suffix_len);
+    auto tiles = [](int n, int splits) { return (std::max(1, (n + splits - 1) / splits) + 3) & ~3; };
+    // Where sharing saves little, its launch costs more: every sequence reads the prefix for itself then.
+    const int64_t saved = std::max<int64_t>(0, static_cast<int64_t>(d->num_seqs) - x->num_groups) * np * kChunk *
+                          d->num_kv_heads * d->head_dim;
+    const bool direct = x->prefix_splits == 0 && saved < kMinShared;
     // the prefix: whole waves of CTAs, splits of whole 64-token tiles
-    const int np = chunks(x->max_prefix_len);
     const int64_t units = std::max<int64_t>(1, x->num_groups * blocks * d->num_kv_heads);
     int sp = x->prefix_splits;
     if (sp == 0) {
         sp = static_cast<int>(std::max<int64_t>(1, sms / units));
         sp = std::min(sp, std::max(1, np / kMinPrefixChunks));
-        // the tensor core cuts each addition to an accumulator off towards zero, 2.4e-9 of the sum per key: fp32
-        // outputs keep a split's share below 5e-6
-        if (d->out_dtype == PA_OUT_F32) sp = std::max(sp, (np + kMaxPrefixChunksF32 - 1) / kMaxPrefixChunksF32);
-        const int per = (std::max(1, (np + sp - 1) / sp) + 3) & ~3;
+        const int per = tiles(np, sp);
         sp = std::max(1, (np + per - 1) / per);
     }
-    auto tiles = [](int n, int splits) { return (std::max(1, (n + splits - 1) / splits) + 3) & ~3; };
-    pl->prefix_splits = std::min(sp, std::max(1, all));
-    pl->prefix_chunks = tiles(np, pl->prefix_splits);
-    pl->prefix_most = std::max(pl->prefix_chunks, tiles(all, pl->prefix_splits));
+    pl->prefix_splits = direct ? 0 : std::min(sp, std::max(1, all));
+    pl->prefix_chunks = direct ? 0 : tiles(np, pl->prefix_splits);
+    pl->prefix_most = direct ? 0 : std::max(pl->prefix_chunks, tiles(all, pl->prefix_splits));
     // the own parts: as the decode's
-    const int ns = chunks(x->max_suffix_len);
+    const int own = direct ? std::min(np + ns, all) : ns;
     const int64_t seqs = std::max<int64_t>(1, static_cast<int64_t>(d->num_seqs) * d->num_kv_heads);
     int ss = d->num_splits;
     if (ss == 0) {
         ss = static_cast<int>(std::max<int64_t>(1, sms / seqs));
-        ss = std::min(ss, std::max(1, ns / kMinChunksPerSplit));
-        if (seqs < sms) ss = std::max(ss, (ns + kMaxChunksPerSplit - 1) / kMaxChunksPerSplit);
-        const int per = std::max(1, (ns + ss - 1) / ss);
-        ss = std::max(1, (ns + per - 1) / per);
+        ss = std::min(ss, std::max(1, own / kMinChunksPerSplit));
+        if (seqs < 4 * sms) ss = std::max(ss, (own + kMaxOwnChunks - 1) / kMaxOwnChunks);
+        const int per = std::max(1, (own + ss - 1) / ss);
+        ss = std::max(1, (own + per - 1) / per);
     }
     pl->suffix_splits = std::min(ss, std::max(1, all));
-    pl->suffix_chunks = std::max(kMinChunksPerSplit, (ns + pl->suffix_splits - 1) / pl->suffix_splits);
+    pl->suffix_chunks = std::max(kMinChunksPerSplit, (own + pl->suffix_splits - 1) / pl->suffix_splits);
     pl->suffix_most = std::max(pl->suffix_chunks, (all + pl->suffix_splits - 1) / pl->suffix_splits);
-    const size_t records =
-        static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits + pl->suffix_splits);
+    size_t records = static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits + pl->suffix_splits);
+    if (pl->prefix_splits + pl->suffix_splits == 1) records = 0;  // (the outputs themselves)
     pl->off_part_ml = round256(records * d->head_dim * sizeof(float));
     pl->ws_bytes = pl->off_part_ml + records * sizeof(float2);
     return PA_OK;
@@ -874,7 +876,8 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     if (!group_starts || !prefix_lens || (reinterpret_cast<uintptr_t>(group_starts) & 3u) ||
         (reinterpret_cast<uintptr_t>(prefix_lens) & 3u))
         return PA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    if (pl.ws_bytes > 0 && (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)))
+        return PA_ERR_WORKSPACE;
     const int group = desc->num_q_heads / desc->num_kv_heads;
     const int rows = std::min(prefix->max_group_seqs, desc->num_seqs) * group;
     CUtensorMap tk, tv;
@@ -940,12 +943,14 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     d.prefix_lens = prefix_lens;
     d.group_starts = group_starts;
     d.num_groups = prefix->num_groups;
+    d.max_members = p.max_members;
     d.prefix_splits = pl.prefix_splits;
     d.suffix_splits = pl.suffix_splits;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 pgrid(pl.prefix_splits, desc->num_kv_heads * pl.row_blocks, prefix->num_groups);
-    cudaError_t e = fp4   ? launch_prefix_fp4(desc->head_dim, p, pgrid, s)
+    cudaError_t e = pl.prefix_splits == 0 ? cudaSuccess
+                    : fp4 ? launch_prefix_fp4(desc->head_dim, p, pgrid, s)
                     : fp8 ? launch_prefix_fp8(desc->head_dim, maps.k, maps.v, maps.k64, maps.v64, p, pgrid, s)
                           : launch_prefix(desc->head_dim, rows, maps.k, maps.v, maps.k64, maps.v64, maps.k128, p, pgrid,
                                           s);
@@ -955,14 +960,16 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
         : fp8 ? launch_decode_fp8_shared(desc->head_dim, group, tk, tv, d, sgrid, s)
               : launch_decode_shared(desc->head_dim, group, tk, tv, d, sgrid, s);
     if (e != cudaSuccess) return PA_ERR_CUDA;
-    ReduceParams r;
-    r.part_o = p.part_o;
-    r.part_ml = p.part_ml;
-    r.out = out;
-    r.num_q_heads = desc->num_q_heads;
-    r.num_splits = p.num_splits;
-    r.out_bf16 = p.out_bf16;
-    if (launch_reduce_rows(desc->head_dim, r, desc->num_seqs, pl.num_sms, s) != cudaSuccess) return PA_ERR_CUDA;
+    if (p.num_splits > 1) {
+        ReduceParams r;
+        r.part_o = p.part_o;
+        r.part_ml = p.part_ml;
+        r.out = out;
+        r.num_q_heads = desc->num_q_heads;
+        r.num_splits = p.num_splits;
+        r.out_bf16 = p.out_bf16;
+        if (launch_reduce_rows(desc->head_dim, r, desc->num_seqs, pl.num_sms, s) != cudaSuccess) return PA_ERR_CUDA;
+    }
     const Plan told{pl.num_sms, p.num_splits, pl.suffix_chunks, 0, 0};
     record_plan(PA_PATH_DECODE_SHARED, told, desc,
                 static_cast<int>(pgrid.x * pgrid.y * pgrid.z + sgrid.x * sgrid.y * sgrid.z));

@@ -7,12 +7,12 @@
 
 namespace pa {
 
-template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool SH = false>
+template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool SH = false, bool FAR = false, int PT = 2>
 cudaError_t launch_verify_tc(const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
                              const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream,
                              int slot) {
-    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK>;
-    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, NSB, TK, false, true, false, SH>;
+    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK, false, PT>;
+    auto kern = pa_verify_tc_kernel<D, NK, NV, NSG, NSB, TK, false, (PT > 1), FAR, SH, PT>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), C::SMEM_BYTES, slot);
     if (e != cudaSuccess) return e;
     // programmatic dependent launch: the set-up overlaps the work before it

@@ -1,15 +1,19 @@
 // verify_launch_shared.cu -- the tensor-core kernel as the common part of a
-// decode over shared prefixes, bf16 and e4m3 caches, in a translation unit of its
-// own so it compiles in parallel with the rest.
+// decode over shared prefixes, bf16 and e4m3 caches, bf16 outputs, in a
+// translation unit of its own so it compiles in parallel with the rest.
 #include "verify_launch.cuh"
 
 namespace pa {
 
 // rows: what the largest group may have, sequences x heads of the group.  The
-// layouts are the verify's (verify_launch.cu).
+// layouts are the verify's (verify_launch.cu), but for one block of rows at
+// head_dim 128: one S/P buffer, 256 tensor-memory columns and half the rings, so
+// that two CTAs share an SM and one's set-up and epilogue pass behind the other's
+// tiles (16 groups of 8 sequences x 4 heads behind 1K-8K: 122 us, 105 so).
 cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tk64, const CUtensorMap &tv64, const CUtensorMap &tk128,
                           const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (!p.out_bf16) return launch_prefix_f32(head_dim, tk, tv, tk64, tv64, p, grid, stream);
     const bool wide = verify_wide_score_tiles(head_dim, rows);
     if (head_dim == 256)
         return wide ? launch_verify_tc<256, 1, 3, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 224)
@@ -20,12 +24,14 @@ cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const C
     return cudaErrorInvalidValue;
 }
 
+// bf16 outputs: a weight enters the product as one f16.
 cudaError_t launch_prefix_fp8(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
                               const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (!p.out_bf16) return launch_prefix_fp8_f32(head_dim, tk, tv, tk64, tv64, p, grid, stream);
     if (head_dim == 256)
-        return launch_verify_tc<256, 2, 3, 2, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 228);
+        return launch_verify_tc<256, 2, 3, 2, 2, 64, true, false, 1>(tk, tv, tk64, tv64, p, grid, stream, 228);
     if (head_dim == 128)
-        return launch_verify_tc<128, 4, 4, 4, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 229);
+        return launch_verify_tc<128, 4, 4, 4, 2, 64, true, false, 1>(tk, tv, tk64, tv64, p, grid, stream, 229);
     return cudaErrorInvalidValue;
 }
 

@@ -1,0 +1,26 @@
+// verify_launch_shared_f32.cu -- the common part of a decode over shared prefixes
+// with fp32 outputs: 64-key tiles, a second sum of O, over a bf16 cache three
+// numbers per weight.
+#include "verify_launch.cuh"
+
+namespace pa {
+
+cudaError_t launch_prefix_f32(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                              const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (head_dim == 256)
+        return launch_verify_tc<256, 2, 3, 0, 2, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 236);
+    if (head_dim == 128)
+        return launch_verify_tc<128, 6, 6, 0, 2, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 237);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefix_fp8_f32(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
+                                  const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream) {
+    if (head_dim == 256)
+        return launch_verify_tc<256, 2, 3, 2, 2, 64, true, true, 2>(tk, tv, tk64, tv64, p, grid, stream, 238);
+    if (head_dim == 128)
+        return launch_verify_tc<128, 4, 4, 4, 2, 64, true, true, 2>(tk, tv, tk64, tv64, p, grid, stream, 239);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

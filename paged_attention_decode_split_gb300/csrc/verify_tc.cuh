@@ -269,10 +269,13 @@ __device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
 // V tiles per score tile.  At D = 256 two 128-column S/P buffers and O fill
 // tensor memory, so Q moves to shared memory as the product's A operand (QSM)
 // and the K ring holds one 128-key tile; at D = 128 Q stays in tensor memory.
-template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64, bool F4 = false>
+// PT = 3: a weight enters P V as three bf16 numbers, in 96 columns of its buffer;
+// at D = 256 Q moves to shared memory for their sake too.
+template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64, bool F4 = false, int PT = 2>
 struct VerifyTcCfg {
     static constexpr bool F8 = NSG > 0;                // fp8 or fp4 cache: staging ring of NSG slots per tensor
-    static constexpr bool QSM = TK == 128 && D == 256;  // Q in shared memory
+    static constexpr bool QSM = D == 256 && (TK == 128 || PT == 3);  // Q in shared memory
+    static constexpr int SW = PT == 3 ? 96 : TK;       // columns of an S/P buffer
     static constexpr int M = 128;                      // MMA rows (query rows, zero padded)
     static constexpr int TT = 64;                      // tokens per V tile (4 TMA chunks)
     static constexpr int CPT = TT / kChunk;            // chunks per V tile
@@ -303,13 +306,13 @@ struct VerifyTcCfg {
     // tensor-memory columns: O (fp32, D), NSB S/P buffers (TK each), Q (bf16
     // pairs, D / 2; not with QSM).  P of a score tile is written over its S
     // buffer, per 64-key half: a bf16 head in 32 columns, then the residual in 32.
-    static constexpr int TMEM_COLS = D + NSB * TK + (QSM ? 0 : D / 2) <= 256 ? 256 : 512;
+    static constexpr int TMEM_COLS = D + NSB * SW + (QSM ? 0 : D / 2) <= 256 ? 256 : 512;
     static constexpr int CTAS = TMEM_COLS == 256 ? 2 : 1;  // per SM
     static constexpr int O_COL = 0;
     static constexpr int S_COL = D;
-    static constexpr int Q_COL = D + NSB * TK;
+    static constexpr int Q_COL = D + NSB * SW;
     static constexpr int Q_TCOLS = QSM ? 0 : D / 2;
-    static constexpr int SBUF(int j) { return S_COL + j * TK; }
+    static constexpr int SBUF(int j) { return S_COL + j * SW; }
     static constexpr int QROW = D * 2 + 16;            // fp4: rows of Q in f16, staged in the V ring
     static constexpr int OFF_QPRE = OFF_V + M * QROW;  // and their pre-scales
     static_assert(!F4 || M * (QROW + 4) <= NV * TILE_BYTES, "the staged Q rows fit in the V ring");
@@ -325,6 +328,7 @@ struct VerifyTcCfg {
     static_assert(Q_COL + Q_TCOLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(TK == 64 || (TK == 128 && !F8), "128-key score tiles: bf16 cache only");
     static_assert(!F4 || F8, "an fp4 cache is staged and widened");
+    static_assert(PT == 2 || (PT == 1 && F8) || (PT == 3 && !F8 && TK == 64), "numbers per weight");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -351,21 +355,21 @@ constexpr float kExactLogits = 16777216.f;
 // SH: the common part of a decode over shared prefixes (VerifyParams): no causal
 // mask, a row per sequence and head.
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
-          bool FAR = false, bool SH = false>
-__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THREADS,
-                                  VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::CTAS)
+          bool FAR = false, bool SH = false, int PT = RES ? 2 : 1>
+__global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::THREADS,
+                                  VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::CTAS)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k64, const __grid_constant__ CUtensorMap tm_v64,
                         const VerifyParams p) {
-    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>;
+    using C = VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>;
     constexpr bool F8 = C::F8, QSM = C::QSM;
-    static_assert(RES || (F4 && C::VPK == 1), "the residual is left out over an fp4 cache only");
+    static_assert(RES == (PT > 1) && (RES || (F8 && C::VPK == 1)), "the residual is left out over quantised caches only");
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
-    static_assert(!FAR || (F4 && RES), "a second sum of O: fp4 cache with fp32 output");
+    static_assert(!FAR || (RES && C::VPK == 1), "a second sum of O: fp32 output");
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
     // fp4: the reference is kept 2^7 below the max, so that P in f16, at most 2^15,
     // holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
-    constexpr float kBelow = F4 ? 7.f : 0.f;
+    constexpr float kBelow = F4 || !RES ? 7.f : 0.f;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     // K and V tiles have their own rings: a K slot is free again as soon as
@@ -879,7 +883,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
 #pragma unroll
                             for (int ks = 0; ks < TT / 16; ++ks) {
 #pragma unroll
-                                for (int h = 0; h < (RES ? 2 : 1); ++h) {
+                                for (int h = 0; h < PT; ++h) {
                                     // P (head, then residual) of this 64-key half: 16 tokens = 8 columns per step
                                     const uint32_t a_tm = tm + C::SBUF(j) + h2 * TT + h * (TT / 2) + ks * 8;
                                     tc::mma_bf16_ta(tm + C::O_COL, a_tm, v_desc + (ks * 16 * 128 >> 4), kIdPV,
@@ -1365,7 +1369,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 const float m_use = m_ref == -INFINITY ? INFINITY : m_ref;
                 float2 ps2 = make_float2(0.f, 0.f);
                 uint32_t hw[TT / 2];
-                [[maybe_unused]] uint32_t lw[TT / 2];
+                [[maybe_unused]] uint32_t lw[TT / 2], xw[PT == 3 ? TT / 2 : 1];
 #pragma unroll
                 for (int c = 0; c < TT / 2; ++c) {
                     const float p0 = fast_exp2(fmaf(sv[2 * c], mul, -m_use));
@@ -1373,6 +1377,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                     ps2 = __fadd2_rn(ps2, make_float2(p0, p1));
                     if constexpr (!RES)
                         hw[c] = pack_f16(p0, p1);
+                    else if constexpr (PT == 3)
+                        split3_bf16(p0, p1, hw[c], lw[c], xw[c]);
                     else if constexpr (F8)
                         split_f16(p0, p1, hw[c], lw[c]);
                     else
@@ -1387,6 +1393,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 }
                 tc::st32(lane_base + C::SBUF(j), hw);
                 if constexpr (RES) tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
+                if constexpr (PT == 3) tc::st32(lane_base + C::SBUF(j) + TT, xw);
                 tc::wait_st();
                 if constexpr (FAR) {
                     if (far_at(i)) {  // (O is free for P_i V_i once it has been read)
@@ -1395,7 +1402,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                             break;
                         }
                         tc::fence_after();
-                        far_add(m_win, i == kVerifyFarTiles);
+                        if (n_live > 0) far_add(m_win, i == kVerifyFarTiles);  // (a warp without rows has nothing to move)
                     }
                 }
                 tc::fence_before();
@@ -1564,7 +1571,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4>::THRE
                 for (int k = 0; k < 4; ++k) tc::ld16_nowait(lane_base + C::O_COL + c1 + 16 * k, r[k]);
                 tc::wait_ld();
                 if constexpr (FAR) {
-                    if (n_tiles > kVerifyFarTiles && !idle_warp) {
+                    if (n_tiles > kVerifyFarTiles && n_live > 0) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float4 *at = far_place(c1 / 4 + j);

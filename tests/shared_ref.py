@@ -30,8 +30,8 @@ class Batch:
         self.width = max(1, -(-int(self.lens.max(initial=1)) // bs))
         self.pages = int(sum(-(-n // bs) for n in lens)) + 3
         order, at = rng.permutation(self.pages), 0
-        self.table = np.full((self.n, self.width), -7, np.int32)   # as the call gets it
-        self.full = np.zeros((self.n, self.width), np.int32)       # every sequence's pages
+        self.table = np.full((self.n, self.width), -7, np.int32)
+        copies = []  # (sequence, leader, page): a prefix that ends inside a page has its part of it copied
         for g, (pre, own) in enumerate(groups):
             leader = None
             for b in range(starts[g], starts[g + 1]):
@@ -39,13 +39,21 @@ class Batch:
                 first = pre // bs if leader is not None and used else 0
                 if lens[b] == 0:
                     continue
-                self.table[b, first:used] = self.full[b, first:used] = order[at:at + used - first]
-                if first:  # (the shared entries of the others are not read)
-                    self.full[b, :first] = self.full[leader, :first]
+                self.table[b, first:used] = order[at:at + used - first]
                 at += used - first
                 if leader is None:
                     leader = b
+                    continue
+                self.table[b, :first] = self.table[leader, :first]
+                if pre % bs >= 16 and first < used:
+                    copies.append((self.table[b, first], self.table[leader, first], pre % bs // 16 * 16))
         self.k, self.v, self.g = self._caches(rng)
+        for to, at, tokens in copies:
+            for c in (self.k, self.v):
+                if kind == "fp4":
+                    c[to, :, :tokens // 16] = c[at, :, :tokens // 16]
+                else:
+                    c[to, :tokens] = c[at, :tokens]
         self.scale = 1 / np.sqrt(d)
         self.q = torch.from_numpy(rng.standard_normal((self.n, hq, d)).astype(np.float32)).to(torch.bfloat16)
 
@@ -64,15 +72,9 @@ class Batch:
         return *codes, g
 
     def slots(self, b):
-        """Where the tokens of sequence b stand: those of the prefix (whole 16-token chunks) in the leader's pages."""
+        """Where the tokens of sequence b stand."""
         t = np.arange(self.lens[b])
-        own = self.full[b].astype(np.int64)[t // self.bs] * self.bs + t % self.bs
-        g = int(np.searchsorted(self.starts, b, side="right")) - 1
-        live = [i for i in range(self.starts[g], self.starts[g + 1]) if self.lens[i] > 0]
-        if not live:
-            return own
-        lead = self.full[live[0]].astype(np.int64)[t // self.bs] * self.bs + t % self.bs
-        return np.where(t < self.prefix[b] // 16 * 16, lead, own)
+        return self.table[b].astype(np.int64)[t // self.bs] * self.bs + t % self.bs
 
     def rows(self, which, slots):
         c = (self.k, self.v)[which]
@@ -131,8 +133,8 @@ class Batch:
                                       max_prefix_len=int(self.prefix.max()),
                                       max_suffix_len=max(1, int((self.lens - self.prefix).max()))) | kw))
 
-    def run(self, t=None, desc=None, shared=None, workspace=None, status=None, out=None, stream=None):
-        t, desc, shared = t or self.tensors(), desc or self.desc(), shared or self.shared()
+    def run(self, t=None, desc=None, shared=None, workspace=None, status=None, out=None, stream=None, **kw):
+        t, desc, shared = t or self.tensors(), desc or self.desc(), shared or self.shared(**kw)
         if out is None:
             out = torch.full((self.n, self.hq, self.d), float("nan"), device="cuda",
                              dtype=torch.bfloat16 if self.out == "bf16" else torch.float32)

@@ -24,6 +24,8 @@ def status0():
     return torch.zeros(1, dtype=torch.int32, device="cuda")
 
 
+# Small batches are read without sharing unless the prefixes' splits are forced: both ways are tried.
+BOTH = pytest.mark.parametrize("splits", [0, 2], ids=["plain", "shared"])
 HYBRID, DENSE, WIDE = (24, 4, 256), (32, 8, 128), (48, 4, 256)
 # prefixes of no chunk, one, a page and a bit, several tiles; own parts of no token, one, a chunk, more; idle sequences
 GROUPS = {
@@ -46,12 +48,14 @@ GROUPS = {
                                           ((16, 16, 128), 64, "f32"), ((32, 2, 128), 16, "bf16")])
 def test_groups(name, shape, bs, out, kind):
     b = Batch(len(name), GROUPS[name], *shape, bs, kind, out)
-    status = status0()
-    got = b.run(status=status)
-    check(got, *b.reference())
-    assert int(status) == 0
-    assert pa.last_plan()["path_id"] == pa.PA_PATH_DECODE_SHARED and pa.last_plan()["reduce_launched"] == 1
-    assert torch.equal(got, b.run())  # bit for bit
+    ref = b.reference()
+    for splits in (0, 2):
+        status = status0()
+        got = b.run(status=status, prefix_splits=splits)
+        check(got, *ref)
+        assert int(status) == 0
+        assert pa.last_plan()["path_id"] == pa.PA_PATH_DECODE_SHARED
+        assert torch.equal(got, b.run(prefix_splits=splits))  # bit for bit
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -59,7 +63,9 @@ def test_groups(name, shape, bs, out, kind):
 @pytest.mark.parametrize("d", [128, 256])
 def test_heads_per_kv_head(g, d, kind):
     b = Batch(g + d, [(144, [1, 0, 33]), (64, [70] * 8)], 2 * g, 2, d, 32, kind)
-    check(b.run(), *b.reference())
+    ref = b.reference()
+    for splits in (0, 2):
+        check(b.run(prefix_splits=splits), *ref)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -76,7 +82,8 @@ def test_hints_bound_nothing(kind):
     ref = b.reference()
     for kw in (dict(max_prefix_len=16, max_suffix_len=1), dict(max_prefix_len=0, max_suffix_len=0),
                dict(max_prefix_len=10 ** 9, max_suffix_len=10 ** 9, max_group_seqs=10 ** 6)):
-        check(b.run(shared=b.shared(**kw)), *ref)
+        for splits in (0, 1, 5):
+            check(b.run(prefix_splits=splits, **kw), *ref)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -95,8 +102,7 @@ def test_one_group_of_everything_equals_decode(kind):
     t, desc = b.tensors(), b.desc()
     out = torch.empty((b.n, b.hq, b.d), device="cuda")
     ws = torch.empty(max(1, pa.workspace_bytes(desc)), dtype=torch.uint8, device="cuda")
-    full = torch.from_numpy(b.full).cuda()
-    getattr(pa, "paged_attention_decode" + ("" if kind == "bf16" else "_" + kind))(t["q"], *t["caches"], *t["scales"], full,
+    getattr(pa, "paged_attention_decode" + ("" if kind == "bf16" else "_" + kind))(t["q"], *t["caches"], *t["scales"], t["table"],
                                                                                   t["lens"], desc, out, ws)
     ref, tol = b.reference()
     check(out, ref, tol)
@@ -113,7 +119,9 @@ def test_growing_scores(kind):
             at = torch.from_numpy(b.slots(s))
             b.k.view(-1, b.hkv, b.d)[at] *= (torch.arange(len(at)) / 40 + 1).to(torch.bfloat16)[:, None, None]
     b.q = (b.q.abs() * 8).to(torch.bfloat16)
-    check(b.run(), *b.reference())
+    ref = b.reference()
+    for splits in (0, 2):
+        check(b.run(prefix_splits=splits), *ref)
 
 
 @pytest.mark.parametrize("rows", [5, 30])
@@ -124,7 +132,11 @@ def test_rising_scores(rows):
         at = torch.from_numpy(b.slots(s))
         b.k.view(-1, b.hkv, b.d)[at] = (torch.arange(len(at)) / 200 + 0.1).to(torch.bfloat16)[:, None, None]
     b.q = (b.q.abs() * 4).to(torch.bfloat16)
-    check(b.run(), *b.reference())
+    for out in ("f32", "bf16"):
+        b.out = out
+        ref = b.reference()
+        for splits in (0, 1):
+            check(b.run(prefix_splits=splits), *ref)
 
 
 # -- lengths, groups and pages that make no sense --------------------------------------------------
@@ -143,30 +155,29 @@ def zero_rows(b, bad):
     (dict(prefix={0: -1}), {0, 1, 2, 3}),                            # the leader's: nobody agrees with it
     (dict(starts={0: 1}), {0}), (dict(starts={2: 5}), {5}),          # not in any group
     (dict(starts={1: 5, 2: 3}), {0, 1, 2, 3, 4, 5}), (dict(starts={0: -1}), {0, 1, 2, 3, 4, 5})])
-def test_bad_lengths_and_groups(change, bad, kind):
+@BOTH
+def test_bad_lengths_and_groups(change, bad, kind, splits):
     b = Batch(4, [(112, [3, 20, 1, 60]), (32, [5, 9])], *HYBRID, 16, kind)
     want = zero_rows(b, bad)
     t = b.tensors()
     for name, values in change.items():
         for i, v in values.items():
             t[name][i] = v
-    if "starts" in change:  # (another sequence leads the group: it needs the entries of the prefix in its row)
-        t["table"].copy_(torch.from_numpy(b.full))
     status = status0()
-    check(b.run(t, status=status), *want)
-    # (a sequence with a shorter prefix than its group reads entries of its own from there on, which are -7 here)
-    assert int(status) & ~(pa.PA_DEV_BAD_PAGE if change.get("prefix") == {2: 96} else 0) == pa.PA_DEV_BAD_SEQLEN
+    check(b.run(t, status=status, prefix_splits=splits), *want)
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
 
 
+@BOTH
 @pytest.mark.parametrize("kind", KINDS)
-def test_more_sequences_than_the_host_said(kind):
+def test_more_sequences_than_the_host_said(kind, splits):
     b = Batch(4, [(64, [3] * 50), (32, [5, 9])], *HYBRID, 16, kind)  # 50 x 6 rows: three blocks
     ref = b.reference()
     for most in (20, 21, 49):
         want = [x.copy() for x in ref]
         want[0][most:50], want[1][most:50] = 0, 0
         status = status0()
-        check(b.run(shared=b.shared(max_group_seqs=most), status=status), *want)
+        check(b.run(max_group_seqs=most, prefix_splits=splits, status=status), *want)
         assert int(status) == pa.PA_DEV_BAD_SEQLEN
 
 
@@ -175,14 +186,16 @@ def test_more_sequences_than_the_host_said(kind):
 def test_bad_pages(page, kind):
     b = Batch(6, [(128, [3, 20, 1]), (32, [90, 9])], *DENSE, 16, kind)
     for where, bad in (((0, 2), {0, 1, 2}), ((1, 8), {1}), ((3, 4), {3})):  # the prefix, two own parts
-        t, status = b.tensors(), status0()
-        t["table"][where] = page
-        check(b.run(t, status=status), *zero_rows(b, bad))
-        assert int(status) == pa.PA_DEV_BAD_PAGE
+        for splits in (0, 2):
+            t, status = b.tensors(), status0()
+            t["table"][where] = page
+            check(b.run(t, status=status, prefix_splits=splits), *zero_rows(b, bad if splits else {where[0]}))
+            assert int(status) == pa.PA_DEV_BAD_PAGE
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_what_no_sequence_sees_may_be_anything(kind):
+@BOTH
+def test_what_no_sequence_sees_may_be_anything(kind, splits):
     """NaN in every slot that is not in use, in the rows of q of idle sequences, and in the workspace."""
     b = Batch(8, [(100, [1, 17, None, 64]), (48, [0, 5]), (16, [None])], *HYBRID, 48, kind)
     ref, tol = b.reference()
@@ -204,11 +217,12 @@ def test_what_no_sequence_sees_may_be_anything(kind):
                 rows[np.broadcast_to(dead.reshape(b.pages, 1, -1, 16)[..., tok], rows.shape[:3])] = 0xFF
                 c[..., places] = rows
     b.q[b.lens == 0] = float("nan")
-    check(b.run(), ref, tol)
+    check(b.run(prefix_splits=splits), ref, tol)
 
 
+@BOTH
 @pytest.mark.parametrize("kind", KINDS)
-def test_nan_reaches_what_depends_on_it(kind):
+def test_nan_reaches_what_depends_on_it(kind, splits):
     b = Batch(9, [(96, [3, 20, 1]), (64, [5, 9])], *HYBRID, 16, kind)
     ref, tol = b.reference()
     b.q[1, 4, 7] = float("nan")  # one head of one sequence
@@ -229,7 +243,7 @@ def test_nan_reaches_what_depends_on_it(kind):
     bad[:3, 12:18] = True
     spoil(int(b.slots(4)[66]), 0)   # a key of the last sequence's own part
     bad[4, :6] = True
-    got = b.run().cpu()
+    got = b.run(prefix_splits=splits).cpu()
     assert torch.isnan(got[torch.from_numpy(bad)]).all()
     good = torch.from_numpy(~bad)
     check(got[good], ref[~bad], tol[~bad])
@@ -237,25 +251,27 @@ def test_nan_reaches_what_depends_on_it(kind):
 
 # -- calls side by side ----------------------------------------------------------------------------
 
+@BOTH
 @pytest.mark.parametrize("kind", KINDS)
-def test_stream_and_graphs_with_one_workspace(kind):
+def test_stream_and_graphs_with_one_workspace(kind, splits):
     """Two captured calls of different shapes share a workspace and are replayed in turn, with lengths that change on
     the GPU between replays; and a call on a stream of its own."""
     a = Batch(1, [(512, [1, 40, 7]), (64, [3])], *HYBRID, 16, kind)
     c = Batch(2, [(80, [9] * 30)], *DENSE, 16, kind, "bf16")
     ta, tc = a.tensors(), c.tensors()
-    ws = torch.empty(max(pa.shared_workspace_bytes(x.desc(), x.shared()) for x in (a, c)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(pa.shared_workspace_bytes(x.desc(), x.shared(prefix_splits=splits)) for x in (a, c)), dtype=torch.uint8,
+                     device="cuda")
     outs = [torch.zeros((x.n, x.hq, x.d), device="cuda", dtype=torch.bfloat16 if x.out == "bf16" else torch.float32) for x in (a, c)]
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    a.run(ta, workspace=ws, out=outs[0], stream=s)
+    a.run(ta, workspace=ws, out=outs[0], stream=s, prefix_splits=splits)
     s.synchronize()
     check(outs[0], *a.reference())
     graphs = []
     for x, t, o in ((a, ta, outs[0]), (c, tc, outs[1])):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            x.run(t, workspace=ws, out=o)
+            x.run(t, workspace=ws, out=o, prefix_splits=splits)
         graphs.append(g)
     for step in range(3):
         for g, x, t, o in zip(graphs, (a, c), (ta, tc), outs):
@@ -267,12 +283,13 @@ def test_stream_and_graphs_with_one_workspace(kind):
             t["lens"].copy_(torch.from_numpy(x.lens))
 
 
-def test_many_calls_behind_one_another():
+@BOTH
+def test_many_calls_behind_one_another(splits):
     """Calls with one workspace and no wait between them, their inputs written just before on the same stream."""
     b = Batch(3, [(256, [1, 33, 80]), (1024, [5] * 12)], *HYBRID, 16)
-    t, desc, shared = b.tensors(), b.desc(), b.shared()
+    t, desc, shared = b.tensors(), b.desc(), b.shared(prefix_splits=splits)
     ws = torch.empty(pa.shared_workspace_bytes(desc, shared), dtype=torch.uint8, device="cuda")
-    want = b.run(t)
+    want = b.run(t, prefix_splits=splits)
     src = {k: t[k].clone() for k in ("q", "table", "lens", "starts", "prefix")}
     outs = []
     for i in range(20):
@@ -294,7 +311,9 @@ def test_cache_past_two_to_the_32_bytes():
         x[shift:] = c
     t["caches"] = tuple(big)
     t["table"] = torch.where(t["table"] >= 0, t["table"] + shift, t["table"])
-    check(b.run(t, desc=b.desc(num_pages=pages)), *b.reference())
+    ref = b.reference()
+    for splits in (0, 2):
+        check(b.run(t, desc=b.desc(num_pages=pages), prefix_splits=splits), *ref)
 
 
 def test_no_sequences():
@@ -309,8 +328,9 @@ def test_no_sequences():
 # -- the operators together ------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", KINDS)
+@BOTH
 @pytest.mark.parametrize("graph", [False, True])
-def test_a_sampling_run(kind, graph):
+def test_a_sampling_run(kind, graph, splits):
     """A prompt is written with its rotations, forked into samples that each go on by a few tokens and are then let
     go: block tables, rotary_and_cache, fork, page copies, shared decode and release, all on the GPU, against
     attention in float64 over the rows as they were written."""
@@ -351,7 +371,7 @@ def test_a_sampling_run(kind, graph):
     # steps: one token per sample
     desc = pa.make_desc(num_seqs=n, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs, max_pages_per_seq=width,
                         max_seq_len=width * bs, num_pages=P, scale=1 / 16)
-    shared = pa.make_prefix(num_groups=1, max_group_seqs=n, max_prefix_len=prompt, max_suffix_len=40)
+    shared = pa.make_prefix(num_groups=1, max_group_seqs=n, max_prefix_len=prompt, max_suffix_len=40, prefix_splits=splits)
     ws = torch.empty(pa.shared_workspace_bytes(desc, shared), dtype=torch.uint8, **dev)
     rows = torch.empty((n, hq + 2 * hkv, d), dtype=torch.bfloat16, **dev)
     q, out = torch.empty((n, hq, d), dtype=torch.bfloat16, **dev), torch.empty((n, hq, d), **dev)
@@ -383,7 +403,7 @@ def test_a_sampling_run(kind, graph):
             replay()
         torch.cuda.synchronize()
         assert int(status) == 0 and held.tolist() == [prompt + i + 1] * n
-        b.lens, b.full, b.q = held.cpu().numpy(), table.cpu().numpy(), q.cpu()
+        b.lens, b.table, b.q = held.cpu().numpy(), table.cpu().numpy(), q.cpu()
         b.k, b.v = (c.cpu() if kind == "bf16" else c.cpu().numpy() for c in caches)
         b.g = None if kind == "bf16" else tuple(s.cpu().numpy() for s in scales)
         check(out, *b.reference())

@@ -39,17 +39,18 @@ def records(d, x):
 
 
 def test_plan(lib):
-    # 64 sequences of 6 heads: 3 row blocks of 4 KV heads, 12 prefix splits; one split of each own part
-    bf16 = dict(out_dtype=pa.PA_OUT_BF16)
-    assert records(desc(**bf16), prefix()) == 12 + 1
+    # 64 sequences of 6 heads: 3 row blocks of 4 KV heads, 12 prefix splits; two splits of each own part (1500 tokens)
+    assert records(desc(), prefix()) == 12 + 2
     # 16 groups of 4 KV heads: two CTAs for each
-    assert records(desc(**bf16), prefix(num_groups=16, max_group_seqs=4)) == 2 + 1
-    # fp32 outputs: 2048 keys a split at most (bf16: as many as one gets)
-    many = dict(num_groups=64, max_group_seqs=1)
-    assert records(desc(), prefix(**many)) == 16 + 1
-    assert records(desc(**bf16), prefix(**many)) == 1 + 1
-    # short prefixes are not cut below 128 tokens, short own parts not below 64
-    assert records(desc(num_seqs=4), prefix(max_group_seqs=4, max_prefix_len=512, max_suffix_len=40)) == 4 + 1
+    assert records(desc(), prefix(num_groups=16, max_group_seqs=4)) == 2 + 2
+    # short prefixes are not cut below 128 tokens
+    assert records(desc(), prefix(max_prefix_len=512, max_suffix_len=40)) == 4 + 1
+    # sharing that saves little is left: 4 sequences of 552 tokens, 35 chunks, split as a decode of that length
+    small = dict(max_group_seqs=4, max_prefix_len=512, max_suffix_len=40)
+    assert records(desc(num_seqs=4), prefix(**small)) == 7
+    assert records(desc(num_seqs=4), prefix(prefix_splits=3, **small)) == 3 + 1
+    # so is a batch without groups; one split of it needs no records
+    assert pa.shared_workspace_bytes(desc(num_splits=1), prefix(num_groups=64, max_group_seqs=1)) == 0
     # forced
     assert records(desc(num_splits=7), prefix(prefix_splits=5)) == 5 + 7
     # the hints bound nothing, and 0 stands for max_seq_len
@@ -130,13 +131,13 @@ def test_reference_against_the_oracle(kind, oracle_mod):
     if kind == "fp4":
         vals = [b.rows(w, np.arange(b.pages * b.bs)).astype(np.float32).reshape(b.pages, b.bs, 2, 128) for w in (0, 1)]
         k, v = (torch.from_numpy(x).to(torch.bfloat16) for x in vals)  # (rounds the head scale's product)
-        want = oracle_mod.paged_attention(b.q, k, v, b.full, b.lens, b.scale)
+        want = oracle_mod.paged_attention(b.q, k, v, b.table, b.lens, b.scale)
         assert np.abs(want - ref).max() < 0.05
         return
     if kind == "bf16":
-        want = oracle_mod.paged_attention(b.q, b.k, b.v, b.full, b.lens, b.scale)
+        want = oracle_mod.paged_attention(b.q, b.k, b.v, b.table, b.lens, b.scale)
     else:
         want = oracle_mod.paged_attention_fp8(b.q, torch.from_numpy(b.k), torch.from_numpy(b.v), torch.from_numpy(b.g[0]),
-                                              torch.from_numpy(b.g[1]), b.full, b.lens, b.scale)
+                                              torch.from_numpy(b.g[1]), b.table, b.lens, b.scale)
     # (the scale is binary32 there)
     assert np.abs(want - ref).max() < 1e-6
