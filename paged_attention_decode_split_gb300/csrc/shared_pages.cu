@@ -7,15 +7,20 @@
 // page of one request has 0 and the calls of block_tables.cu need not know it.
 //
 // All are integer work, bound by launches and by a few dependent loads.  Counts
-// change by atomic adds of whole numbers, whose order does not show, in a copy
-// of the counts (the outputs are buffers of their own, so that a replayed call
-// gives the same again): one kernel copies, the next adds.  Freed pages enter
-// the pool in ascending order, whichever request held them last, which takes a
-// prefix sum over the pages: one cluster of 8 CTAs, whose sums pass through
-// distributed shared memory.
+// change by atomic adds of whole numbers, whose order does not show; freed pages
+// enter the pool in ascending order, whichever request held them last, which
+// takes a prefix sum over the pages.  The outputs are buffers of their own, so that
+// a replayed call gives the same again.
+//
+// A step of a serving loop is one launch of one cluster of 8 CTAs: the pages are
+// spread over their shared memories, an entry of a block table adds to its page's
+// counter there, and the sums pass through distributed shared memory.  That holds
+// 409,600 pages.  More pages, or tables of more than kClusterEntries entries,
+// which 8 SMs would take long to walk, go through kernels that fill the GPU: one
+// copies the counts, the next adds to them, a cluster scans.
 #include <algorithm>
 
-#include "pa_device.cuh"
+#include "pa_internal.h"
 
 namespace pa {
 
@@ -26,6 +31,8 @@ constexpr int kShareCtas = 304;       // two per SM
 constexpr int kScanCtas = 8;          // CTAs of the cluster that scans the pages
 constexpr int kScanThreads = 1024;
 constexpr int kScanItems = 4;         // pages per thread and step
+constexpr int kClusterPages = 50 * 1024;         // counters of a CTA of the cluster (200 KiB)
+constexpr int64_t kClusterEntries = 128 * 1024;  // of the block table
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPiece = 16 * 1024; // bytes that a CTA copies at a time: four 16-byte loads per thread
 constexpr int kCopyCtas = 152 * 8;
@@ -252,6 +259,169 @@ __device__ __forceinline__ Span span_of(int64_t pages) {
     return {lo, min(pages, lo + per)};
 }
 
+// The pages of a CTA as counters in its shared memory: page p is counter p -
+// rank * per of CTA rank = p / per.
+struct Counters {
+    uint32_t base;   // shared-memory address in this CTA
+    int lo, n, per;  // the CTA's pages [lo, lo + n)
+};
+__device__ __forceinline__ Counters counters_of(const ShareParams &p, int32_t *smem) {
+    const int per = ((int)((p.num_pages + kScanCtas - 1) / kScanCtas) + 3) & ~3;
+    const int lo = (int)min(p.num_pages, (int64_t)per * blockIdx.x);
+    return {smem_addr(smem), lo, (int)min((int64_t)per, p.num_pages - lo), per};
+}
+__device__ __forceinline__ uint32_t counter_at(const Counters &c, int page) {
+    const int rank = page / c.per;
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(c.base + 4u * (uint32_t)(page - rank * c.per)), "r"(rank));
+    return there;
+}
+__device__ __forceinline__ void counter_add(const Counters &c, int page, int v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(counter_at(c, page)), "r"(v) : "memory");
+}
+
+// A thread's share of the CTA's pages for a scan: [lo, hi), relative to the CTA's first.
+struct Share {
+    int lo, hi;
+};
+__device__ __forceinline__ Share share_of(int n) {
+    const int per = (n + kScanThreads - 1) / kScanThreads;
+    const int lo = min(n, (int)threadIdx.x * per);
+    return {lo, min(n, lo + per)};
+}
+
+// Sum of v over the CTAs before this one (and the threads before this one, which
+// block_before gave), and over all: `box` is used once.
+__device__ __forceinline__ int64_t cluster_before(int total, int *box, int64_t &all) {
+    cluster_share(total, box);
+    int64_t before = 0;
+    all = 0;
+    for (int c = 0; c < kScanCtas; ++c) {
+        if (c < (int)blockIdx.x) before += box[c];
+        all += box[c];
+    }
+    return before;
+}
+
+// ---- the calls of a step, a cluster each ----------------------------------------
+
+__global__ void __launch_bounds__(kScanThreads) pa_fork_cluster_kernel(const ShareParams p) {
+    pdl_wait_primary();  // (no early launch of dependents: a kernel behind may read tables ahead of the stream order)
+    extern __shared__ int32_t counts[];
+    __shared__ int tmp[32];
+    __shared__ int box[kScanCtas];
+    const Counters c = counters_of(p, counts);
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) counts[i] = 0;
+    cluster_sync();
+    // the requests of this CTA, a thread each (kClusterEntries bounds them), and what all requests before them want
+    const int per = (p.B + kScanCtas - 1) / kScanCtas, b0 = min(p.B, per * (int)blockIdx.x), b1 = min(p.B, b0 + per);
+    const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
+    int wanted = 0;
+    for (int i0 = b0; i0 < b1; i0 += kScanThreads) {
+        const int b = i0 + threadIdx.x;
+        wanted += b < b1 ? wants(p, child_of(p, b)) : 0;
+    }
+    int64_t all;
+    int64_t before = cluster_before(block_sum(wanted, tmp), box, all);
+    __shared__ int job_parent[kScanThreads], job_full[kScanThreads];  // of the requests at hand; parent -1: nothing to do
+    for (int i0 = b0; i0 < b1; i0 += kScanThreads) {
+        const int b = i0 + threadIdx.x;
+        const bool in = b < b1;
+        Child k{-1, 0, false, false};
+        if (in) k = child_of(p, b);
+        const int want = wants(p, k);
+        int total;
+        const int64_t upto = before + block_before(want, tmp, total) + want;
+        before += total;
+        const bool served = k.ok && (!want || upto <= F);
+        job_parent[threadIdx.x] = served ? k.parent : -1;
+        job_full[threadIdx.x] = k.len / p.block_size;
+        if (in) {
+            const int len = p.lens[b], full = k.len / p.block_size;
+            const bool part = served && want;
+            const int page = part ? p.free_pages[F - upto] : -1;
+            int bits = 0;
+            if (k.is ? !k.ok : (len < 0 || len > room_of(p))) bits |= PA_DEV_BAD_SEQLEN;
+            if (k.ok && !served) bits |= PA_DEV_NO_PAGES;
+            if (part && !valid_page(p, page)) bits |= PA_DEV_BAD_PAGE;
+            p.lens_out[b] = served ? k.len : max(len, 0);
+            p.src[b] = part ? p.table[(int64_t)k.parent * p.width + full] : -1;
+            p.dst[b] = page;
+            p.tokens[b] = part ? k.len % p.block_size : 0;
+            if (part) p.table[(int64_t)b * p.width + full] = page;
+            if (bits) set_status(p.status, bits);
+        }
+        __syncthreads();
+        // the full pages: a warp per child
+        for (int i = threadIdx.x >> 5; i < min(kScanThreads, b1 - i0); i += kScanThreads / 32) {
+            const int parent = job_parent[i], full = job_full[i];
+            if (parent < 0) continue;
+            const int32_t *from = p.table + (int64_t)parent * p.width;
+            int32_t *to = p.table + (int64_t)(i0 + i) * p.width;
+            for (int e = threadIdx.x & 31; e < full; e += 32) {
+                const int page = from[e];
+                to[e] = page;
+                if (valid_page(p, page))
+                    counter_add(c, page, 1);
+                else
+                    set_status(p.status, PA_DEV_BAD_PAGE);
+            }
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = F - (int)min((int64_t)F, all);
+    cluster_sync();  // every holder is counted
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) p.shares_out[c.lo + i] = p.shares[c.lo + i] + counts[i];
+}
+
+__global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const ShareParams p) {
+    pdl_wait_primary();  // (no early launch of dependents, as above)
+    extern __shared__ int32_t counts[];
+    __shared__ int tmp[32];
+    __shared__ int box[kScanCtas];
+    const Counters c = counters_of(p, counts);
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) counts[i] = p.shares[c.lo + i];
+    const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
+    cluster_sync();
+    // a warp per request
+    for (int b = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); b < p.B; b += kScanCtas * (kScanThreads / 32)) {
+        const int len = p.lens[b], done = p.count[b];
+        const bool ok = len >= 0 && len <= room_of(p);
+        if ((threadIdx.x & 31) == 0) {
+            if (!ok) set_status(p.status, PA_DEV_BAD_SEQLEN);
+            p.lens_out[b] = done != 0 ? 0 : max(len, 0);
+        }
+        const int held = ok && done != 0 ? (int)(((int64_t)len + p.block_size - 1) / p.block_size) : 0;
+        for (int e = threadIdx.x & 31; e < held; e += 32) {
+            const int page = p.table[(int64_t)b * p.width + e];
+            if (valid_page(p, page))
+                counter_add(c, page, -1);
+            else
+                set_status(p.status, PA_DEV_BAD_PAGE);
+        }
+    }
+    cluster_sync();
+    const Share s = share_of(c.n);
+    int mine = 0;
+    for (int i = s.lo; i < s.hi; ++i) mine += counts[i] < 0;
+    int total;
+    const int in_cta = block_before(mine, tmp, total);
+    int64_t all;
+    int64_t to = F + cluster_before(total, box, all) + in_cta;
+    if (mine > 0) {
+        for (int i = s.lo; i < s.hi; ++i) {
+            if (counts[i] >= 0) continue;
+            // released more often than it was held, or more pages than the pool has
+            if (counts[i] < -1 || to >= p.num_pages) set_status(p.status, PA_DEV_BAD_PAGE);
+            if (to < p.num_pages) p.free_pages[to] = c.lo + i;
+            ++to;
+        }
+    }
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) p.shares_out[c.lo + i] = max(counts[i], 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = (int)min(F + all, p.num_pages);
+    cluster_sync();  // (no CTA leaves while another may still write into its shared memory)
+}
+
 // (grid = one cluster of kScanCtas CTAs)
 __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const ShareParams p) {
     pdl_wait_primary();  // (no early launch of dependents, as above)
@@ -303,6 +473,85 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const Sha
 // one kind goes with the k-th of the other.  After m moves, before(p) has grown
 // by the free pages filled below p and lost the moved ones, which places every
 // free page on the new list without a second scan.
+// The marks and the ranks stand in the cluster's shared memory; a thread scans a
+// stretch of pages of its own.
+__global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const ShareParams p) {
+    pdl_launch_dependents();  // (the kernel behind this one rewrites the tables and is the call's last)
+    pdl_wait_primary();
+    extern __shared__ int32_t used[];
+    __shared__ int tmp[32];
+    __shared__ int box[3][kScanCtas];
+    __shared__ int top;
+    const int64_t P = p.num_pages;
+    const Counters c = counters_of(p, used);
+    const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
+    const int tid = blockIdx.x * kScanThreads + threadIdx.x;
+    constexpr int stride = kScanCtas * kScanThreads;
+    if (threadIdx.x == 0) top = 0;
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) {
+        used[i] = 1;
+        __stcg(p.page_map + c.lo + i, c.lo + i);
+        __stcg(p.shares_out + c.lo + i, p.shares[c.lo + i]);
+    }
+    cluster_sync();
+    for (int i = tid; i < F; i += stride) {
+        const int page = p.free_pages[i];
+        if (valid_page(p, page))
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(counter_at(c, page)), "r"(0) : "memory");
+        else
+            set_status(p.status, PA_DEV_BAD_PAGE);
+    }
+    cluster_sync();
+    const Share s = share_of(c.n);
+    int mine = 0;
+    for (int i = s.lo; i < s.hi; ++i) mine += used[i];
+    int total;
+    const int in_cta = block_before(mine, tmp, total);
+    int64_t n;
+    int64_t bef = cluster_before(total, box[0], n) + in_cta;
+    mine = 0;
+    for (int i = max((int64_t)s.lo, n - c.lo); i < s.hi; ++i) mine += used[i];
+    int64_t m;
+    cluster_before(block_sum(mine, tmp), box[1], m);
+    m = min(m, (int64_t)p.moves);
+    const int64_t n_free = P - n;
+    int highest = 0;
+    for (int i = s.lo; i < s.hi; ++i) {
+        const int64_t page = c.lo + i;
+        const int u = used[i];
+        const int64_t rank = u ? n - 1 - bef : page - bef;  // from the top, from the bottom
+        const bool moves = rank < m && (u ? page >= n : page < n);
+        if (moves) __stcg((u ? p.src : p.dst) + rank, (int)page);
+        if ((u != 0) != moves) {  // in use from now on
+            highest = (int)page + 1;
+        } else {
+            const int64_t in_use = bef + min(m, page - bef) - max((int64_t)0, bef - (n - m));
+            p.free_out[n_free - 1 - (page - in_use)] = (int)page;
+        }
+        bef += u;
+    }
+    for (int64_t i = m + tid; i < p.moves; i += stride) p.src[i] = p.dst[i] = -1;
+    for (int64_t i = n_free + tid; i < P; i += stride) p.free_out[i] = -1;
+    highest = __reduce_max_sync(0xffffffffu, highest);
+    if ((threadIdx.x & 31) == 0) atomicMax(&top, highest);
+    __syncthreads();
+    cluster_share(top, box[2]);  // (also: every move is listed)
+    for (int64_t i = tid; i < m; i += stride) {
+        const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i), held = p.shares[from];
+        __stcg(p.page_map + from, to);
+        __stcg(p.shares_out + to, held);
+        __stcg(p.shares_out + from, 0);
+    }
+    if (tid == 0) {
+        int e = 0;
+        for (int k = 0; k < kScanCtas; ++k) e = max(e, box[2][k]);
+        p.extent[0] = e;
+        p.num_free_out[0] = (int)n_free;
+    }
+    cluster_sync();
+}
+
+// The same for more pages than the cluster's shared memory holds.
 __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const ShareParams p) {
     pdl_launch_dependents();  // (the kernel behind this one rewrites the tables and is the call's last)
     pdl_wait_primary();
@@ -502,10 +751,11 @@ pa_status check_sizes(const ShareParams &p) {
 }
 
 template <typename... K, typename... A>
-bool launch_on(void (*kern)(K...), int ctas, int threads, bool cluster, void *stream, A... args) {
+bool launch_on(void (*kern)(K...), int ctas, int threads, bool cluster, size_t smem, void *stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -522,6 +772,17 @@ bool launch_on(void (*kern)(K...), int ctas, int threads, bool cluster, void *st
 int share_ctas(const ShareParams &p) {
     const int64_t pages = (p.num_pages + 4 * kShareThreads - 1) / (4 * kShareThreads);
     return (int)std::max<int64_t>(1, std::min<int64_t>(kShareCtas, std::max<int64_t>(pages, p.B)));
+}
+
+// Whether a step's pages and tables suit one cluster, and its launch with the
+// counters of `per` pages in every CTA.
+bool suits_cluster(const ShareParams &p) {
+    return p.num_pages <= (int64_t)kScanCtas * kClusterPages && (int64_t)p.B * p.width <= kClusterEntries;
+}
+pa_status launch_cluster(void (*kern)(ShareParams), const ShareParams &p, int slot, void *stream) {
+    const size_t smem = 4 * ((((size_t)p.num_pages + kScanCtas - 1) / kScanCtas + 3) & ~size_t(3));
+    if (ensure_smem_limit(reinterpret_cast<const void *>(kern), kClusterPages * 4, slot) != cudaSuccess) return PA_ERR_CUDA;
+    return launch_on(kern, kScanCtas, kScanThreads, true, smem, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -571,12 +832,13 @@ pa_status pa_fork_block_tables(const int32_t *seq_lens, const int32_t *parent, i
                             {copy_tokens, rows, true, true},
                             {num_free_out, 4, true, true}});
     if (st != PA_OK) return st;
+    if (suits_cluster(p)) return launch_cluster(pa_fork_cluster_kernel, p, 280, stream);
     const int ctas = share_ctas(p);
     // whole CTAs of requests: at least one request, so that the last CTA that has any writes the pool's size
     const int per = std::max(1, (p.B + ctas - 1) / ctas);
-    if (!launch_on(pa_fork_tables_kernel, ctas, kShareThreads, false, stream, p, per)) return PA_ERR_CUDA;
+    if (!launch_on(pa_fork_tables_kernel, ctas, kShareThreads, false, 0, stream, p, per)) return PA_ERR_CUDA;
     const int count_ctas = std::max(1, std::min(p.B, 4 * kShareCtas));
-    return launch_on(pa_fork_counts_kernel, count_ctas, kShareThreads, false, stream, p) ? PA_OK : PA_ERR_CUDA;
+    return launch_on(pa_fork_counts_kernel, count_ctas, kShareThreads, false, 0, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_release_shared_block_tables(const int32_t *seq_lens, const int32_t *finished, const int32_t *block_table,
@@ -612,10 +874,11 @@ pa_status pa_release_shared_block_tables(const int32_t *seq_lens, const int32_t 
                            {share_counts_out, 4 * num_pages, true, true},
                            {num_free_out, 4, true, true}});
     if (st != PA_OK) return st;
-    if (!launch_on(pa_release_lens_kernel, share_ctas(p), kShareThreads, false, stream, p)) return PA_ERR_CUDA;
+    if (suits_cluster(p)) return launch_cluster(pa_release_cluster_kernel, p, 281, stream);
+    if (!launch_on(pa_release_lens_kernel, share_ctas(p), kShareThreads, false, 0, stream, p)) return PA_ERR_CUDA;
     const int count_ctas = std::max(1, std::min(p.B, 4 * kShareCtas));
-    if (!launch_on(pa_release_counts_kernel, count_ctas, kShareThreads, false, stream, p)) return PA_ERR_CUDA;
-    return launch_on(pa_release_pool_kernel, kScanCtas, kScanThreads, true, stream, p) ? PA_OK : PA_ERR_CUDA;
+    if (!launch_on(pa_release_counts_kernel, count_ctas, kShareThreads, false, 0, stream, p)) return PA_ERR_CUDA;
+    return launch_on(pa_release_pool_kernel, kScanCtas, kScanThreads, true, 0, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_compact_block_tables(const int32_t *seq_lens, int32_t *block_table, const int32_t *free_pages,
@@ -659,9 +922,14 @@ pa_status pa_compact_block_tables(const int32_t *seq_lens, int32_t *block_table,
                             {copy_dst, moved, true, true},
                             {extent, 4, true, true}});
     if (st != PA_OK) return st;
-    if (!launch_on(pa_compact_pool_kernel, kScanCtas, kScanThreads, true, stream, p)) return PA_ERR_CUDA;
+    if (p.num_pages <= (int64_t)kScanCtas * kClusterPages) {
+        st = launch_cluster(pa_compact_cluster_kernel, p, 282, stream);
+        if (st != PA_OK) return st;
+    } else if (!launch_on(pa_compact_pool_kernel, kScanCtas, kScanThreads, true, 0, stream, p)) {
+        return PA_ERR_CUDA;
+    }
     const int ctas = std::max(1, std::min(p.B, 4 * kShareCtas));
-    return launch_on(pa_compact_tables_kernel, ctas, kShareThreads, false, stream, p) ? PA_OK : PA_ERR_CUDA;
+    return launch_on(pa_compact_tables_kernel, ctas, kShareThreads, false, 0, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_copy_cache_pages(void *const *caches, int32_t num_caches, const int32_t *copy_src,
@@ -697,7 +965,7 @@ pa_status pa_copy_cache_pages(void *const *caches, int32_t num_caches, const int
         p.caches[i] = static_cast<uint8_t *>(caches[i]);
     }
     const int64_t units = (int64_t)num_pairs * num_caches * parts_per_page * pieces;
-    return launch_on(pa_copy_cache_pages_kernel, (int)std::min<int64_t>(kCopyCtas, units), kCopyThreads, false, stream, p)
+    return launch_on(pa_copy_cache_pages_kernel, (int)std::min<int64_t>(kCopyCtas, units), kCopyThreads, false, 0, stream, p)
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -10,7 +10,7 @@ cudaError_t launch_prefix_f32(int head_dim, const CUtensorMap &tk, const CUtenso
     if (head_dim == 256)
         return launch_verify_tc<256, 2, 3, 0, 2, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 236);
     if (head_dim == 128)
-        return launch_verify_tc<128, 6, 6, 0, 2, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 237);
+        return launch_verify_tc<128, 2, 2, 0, 1, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 237);
     return cudaErrorInvalidValue;
 }
 

@@ -274,7 +274,7 @@ __device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
 template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64, bool F4 = false, int PT = 2>
 struct VerifyTcCfg {
     static constexpr bool F8 = NSG > 0;                // fp8 or fp4 cache: staging ring of NSG slots per tensor
-    static constexpr bool QSM = D == 256 && (TK == 128 || PT == 3);  // Q in shared memory
+    static constexpr bool QSM = (D == 256 && TK == 128) || (PT == 3 && (D == 256 || NSB == 1));  // Q in shared memory
     static constexpr int SW = PT == 3 ? 96 : TK;       // columns of an S/P buffer
     static constexpr int M = 128;                      // MMA rows (query rows, zero padded)
     static constexpr int TT = 64;                      // tokens per V tile (4 TMA chunks)
@@ -289,7 +289,9 @@ struct VerifyTcCfg {
     static constexpr int STG_BYTES = F4 ? CPT * fp4::rec_bytes(D)  // the tile's records
                                         : TT * D;  // one e4m3 tile, [D/128][64 tokens][128 B] swizzled
     static constexpr int OFF_V = NK * KTILE_BYTES;      // K ring, then V ring
-    static constexpr int OFF_STG = OFF_V + NV * TILE_BYTES;  // K staging, then V staging
+    static constexpr int SROW = D * 4 + 16;             // epilogue: output rows staged in the K/V rings
+    static constexpr int RINGS = OFF_V + NV * TILE_BYTES;
+    static constexpr int OFF_STG = RINGS > M * SROW ? RINGS : (M * SROW + 1023) / 1024 * 1024;  // K staging, then V staging
     static constexpr int OFF_Q = OFF_STG + 2 * NSG * STG_BYTES;  // QSM: Q as [D/64][M rows][128 B], swizzled
     static constexpr int Q_BYTES = QSM ? M * D * 2 : 0;
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
@@ -316,7 +318,6 @@ struct VerifyTcCfg {
     static constexpr int QROW = D * 2 + 16;            // fp4: rows of Q in f16, staged in the V ring
     static constexpr int OFF_QPRE = OFF_V + M * QROW;  // and their pre-scales
     static_assert(!F4 || M * (QROW + 4) <= NV * TILE_BYTES, "the staged Q rows fit in the V ring");
-    static constexpr int SROW = D * 4 + 16;            // epilogue: output rows staged in the K/V rings
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
     static constexpr int W0 = F4 ? 8 : 6;              // first widening warp
     static constexpr int THREADS = (F8 ? W0 + 2 * CW : 6) * 32;
@@ -575,7 +576,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     const int n_tiles = (n_my + CPK - 1) / CPK;   // score tiles (K tiles)
     const int n_vtiles = (n_my + CPT - 1) / CPT;  // V tiles (VPK per score tile)
     // tile i starts O anew: what the tiles before it summed goes to the second sum
-    auto far_at = [&](int i) { return FAR && i > 0 && i % kVerifyFarTiles == 0; };
+    constexpr int kFarTiles = PT == 3 && D == 256 ? 3 : kVerifyFarTiles;  // (three products a step, and Q K^T's own loss)
+    auto far_at = [&](int i) { return FAR && i > 0 && i % kFarTiles == 0; };
 
     // The split's block-table entries, staged in shared memory by all threads
     // (visible to the producer after the next __syncthreads); splits spanning
@@ -1402,7 +1404,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                             break;
                         }
                         tc::fence_after();
-                        if (n_live > 0) far_add(m_win, i == kVerifyFarTiles);  // (a warp without rows has nothing to move)
+                        if (n_live > 0) far_add(m_win, i == kFarTiles);  // (a warp without rows has nothing to move)
                     }
                 }
                 tc::fence_before();
@@ -1571,7 +1573,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                 for (int k = 0; k < 4; ++k) tc::ld16_nowait(lane_base + C::O_COL + c1 + 16 * k, r[k]);
                 tc::wait_ld();
                 if constexpr (FAR) {
-                    if (n_tiles > kVerifyFarTiles && n_live > 0) {
+                    if (n_tiles > kFarTiles && n_live > 0) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float4 *at = far_place(c1 / 4 + j);

@@ -69,7 +69,7 @@ def run_compact(p, bs, most):
 
 
 SIZES = [(1, 3, 16, 5), (2, 1, 1, 1), (9, 12, 16, 40), (40, 30, 784, 7), (255, 9, 16, 300), (257, 5, 48, 3), (700, 6, 16, 1),
-         (3000, 4, 5, 2000)]
+         (3000, 4, 5, 2000), (2100, 70, 16, 900)]  # (the last: more entries than one cluster walks)
 
 
 @pytest.mark.parametrize("B,width,bs,spare", SIZES)
@@ -148,7 +148,7 @@ def test_release_of_what_was_not_held():
     assert status == code == pa.PA_DEV_BAD_PAGE
 
 
-@pytest.mark.parametrize("B,width,bs,spare", SIZES + [(30, 400, 16, 70000)])
+@pytest.mark.parametrize("B,width,bs,spare", SIZES + [(30, 400, 16, 70000), (30, 400, 16, 420000)])  # (the last: more pages than one cluster holds)
 @pytest.mark.parametrize("most", [1, 7, 300])
 def test_compact_matches_the_model(B, width, bs, spare, most):
     rng = np.random.default_rng(B * 7 + width)
