@@ -12,12 +12,18 @@
 // takes a prefix sum over the pages.  The outputs are buffers of their own, so that
 // a replayed call gives the same again.
 //
-// A step of a serving loop is one launch of one cluster of 8 CTAs: the pages are
-// spread over their shared memories, an entry of a block table adds to its page's
-// counter there, and the sums pass through distributed shared memory.  That holds
-// 409,600 pages.  More pages, or tables of more than kClusterEntries entries,
-// which 8 SMs would take long to walk, go through kernels that fill the GPU: one
-// copies the counts, the next adds to them, a cluster scans.
+// What bounds them is the chain of launches and of dependent loads.  A release
+// and a compaction are one cluster of 8 CTAs (and the rewriting of the tables): the
+// pages are spread over the CTAs' shared memories, which hold 409,600, an entry of a
+// block table adds to its page's counter there, and the sums pass through
+// distributed shared memory.  Where 8 SMs would take long to walk the pages and
+// the tables, a release goes through kernels that fill the GPU: one copies the
+// counts, the next adds to them, a cluster scans.  A fork has nothing to scan; it
+// takes two such kernels at any size.
+// (us per call, requests x pages per request of a pool of so many pages, release
+// by one cluster / by three kernels: 64 x 40, 1.2K: 6.3 / 8.0; 256 x 100, 15K: 7.4 /
+// 9.0; 256 x 300, 60K: 12 / 11.  Fork 4.8 us for 8 requests, 10.4 for 1000 x 600;
+// as one cluster it took 6.9 and 12.)
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -30,9 +36,9 @@ constexpr int kShareThreads = 256;
 constexpr int kShareCtas = 304;       // two per SM
 constexpr int kScanCtas = 8;          // CTAs of the cluster that scans the pages
 constexpr int kScanThreads = 1024;
-constexpr int kScanItems = 4;         // pages per thread and step
+constexpr int kScanItems = 8;         // pages per thread and step
 constexpr int kClusterPages = 50 * 1024;         // counters of a CTA of the cluster (200 KiB)
-constexpr int64_t kClusterEntries = 128 * 1024;  // of the block table
+constexpr int64_t kClusterMost = 64 * 1024;      // pages, and entries of the block table, of a release by one cluster
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPiece = 16 * 1024; // bytes that a CTA copies at a time: four 16-byte loads per thread
 constexpr int kCopyCtas = 152 * 8;
@@ -65,10 +71,25 @@ __device__ __forceinline__ int pool_of(const ShareParams &p, bool flag) {
 
 __device__ __forceinline__ bool valid_page(const ShareParams &p, int page) { return page >= 0 && page < p.num_pages; }
 
+// For i = first, first + stride, ... below n: use(i, load(i)), eight loads at a
+// time (one by one, every step would wait for its own).
+template <typename Load, typename Use>
+__device__ __forceinline__ void for_each(int64_t first, int64_t n, int64_t stride, Load load, Use use) {
+    constexpr int U = 8;
+    for (int64_t i0 = first; i0 < n; i0 += U * stride) {
+        int v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * stride < n) v[u] = load(i0 + u * stride);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * stride < n) use(i0 + u * stride, v[u]);
+    }
+}
+
 __device__ __forceinline__ void copy_shares(const ShareParams &p) {
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.num_pages;
-         i += (int64_t)gridDim.x * blockDim.x)
-        p.shares_out[i] = p.shares[i];
+    for_each((int64_t)blockIdx.x * blockDim.x + threadIdx.x, p.num_pages, (int64_t)gridDim.x * blockDim.x,
+             [&](int64_t i) { return p.shares[i]; }, [&](int64_t i, int v) { p.shares_out[i] = v; });
 }
 
 // Sum of v over the CTA (every thread gets it); `tmp`: 32 words.
@@ -285,7 +306,7 @@ struct Share {
     int lo, hi;
 };
 __device__ __forceinline__ Share share_of(int n) {
-    const int per = (n + kScanThreads - 1) / kScanThreads;
+    const int per = (n + kScanThreads - 1) / kScanThreads | 1;  // (odd: a warp's lanes meet 32 banks)
     const int lo = min(n, (int)threadIdx.x * per);
     return {lo, min(n, lo + per)};
 }
@@ -303,84 +324,14 @@ __device__ __forceinline__ int64_t cluster_before(int total, int *box, int64_t &
     return before;
 }
 
-// ---- the calls of a step, a cluster each ----------------------------------------
-
-__global__ void __launch_bounds__(kScanThreads) pa_fork_cluster_kernel(const ShareParams p) {
-    pdl_wait_primary();  // (no early launch of dependents: a kernel behind may read tables ahead of the stream order)
-    extern __shared__ int32_t counts[];
-    __shared__ int tmp[32];
-    __shared__ int box[kScanCtas];
-    const Counters c = counters_of(p, counts);
-    for (int i = threadIdx.x; i < c.n; i += kScanThreads) counts[i] = 0;
-    cluster_sync();
-    // the requests of this CTA, a thread each (kClusterEntries bounds them), and what all requests before them want
-    const int per = (p.B + kScanCtas - 1) / kScanCtas, b0 = min(p.B, per * (int)blockIdx.x), b1 = min(p.B, b0 + per);
-    const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
-    int wanted = 0;
-    for (int i0 = b0; i0 < b1; i0 += kScanThreads) {
-        const int b = i0 + threadIdx.x;
-        wanted += b < b1 ? wants(p, child_of(p, b)) : 0;
-    }
-    int64_t all;
-    int64_t before = cluster_before(block_sum(wanted, tmp), box, all);
-    __shared__ int job_parent[kScanThreads], job_full[kScanThreads];  // of the requests at hand; parent -1: nothing to do
-    for (int i0 = b0; i0 < b1; i0 += kScanThreads) {
-        const int b = i0 + threadIdx.x;
-        const bool in = b < b1;
-        Child k{-1, 0, false, false};
-        if (in) k = child_of(p, b);
-        const int want = wants(p, k);
-        int total;
-        const int64_t upto = before + block_before(want, tmp, total) + want;
-        before += total;
-        const bool served = k.ok && (!want || upto <= F);
-        job_parent[threadIdx.x] = served ? k.parent : -1;
-        job_full[threadIdx.x] = k.len / p.block_size;
-        if (in) {
-            const int len = p.lens[b], full = k.len / p.block_size;
-            const bool part = served && want;
-            const int page = part ? p.free_pages[F - upto] : -1;
-            int bits = 0;
-            if (k.is ? !k.ok : (len < 0 || len > room_of(p))) bits |= PA_DEV_BAD_SEQLEN;
-            if (k.ok && !served) bits |= PA_DEV_NO_PAGES;
-            if (part && !valid_page(p, page)) bits |= PA_DEV_BAD_PAGE;
-            p.lens_out[b] = served ? k.len : max(len, 0);
-            p.src[b] = part ? p.table[(int64_t)k.parent * p.width + full] : -1;
-            p.dst[b] = page;
-            p.tokens[b] = part ? k.len % p.block_size : 0;
-            if (part) p.table[(int64_t)b * p.width + full] = page;
-            if (bits) set_status(p.status, bits);
-        }
-        __syncthreads();
-        // the full pages: a warp per child
-        for (int i = threadIdx.x >> 5; i < min(kScanThreads, b1 - i0); i += kScanThreads / 32) {
-            const int parent = job_parent[i], full = job_full[i];
-            if (parent < 0) continue;
-            const int32_t *from = p.table + (int64_t)parent * p.width;
-            int32_t *to = p.table + (int64_t)(i0 + i) * p.width;
-            for (int e = threadIdx.x & 31; e < full; e += 32) {
-                const int page = from[e];
-                to[e] = page;
-                if (valid_page(p, page))
-                    counter_add(c, page, 1);
-                else
-                    set_status(p.status, PA_DEV_BAD_PAGE);
-            }
-        }
-        __syncthreads();
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = F - (int)min((int64_t)F, all);
-    cluster_sync();  // every holder is counted
-    for (int i = threadIdx.x; i < c.n; i += kScanThreads) p.shares_out[c.lo + i] = p.shares[c.lo + i] + counts[i];
-}
-
 __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const ShareParams p) {
     pdl_wait_primary();  // (no early launch of dependents, as above)
     extern __shared__ int32_t counts[];
     __shared__ int tmp[32];
     __shared__ int box[kScanCtas];
     const Counters c = counters_of(p, counts);
-    for (int i = threadIdx.x; i < c.n; i += kScanThreads) counts[i] = p.shares[c.lo + i];
+    for_each(threadIdx.x, c.n, kScanThreads, [&](int64_t i) { return p.shares[c.lo + i]; },
+             [&](int64_t i, int v) { counts[i] = v; });
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();
     // a warp per request
@@ -431,7 +382,8 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const Sha
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
     int mine = 0;
-    for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kScanThreads) mine += __ldcg(p.shares_out + i) < 0;
+    for_each(s.lo + threadIdx.x, s.hi, kScanThreads, [&](int64_t i) { return __ldcg(p.shares_out + i); },
+             [&](int64_t, int v) { mine += v < 0; });
     cluster_share(block_sum(mine, tmp), box);
     int64_t at = F, all = F;
     for (int c = 0; c < kScanCtas; ++c) {
@@ -488,19 +440,18 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
     const int tid = blockIdx.x * kScanThreads + threadIdx.x;
     constexpr int stride = kScanCtas * kScanThreads;
     if (threadIdx.x == 0) top = 0;
-    for (int i = threadIdx.x; i < c.n; i += kScanThreads) {
+    for_each(threadIdx.x, c.n, kScanThreads, [&](int64_t i) { return p.shares[c.lo + i]; }, [&](int64_t i, int v) {
         used[i] = 1;
-        __stcg(p.page_map + c.lo + i, c.lo + i);
-        __stcg(p.shares_out + c.lo + i, p.shares[c.lo + i]);
-    }
+        __stcg(p.page_map + c.lo + i, c.lo + (int)i);
+        __stcg(p.shares_out + c.lo + i, v);
+    });
     cluster_sync();
-    for (int i = tid; i < F; i += stride) {
-        const int page = p.free_pages[i];
+    for_each(tid, F, stride, [&](int64_t i) { return p.free_pages[i]; }, [&](int64_t, int page) {
         if (valid_page(p, page))
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(counter_at(c, page)), "r"(0) : "memory");
         else
             set_status(p.status, PA_DEV_BAD_PAGE);
-    }
+    });
     cluster_sync();
     const Share s = share_of(c.n);
     int mine = 0;
@@ -575,7 +526,8 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
     }
     cluster_sync();
     int mine = 0;
-    for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kScanThreads) mine += __ldcg(p.page_map + i);
+    auto mark = [&](int64_t i) { return __ldcg(p.page_map + i); };
+    for_each(s.lo + threadIdx.x, s.hi, kScanThreads, mark, [&](int64_t, int v) { mine += v; });
     cluster_share(block_sum(mine, tmp), box[0]);
     int64_t before = 0, n = 0;
     for (int c = 0; c < kScanCtas; ++c) {
@@ -583,7 +535,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
         n += box[0][c];
     }
     mine = 0;
-    for (int64_t i = max(s.lo, n) + threadIdx.x; i < s.hi; i += kScanThreads) mine += __ldcg(p.page_map + i);
+    for_each(max(s.lo, n) + threadIdx.x, s.hi, kScanThreads, mark, [&](int64_t, int v) { mine += v; });
     cluster_share(block_sum(mine, tmp), box[1]);
     int64_t m = 0;
     for (int c = 0; c < kScanCtas; ++c) m += box[1][c];
@@ -774,10 +726,10 @@ int share_ctas(const ShareParams &p) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(kShareCtas, std::max<int64_t>(pages, p.B)));
 }
 
-// Whether a step's pages and tables suit one cluster, and its launch with the
-// counters of `per` pages in every CTA.
+// Whether a release's pages and tables suit one cluster; a cluster's launch, with
+// the counters of its share of the pages in every CTA.
 bool suits_cluster(const ShareParams &p) {
-    return p.num_pages <= (int64_t)kScanCtas * kClusterPages && (int64_t)p.B * p.width <= kClusterEntries;
+    return p.num_pages <= kClusterMost && (int64_t)p.B * p.width <= kClusterMost;
 }
 pa_status launch_cluster(void (*kern)(ShareParams), const ShareParams &p, int slot, void *stream) {
     const size_t smem = 4 * ((((size_t)p.num_pages + kScanCtas - 1) / kScanCtas + 3) & ~size_t(3));
@@ -832,7 +784,6 @@ pa_status pa_fork_block_tables(const int32_t *seq_lens, const int32_t *parent, i
                             {copy_tokens, rows, true, true},
                             {num_free_out, 4, true, true}});
     if (st != PA_OK) return st;
-    if (suits_cluster(p)) return launch_cluster(pa_fork_cluster_kernel, p, 280, stream);
     const int ctas = share_ctas(p);
     // whole CTAs of requests: at least one request, so that the last CTA that has any writes the pool's size
     const int per = std::max(1, (p.B + ctas - 1) / ctas);
