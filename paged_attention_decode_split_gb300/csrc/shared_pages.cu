@@ -73,10 +73,10 @@ __device__ __forceinline__ bool valid_page(const ShareParams &p, int page) { ret
 
 // For i = first, first + stride, ... below n: use(i, load(i)), eight loads at a
 // time (one by one, every step would wait for its own).
-template <typename Load, typename Use>
-__device__ __forceinline__ void for_each(int64_t first, int64_t n, int64_t stride, Load load, Use use) {
+template <typename I, typename Load, typename Use>
+__device__ __forceinline__ void for_each(I first, I n, I stride, Load load, Use use) {
     constexpr int U = 8;
-    for (int64_t i0 = first; i0 < n; i0 += U * stride) {
+    for (I i0 = first; i0 < n; i0 += U * stride) {
         int v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -313,9 +313,9 @@ __device__ __forceinline__ Share share_of(int n) {
 
 // Sum of v over the CTAs before this one (and the threads before this one, which
 // block_before gave), and over all: `box` is used once.
-__device__ __forceinline__ int64_t cluster_before(int total, int *box, int64_t &all) {
+__device__ __forceinline__ int cluster_before(int total, int *box, int &all) {
     cluster_share(total, box);
-    int64_t before = 0;
+    int before = 0;
     all = 0;
     for (int c = 0; c < kScanCtas; ++c) {
         if (c < (int)blockIdx.x) before += box[c];
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const 
     __shared__ int tmp[32];
     __shared__ int box[kScanCtas];
     const Counters c = counters_of(p, counts);
-    for_each(threadIdx.x, c.n, kScanThreads, [&](int64_t i) { return p.shares[c.lo + i]; },
-             [&](int64_t i, int v) { counts[i] = v; });
+    for_each((int)threadIdx.x, c.n, kScanThreads, [&](int i) { return p.shares[c.lo + i]; },
+             [&](int i, int v) { counts[i] = v; });
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();
     // a warp per request
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const 
     for (int i = s.lo; i < s.hi; ++i) mine += counts[i] < 0;
     int total;
     const int in_cta = block_before(mine, tmp, total);
-    int64_t all;
-    int64_t to = F + cluster_before(total, box, all) + in_cta;
+    int all;
+    int64_t to = (int64_t)F + cluster_before(total, box, all) + in_cta;
     if (mine > 0) {
         for (int i = s.lo; i < s.hi; ++i) {
             if (counts[i] >= 0) continue;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const 
         }
     }
     for (int i = threadIdx.x; i < c.n; i += kScanThreads) p.shares_out[c.lo + i] = max(counts[i], 0);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = (int)min(F + all, p.num_pages);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = (int)min((int64_t)F + all, p.num_pages);
     cluster_sync();  // (no CTA leaves while another may still write into its shared memory)
 }
 
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const Sha
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
     int mine = 0;
-    for_each(s.lo + threadIdx.x, s.hi, kScanThreads, [&](int64_t i) { return __ldcg(p.shares_out + i); },
+    for_each(s.lo + threadIdx.x, s.hi, (int64_t)kScanThreads, [&](int64_t i) { return __ldcg(p.shares_out + i); },
              [&](int64_t, int v) { mine += v < 0; });
     cluster_share(block_sum(mine, tmp), box);
     int64_t at = F, all = F;
@@ -434,19 +434,19 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
     __shared__ int tmp[32];
     __shared__ int box[3][kScanCtas];
     __shared__ int top;
-    const int64_t P = p.num_pages;
+    const int P = (int)p.num_pages;
     const Counters c = counters_of(p, used);
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     const int tid = blockIdx.x * kScanThreads + threadIdx.x;
     constexpr int stride = kScanCtas * kScanThreads;
     if (threadIdx.x == 0) top = 0;
-    for_each(threadIdx.x, c.n, kScanThreads, [&](int64_t i) { return p.shares[c.lo + i]; }, [&](int64_t i, int v) {
+    for_each((int)threadIdx.x, c.n, kScanThreads, [&](int i) { return p.shares[c.lo + i]; }, [&](int i, int v) {
         used[i] = 1;
-        __stcg(p.page_map + c.lo + i, c.lo + (int)i);
+        __stcg(p.page_map + c.lo + i, c.lo + i);
         __stcg(p.shares_out + c.lo + i, v);
     });
     cluster_sync();
-    for_each(tid, F, stride, [&](int64_t i) { return p.free_pages[i]; }, [&](int64_t, int page) {
+    for_each(tid, F, stride, [&](int i) { return p.free_pages[i]; }, [&](int, int page) {
         if (valid_page(p, page))
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(counter_at(c, page)), "r"(0) : "memory");
         else
@@ -458,31 +458,30 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
     for (int i = s.lo; i < s.hi; ++i) mine += used[i];
     int total;
     const int in_cta = block_before(mine, tmp, total);
-    int64_t n;
-    int64_t bef = cluster_before(total, box[0], n) + in_cta;
+    int n;  // (pages are fewer than 2^19 here)
+    int bef = cluster_before(total, box[0], n) + in_cta;
     mine = 0;
-    for (int i = max((int64_t)s.lo, n - c.lo); i < s.hi; ++i) mine += used[i];
-    int64_t m;
+    for (int i = max(s.lo, n - c.lo); i < s.hi; ++i) mine += used[i];
+    int m;
     cluster_before(block_sum(mine, tmp), box[1], m);
-    m = min(m, (int64_t)p.moves);
-    const int64_t n_free = P - n;
+    m = min(m, p.moves);
+    const int n_free = P - n;
     int highest = 0;
     for (int i = s.lo; i < s.hi; ++i) {
-        const int64_t page = c.lo + i;
-        const int u = used[i];
-        const int64_t rank = u ? n - 1 - bef : page - bef;  // from the top, from the bottom
+        const int page = c.lo + i, u = used[i];
+        const int rank = u ? n - 1 - bef : page - bef;  // from the top, from the bottom
         const bool moves = rank < m && (u ? page >= n : page < n);
-        if (moves) __stcg((u ? p.src : p.dst) + rank, (int)page);
+        if (moves) __stcg((u ? p.src : p.dst) + rank, page);
         if ((u != 0) != moves) {  // in use from now on
-            highest = (int)page + 1;
+            highest = page + 1;
         } else {
-            const int64_t in_use = bef + min(m, page - bef) - max((int64_t)0, bef - (n - m));
-            p.free_out[n_free - 1 - (page - in_use)] = (int)page;
+            const int in_use = bef + min(m, page - bef) - max(0, bef - (n - m));
+            p.free_out[n_free - 1 - (page - in_use)] = page;
         }
         bef += u;
     }
     for (int64_t i = m + tid; i < p.moves; i += stride) p.src[i] = p.dst[i] = -1;
-    for (int64_t i = n_free + tid; i < P; i += stride) p.free_out[i] = -1;
+    for (int i = n_free + tid; i < P; i += stride) p.free_out[i] = -1;
     highest = __reduce_max_sync(0xffffffffu, highest);
     if ((threadIdx.x & 31) == 0) atomicMax(&top, highest);
     __syncthreads();
@@ -527,7 +526,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
     cluster_sync();
     int mine = 0;
     auto mark = [&](int64_t i) { return __ldcg(p.page_map + i); };
-    for_each(s.lo + threadIdx.x, s.hi, kScanThreads, mark, [&](int64_t, int v) { mine += v; });
+    for_each(s.lo + threadIdx.x, s.hi, (int64_t)kScanThreads, mark, [&](int64_t, int v) { mine += v; });
     cluster_share(block_sum(mine, tmp), box[0]);
     int64_t before = 0, n = 0;
     for (int c = 0; c < kScanCtas; ++c) {
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
         n += box[0][c];
     }
     mine = 0;
-    for_each(max(s.lo, n) + threadIdx.x, s.hi, kScanThreads, mark, [&](int64_t, int v) { mine += v; });
+    for_each(max(s.lo, n) + threadIdx.x, s.hi, (int64_t)kScanThreads, mark, [&](int64_t, int v) { mine += v; });
     cluster_share(block_sum(mine, tmp), box[1]);
     int64_t m = 0;
     for (int c = 0; c < kScanCtas; ++c) m += box[1][c];
