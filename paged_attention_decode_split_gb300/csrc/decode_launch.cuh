@@ -80,7 +80,7 @@ cudaError_t launch_decode_cfg(int head_dim, int group, const CUtensorMap &tk, co
     return cudaErrorInvalidValue;
     if constexpr (SH && F8) {
         if (head_dim == 256) {
-            PA_DECODE_CASES(256, 4, 3, 1, true, 4, 6, 1, slot0)
+            PA_DECODE_CASES(256, 4, 3, 1, true, 6, 4, 1, slot0)
         } else if (head_dim == 128) {
             PA_DECODE_CASES(128, 6, 4, 1, true, 6, 8, 1, slot0 + 10)
         }

@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kMaxChunksPerSplit = 256; // 4096 tokens: bounds the longest CTA for load balance
 constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tokens
-constexpr int kMaxOwnChunks = 128;        // a split of a sequence's own part, unless there are many: 2048 tokens
 constexpr int64_t kMinShared = 6 << 20;   // elements of K that sharing must save
 constexpr int kMaxDevices = 64;
 constexpr int kKernelSlots = 288;
@@ -149,6 +148,7 @@ struct SharedPlan {
     int prefix_splits, prefix_chunks, prefix_most;
     int suffix_splits, suffix_chunks, suffix_most;  // likewise of a sequence's own part
     int row_blocks;                    // of the largest group
+    int copies;                        // of its rows, over a bf16 cache: records of a prefix split
     size_t ws_bytes, off_part_ml;
 };
 
@@ -208,14 +208,16 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
     if (ss == 0) {
         ss = static_cast<int>(std::max<int64_t>(1, sms / seqs));
         ss = std::min(ss, std::max(1, own / kMinChunksPerSplit));
-        if (seqs < 4 * sms) ss = std::max(ss, (own + kMaxOwnChunks - 1) / kMaxOwnChunks);
+        if (seqs < sms) ss = std::max(ss, (own + kMaxChunksPerSplit - 1) / kMaxChunksPerSplit);
         const int per = std::max(1, (own + ss - 1) / ss);
         ss = std::max(1, (own + per - 1) / per);
     }
     pl->suffix_splits = std::min(ss, std::max(1, all));
     pl->suffix_chunks = std::max(kMinChunksPerSplit, (own + pl->suffix_splits - 1) / pl->suffix_splits);
     pl->suffix_most = std::max(pl->suffix_chunks, (all + pl->suffix_splits - 1) / pl->suffix_splits);
-    size_t records = static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits + pl->suffix_splits);
+    pl->copies = prefix_copies(d->head_dim, static_cast<int>(rows), true);
+    size_t records =
+        static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits * pl->copies + pl->suffix_splits);
     if (pl->prefix_splits + pl->suffix_splits == 1) records = 0;  // (the outputs themselves)
     pl->off_part_ml = round256(records * d->head_dim * sizeof(float));
     pl->ws_bytes = pl->off_part_ml + records * sizeof(float2);
@@ -914,7 +916,8 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     p.block_size = desc->block_size;
     p.chunks_per_split = pl.prefix_most;
     p.prefix_chunks = pl.prefix_chunks;
-    p.num_splits = pl.prefix_splits + pl.suffix_splits;
+    const int prefix_records = pl.prefix_splits * (fp8 || fp4 ? 1 : pl.copies);
+    p.num_splits = prefix_records + pl.suffix_splits;
     p.scale_log2 = desc->scale * 1.4426950408889634f;
     p.out_bf16 = desc->out_dtype == PA_OUT_BF16;
     p.num_kv_heads = desc->num_kv_heads;
@@ -954,7 +957,7 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     d.group_starts = group_starts;
     d.num_groups = prefix->num_groups;
     d.max_members = p.max_members;
-    d.prefix_splits = pl.prefix_splits;
+    d.prefix_splits = prefix_records;
     d.suffix_splits = pl.suffix_splits;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);

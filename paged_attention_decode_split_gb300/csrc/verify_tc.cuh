@@ -244,6 +244,25 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t (&r)[32]) {
         "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// N 32-bit columns, without waiting.
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 32) {
+        st32(taddr, r);
+    } else {
+        static_assert(N % 8 == 0, "whole groups of columns");
+#pragma unroll
+        for (int c = 0; c < N; c += 8) {
+            const uint32_t part[8] = {r[c], r[c + 1], r[c + 2], r[c + 3], r[c + 4], r[c + 5], r[c + 6], r[c + 7]};
+            st8(taddr + c, part);
+        }
+    }
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
     asm volatile(
@@ -297,7 +316,8 @@ struct VerifyTcCfg {
     static constexpr int OFF_BAR = OFF_Q + Q_BYTES;
     // k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[NSB], p_full[NP], o_done[NSB], mma_fin,
     // then (fp8, fp4) kst_full[NSG], kst_empty[NSG], vst_full[NSG], vst_empty[NSG]
-    static constexpr int CW = F4 ? 8 : 2;              // fp8, fp4: widening warps per tensor
+    static constexpr bool F8W = F8 && !F4 && PT == 1 && D == 256;  // e4m3, one number per weight: widening bounds it
+    static constexpr int CW = F4 ? 8 : F8W ? 4 : 2;    // fp8, fp4: widening warps per tensor
     static constexpr int NP = F8 ? NV : NSB;           // P barriers (fp8, fp4: the V slot's too)
     static constexpr int OFF_TMEM = OFF_BAR + (2 * NK + 2 * NV + 2 * NSB + NP + 1 + 4 * NSG) * 8;
     static constexpr int OFF_FLAGS = OFF_TMEM + 16;
@@ -319,11 +339,12 @@ struct VerifyTcCfg {
     static constexpr int OFF_QPRE = OFF_V + M * QROW;  // and their pre-scales
     static_assert(!F4 || M * (QROW + 4) <= NV * TILE_BYTES, "the staged Q rows fit in the V ring");
     static_assert(M * SROW <= OFF_STG, "the staged output rows fit in the K/V rings");
-    static constexpr int W0 = F4 ? 8 : 6;              // first widening warp
+    static constexpr int W0 = F4 || F8W ? 8 : 6;       // first widening warp
     static constexpr int THREADS = (F8 ? W0 + 2 * CW : 6) * 32;
-    // fp4: registers of the softmax warpgroup and of the others (setmaxnreg).  Their sum draws on what the block
-    // was launched with, which the launch checks.
-    static constexpr int REGS_SM = 152, REGS_OTHER = 64;
+    // many widening warps: registers of the softmax warpgroup and of the others (setmaxnreg).  Their sum draws on
+    // what the block was launched with, which the launch checks.
+    static constexpr bool RSPLIT = F4 || F8W;
+    static constexpr int REGS_SM = F4 ? 152 : 168, REGS_OTHER = F4 ? 64 : 104;
     static constexpr int REGS_LAUNCH = (128 * REGS_SM + (THREADS - 128) * REGS_OTHER + THREADS - 1) / THREADS;
     static_assert(D == 256 || D == 128, "head_dim 256 or 128");
     static_assert(Q_COL + Q_TCOLS <= TMEM_COLS, "tensor-memory columns");
@@ -355,8 +376,12 @@ constexpr int kVerifyFarTiles = 4;
 constexpr float kExactLogits = 16777216.f;
 // SH: the common part of a decode over shared prefixes (VerifyParams): no causal
 // mask, a row per sequence and head.
+// COP: up to M / COP rows stand in the block COP times, and copy k takes keys k * 64
+// / COP .. of every tile, with zeros for its other weights: small groups leave
+// most softmax threads without a row, and a tile waits for the few that have one.
+// A copy is a split of its own to the merge.
 template <int D, int NK, int NV, int NSG, int NSB, int TK = 64, bool F4 = false, bool RES = true,
-          bool FAR = false, bool SH = false, int PT = RES ? 2 : 1>
+          bool FAR = false, bool SH = false, int PT = RES ? 2 : 1, int COP = 1>
 __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::THREADS,
                                   VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::CTAS)
     pa_verify_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -367,6 +392,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     static_assert(RES == (PT > 1) && (RES || (F8 && C::VPK == 1)), "the residual is left out over quantised caches only");
     constexpr int TT = C::TT, CPT = C::CPT, CPK = C::CPK, VPK = C::VPK;
     static_assert(!FAR || (RES && C::VPK == 1), "a second sum of O: fp32 output");
+    constexpr int RB = C::M / COP, KPT = TT / COP;  // rows of a copy; keys of a tile per softmax thread
+    static_assert(COP == 1 || (SH && VPK == 1 && !F4), "copies of rows: the common part of a shared prefix");
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
     // fp4: the reference is kept 2^7 below the max, so that P in f16, at most 2^15,
     // holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
@@ -408,6 +435,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     const int n_blocks = gridDim.y / p.num_kv_heads;
     const int row0 = (n_blocks - 1 - (int)(blockIdx.y / p.num_kv_heads)) * C::M;  // first row (rho = r G + g)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row_l = COP > 1 ? (int)threadIdx.x % RB : (int)threadIdx.x;  // softmax threads: row of the block, and its copy
+    [[maybe_unused]] const int copy = COP > 1 ? (int)threadIdx.x / RB : 0;
     const int G = p.group;
     size_t row_base = (size_t)blockIdx.z * p.q_len;  // of the call's (sequence, new row) pairs: this CTA's first
     int members = p.q_len;                           // pairs of this CTA's sequence (SH: sequences of its group)
@@ -436,14 +465,15 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
         if (row0 == 0 && members < hi - lo) {  // more than the host said: rows without a CTA
             if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
             for (int rho = members * G + threadIdx.x; rho < (hi - lo) * G; rho += C::THREADS)
-                p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split] =
-                    make_float2(-INFINITY, -1.f);
+                for (int k = 0; k < COP; ++k)
+                    p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split * COP + k] =
+                        make_float2(-INFINITY, -1.f);
         }
         if (row0 >= members * G) return;  // no row in this block
     } else {
         pdl_launch_dependents();
     }
-    const int R = min(C::M, members * G - row0);  // rows of this block
+    const int R = min(RB, members * G - row0);  // rows of this block
     // SH: what becomes of row rho: 0 its share of the prefix, 1 nothing (an idle
     // sequence), 2 zeros (its lengths are bad, or not those of the group)
     [[maybe_unused]] auto row_state = [&](int rho) {
@@ -491,7 +521,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     // This row's q goes to L2 ahead of the dependency wait: L2 is where global
     // memory is kept coherent, so a row the work before this call is still
     // writing is read in its final state after the wait all the same.
-    const int rho_q = row0 + (int)threadIdx.x;  // the softmax threads' rows (rows past R are zero padding)
+    const int rho_q = row0 + row_l;  // the softmax threads' rows (rows past R are zero padding)
     const __nv_bfloat16 *qrow = p.q + ((row_base + rho_q / G) * p.num_q_heads + kvh * G + rho_q % G) * D;
     if (!SH && !F4 && warp < 4 && (int)threadIdx.x < R) {
 #pragma unroll
@@ -549,9 +579,11 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     const int k_last = SH ? L - 1 : L - p.q_len + (row0 + R - 1) / G;
     const int n_my = min((SH ? n_chunks : min(n_chunks, k_last / kChunk + 1)) - c_begin, cps);
     if (SH && n_my <= 0) {  // the row's other splits have its keys, if there are any
-        for (int rho = row0 + threadIdx.x; rho < row0 + R; rho += C::THREADS)
-            p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split] =
-                make_float2(-INFINITY, row_state(rho) == 2 ? -1.f : 0.f);
+        for (int rho = row0 + threadIdx.x; rho < row0 + R; rho += C::THREADS) {
+            const float2 empty = make_float2(-INFINITY, row_state(rho) == 2 ? -1.f : 0.f);
+            for (int k = 0; k < COP; ++k)
+                p.part_ml[((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split * COP + k] = empty;
+        }
         return;
     }
     if (n_my <= 0) {
@@ -576,7 +608,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     const int n_tiles = (n_my + CPK - 1) / CPK;   // score tiles (K tiles)
     const int n_vtiles = (n_my + CPT - 1) / CPT;  // V tiles (VPK per score tile)
     // tile i starts O anew: what the tiles before it summed goes to the second sum
-    constexpr int kFarTiles = PT == 3 && D == 256 ? 3 : kVerifyFarTiles;  // (three products a step, and Q K^T's own loss)
+    // (three products a step at D = 256, beside Q K^T's own loss: fewer tiles; a copy adds to its sums in every COP-th step)
+    constexpr int kFarTiles = (PT == 3 && D == 256 ? 3 : kVerifyFarTiles) * COP;
     auto far_at = [&](int i) { return FAR && i > 0 && i % kFarTiles == 0; };
 
     // The split's block-table entries, staged in shared memory by all threads
@@ -693,7 +726,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     constexpr int NQ = D / 8;
     [[maybe_unused]] uint4 qv[NQ];
     if (!F4 && warp < 4) {
-        const bool qlive = (int)threadIdx.x < R;
+        const bool qlive = row_l < R;
 #pragma unroll
         for (int v = 0; v < NQ; ++v)
             qv[v] = qlive ? *reinterpret_cast<const uint4 *>(qrow + 8 * v) : make_uint4(0u, 0u, 0u, 0u);
@@ -769,7 +802,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
 
     // (a branch for setmaxnreg: what either side may use is known only where the sides are apart)
     if (warp >= 4) {
-    if constexpr (F4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+    if constexpr (C::RSPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (F4 && (warp == 5 || warp == 6)) {
         // ---------------- fp4 producers: records of K (warp 5) and V (warp 6) ----------------
         const uint64_t policy = l2_policy_evict_first();
@@ -1092,7 +1125,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
             }
         } else if constexpr (F8) {
             // ---------------- fp8: widen staged e4m3 tiles into the K (warps 6, 7) / V (8, 9) ring ----------------
-            const int tensor = (warp - 6) / C::CW, part = (warp - 6) % C::CW;
+            const int tensor = (warp - C::W0) / C::CW, part = (warp - C::W0) % C::CW;
             constexpr int NR0 = NK, NR1 = NV;
             const int NR = tensor == 0 ? NR0 : NR1;
             uint64_t *ring_full = tensor == 0 ? k_full : p_full;
@@ -1150,8 +1183,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     }
     } else {
         // ---------------- softmax: thread = query row = tensor-memory lane ----------------
+        if constexpr (C::RSPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SM));
         if constexpr (F4) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SM));
             // Q, staged by the widening warps (barrier 3), to tensor memory; then the V ring is theirs (barrier 4)
             asm volatile("bar.sync 3, 640;" ::: "memory");
             const uint8_t *qs = smem + C::OFF_V + threadIdx.x * C::QROW;
@@ -1171,8 +1204,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
             asm volatile("bar.arrive 1, 160;" ::: "memory");
             asm volatile("bar.arrive 4, 384;" ::: "memory");
         }
-        const int rho = row0 + threadIdx.x;  // this thread's row (tensor-memory lane threadIdx.x)
-        const bool live = (int)threadIdx.x < R;
+        const int rho = row0 + row_l;  // this thread's row (tensor-memory lane threadIdx.x)
+        const bool live = row_l < R;
+        const int record = split * COP + copy;  // of the row's num_splits
         // last visible key: the causal limit of the row, and never past this
         // split's last chunk (a tile may reach into the next split's tokens)
         const int t_end = min(L, (c_begin + n_my) * kChunk);
@@ -1194,8 +1228,8 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
         // or read, added and stored without red: no less).
         [[maybe_unused]] float m_far = -INFINITY;  // the reference max that the second sum stands for
         [[maybe_unused]] const uint32_t my_row =
-            live ? (uint32_t)(((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + split) : 0u;
-        [[maybe_unused]] const int n_live = min(32, R - warp * 32);
+            live ? (uint32_t)(((row_base + rho / G) * p.num_q_heads + kvh * G + rho % G) * p.num_splits + record) : 0u;
+        [[maybe_unused]] const int n_live = min(32, R - (COP > 1 ? warp * 32 % RB : warp * 32));
         [[maybe_unused]] float *far_base = !SH && p.num_splits == 1 ? static_cast<float *>(p.out) : p.part_o;
         [[maybe_unused]] auto far_place = [&](int j) {  // (the whole warp) the lane's float4 j of the second sum
             const int at = j * n_live + min(lane, n_live - 1);
@@ -1277,43 +1311,44 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
             }
             if constexpr (VPK == 1) {
                 tc::fence_after();
-                float sv[TT];
+                float sv[KPT];
                 {
-                    uint32_t r[TT / 16][16];  // the tile's scores: all loads in flight, one wait
+                    uint32_t r[KPT / 16][16];  // the thread's scores: all loads in flight, one wait
 #pragma unroll
-                    for (int c0 = 0; c0 < TT / 16; ++c0) tc::ld16_nowait(lane_base + C::SBUF(j) + 16 * c0, r[c0]);
+                    for (int c0 = 0; c0 < KPT / 16; ++c0)
+                        tc::ld16_nowait(lane_base + C::SBUF(j) + copy * KPT + 16 * c0, r[c0]);
                     tc::wait_ld();
 #pragma unroll
-                    for (int c = 0; c < TT; ++c) sv[c] = __uint_as_float(r[c / 16][c % 16]);
+                    for (int c = 0; c < KPT; ++c) sv[c] = __uint_as_float(r[c / 16][c % 16]);
                 }
-                const int t0 = (c_begin + i * CPT) * kChunk;
+                const int t_tile = (c_begin + i * CPT) * kChunk, t0 = t_tile + copy * KPT;
                 float mx = -INFINITY;
                 // the exponent is 2^(sv * mul - m): raw scores with mul = scale when
                 // every key of the tile is visible to this row (no mask, and the
                 // max of the scaled scores is the scaled max for scale > 0), else
                 // scaled and masked scores with mul = 1
                 float mul = 1.f;
-                if (sl > 0.f && t0 + TT - 1 <= lim && t0 >= lo) {
+                if (sl > 0.f && t0 + KPT - 1 <= lim && t0 >= lo) {
                     float mr[4];  // four chains: one alone is 32 dependent steps
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mr[c] = fmax3(sv[c], sv[c + 4], sv[c + 8]);
 #pragma unroll
-                    for (int c = 12; c + 7 < TT; c += 8)
+                    for (int c = 12; c + 7 < KPT; c += 8)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mr[e] = fmax3(mr[e], sv[c + e], sv[c + e + 4]);
-                    mr[0] = fmaxf(fmax3(mr[0], sv[TT - 4], sv[TT - 3]), sv[TT - 2]);
-                    mx = fmaxf(fmax3(mr[0], mr[1], mr[2]), fmaxf(mr[3], sv[TT - 1])) * sl;
+                    mr[0] = fmaxf(fmax3(mr[0], sv[KPT - 4], sv[KPT - 3]), sv[KPT - 2]);
+                    mx = fmaxf(fmax3(mr[0], mr[1], mr[2]), fmaxf(mr[3], sv[KPT - 1])) * sl;
                     mul = sl;
                     if (SH && fabsf(mx) > kExactLogits) {
 #pragma unroll
-                        for (int c = 0; c < TT; ++c) sv[c] *= sl;
+                        for (int c = 0; c < KPT; ++c) sv[c] *= sl;
                         mul = 1.f;
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < TT; ++c) sv[c] = (t0 + c <= lim && t0 + c >= lo) ? sv[c] * sl : -INFINITY;
+                    for (int c = 0; c < KPT; ++c) sv[c] = (t0 + c <= lim && t0 + c >= lo) ? sv[c] * sl : -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < TT; c += 2) mx = fmax3(mx, sv[c], sv[c + 1]);
+                    for (int c = 0; c < KPT; c += 2) mx = fmax3(mx, sv[c], sv[c + 1]);
                 }
                 // lazy rescale: only when the max grows by more than 2^kLazy, and
                 // then only after the previous tile's P.V product has finished
@@ -1351,7 +1386,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                 // The tile may be short or end in a partial chunk: V rows past the
                 // end hold stale data (even NaN), and 0 * NaN would reach O through
                 // the tensor core, so zero them before the P.V product reads them.
-                const int nv = min(TT, t_end - t0);
+                const int nv = min(TT, t_end - t_tile);
                 if (!F8 && nv < TT) {  // (fp8: the widening warp writes those rows as zeros)
                     if (!__all_sync(0xffffffffu, mbar_wait(&v_full[i % NV], (i / NV) & 1, &flags[0]))) {
                         ok = false;
@@ -1370,10 +1405,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                 // with no visible key yet (m = -inf) every p is 0: 2^(x - inf)
                 const float m_use = m_ref == -INFINITY ? INFINITY : m_ref;
                 float2 ps2 = make_float2(0.f, 0.f);
-                uint32_t hw[TT / 2];
-                [[maybe_unused]] uint32_t lw[TT / 2], xw[PT == 3 ? TT / 2 : 1];
+                uint32_t hw[KPT / 2];
+                [[maybe_unused]] uint32_t lw[KPT / 2], xw[PT == 3 ? KPT / 2 : 1];
 #pragma unroll
-                for (int c = 0; c < TT / 2; ++c) {
+                for (int c = 0; c < KPT / 2; ++c) {
                     const float p0 = fast_exp2(fmaf(sv[2 * c], mul, -m_use));
                     const float p1 = fast_exp2(fmaf(sv[2 * c + 1], mul, -m_use));
                     ps2 = __fadd2_rn(ps2, make_float2(p0, p1));
@@ -1393,9 +1428,17 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                 } else {
                     l_sum += ps2.x + ps2.y;
                 }
-                tc::st32(lane_base + C::SBUF(j), hw);
-                if constexpr (RES) tc::st32(lane_base + C::SBUF(j) + TT / 2, lw);
-                if constexpr (PT == 3) tc::st32(lane_base + C::SBUF(j) + TT, xw);
+                if constexpr (COP > 1) {  // the other copies' keys: no weight
+                    const uint32_t none[KPT / 2] = {};
+#pragma unroll
+                    for (int k = 1; k < COP; ++k)
+#pragma unroll
+                        for (int h = 0; h < PT; ++h)
+                            tc::st_cols(lane_base + C::SBUF(j) + h * (TT / 2) + (copy + k) % COP * (KPT / 2), none);
+                }
+                tc::st_cols(lane_base + C::SBUF(j) + copy * (KPT / 2), hw);
+                if constexpr (RES) tc::st_cols(lane_base + C::SBUF(j) + TT / 2 + copy * (KPT / 2), lw);
+                if constexpr (PT == 3) tc::st_cols(lane_base + C::SBUF(j) + TT + copy * (KPT / 2), xw);
                 tc::wait_st();
                 if constexpr (FAR) {
                     if (far_at(i)) {  // (O is free for P_i V_i once it has been read)
@@ -1629,7 +1672,7 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
             if (live) {
                 tc::fence_async_smem();  // the staged row is read by the copy engine
                 uint8_t *dst = direct ? static_cast<uint8_t *>(p.out) + orow * D * (bf ? 2 : 4)
-                                      : reinterpret_cast<uint8_t *>(p.part_o + (orow * p.num_splits + split) * D);
+                                      : reinterpret_cast<uint8_t *>(p.part_o + (orow * p.num_splits + record) * D);
                 bulk_store_s2g(dst, srow, bf ? D * 2 : D * 4);
                 bulk_commit();
                 bulk_wait_read();  // the row has left shared memory before the CTA ends
@@ -1641,19 +1684,19 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                 if (direct)
                     store_out(p.out, orow * D + c, 0.f, p.out_bf16);
                 else
-                    p.part_o[(orow * p.num_splits + split) * D + c] = 0.f;
+                    p.part_o[(orow * p.num_splits + record) * D + c] = 0.f;
             }
         }
         if (SH && live) {
             const int state = row_state(rho);
-            p.part_ml[orow * p.num_splits + split] = poisoned || state == 2 ? make_float2(m_ref, -1.f)
-                                                     : state == 1          ? make_float2(-INFINITY, 0.f)
-                                                     : l_sum != l_sum      ? make_float2(0.f, 1.f)
-                                                                           : make_float2(m_ref, l_sum);
+            p.part_ml[orow * p.num_splits + record] = poisoned || state == 2 ? make_float2(m_ref, -1.f)
+                                                      : state == 1          ? make_float2(-INFINITY, 0.f)
+                                                      : l_sum != l_sum      ? make_float2(0.f, 1.f)
+                                                                            : make_float2(m_ref, l_sum);
         } else if (live && !direct)
             // (F4: a NaN sum goes on as a NaN row with max 0 and sum 1: the reduce takes a sum that is not > 0 for
             // an empty split, and the max may be infinite)
-            p.part_ml[orow * p.num_splits + split] = poisoned                  ? make_float2(m_ref, -1.f)
+            p.part_ml[orow * p.num_splits + record] = poisoned                 ? make_float2(m_ref, -1.f)
                                                      : F4 && l_sum != l_sum ? make_float2(0.f, 1.f)
                                                                             : make_float2(m_ref, l_sum);
     }

@@ -46,8 +46,8 @@ def test_plan(lib):
     # 16 groups of 4 KV heads: two CTAs for each, and at most 4096 tokens for one
     assert records(desc(), prefix(num_groups=16, max_group_seqs=4, max_prefix_len=8000)) == 2 + 1
     assert records(desc(), prefix(num_groups=16, max_group_seqs=4)) == 8 + 1
-    # short prefixes are not cut below 128 tokens, own parts at 2048
-    assert records(desc(), prefix(max_prefix_len=512, max_suffix_len=4000)) == 4 + 2
+    # short prefixes are not cut below 128 tokens; own parts are cut while SMs are left
+    assert records(desc(), prefix(max_prefix_len=512, max_suffix_len=4000)) == 4 + 1
     # sharing that saves little is left: 4 sequences of 552 tokens, 35 chunks, split as a decode of that length
     small = dict(max_group_seqs=4, max_prefix_len=512, max_suffix_len=40)
     assert records(desc(num_seqs=4), prefix(**small)) == 7
