@@ -491,7 +491,7 @@ size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc 
  * rows of the block table lead to the same pages for them, or to copies (as
  * pa_fork_block_tables leaves them).  Those tokens are read once per group,
  * through the row of its first sequence that is not idle; where that would save
- * too little (about 12 MB of a bf16 cache by the description) every sequence
+ * too little (less than 40 MiB of K and V by the description) every sequence
  * reads them through its own row.
  * prefix_lens[b] is the same throughout a group, and at most seq_lens[b]; a group
  * without a common part has 0, and any length serves, also one that ends inside a
@@ -687,7 +687,7 @@ pa_status pa_rotary_frequencies(const pa_rotary_scaling *scaling, int64_t *freqs
 
 /* One rotary call: num_tokens rows of num_q_heads (and num_kv_heads) heads of
  * head_dim; heads are dense, rows are *_stride elements apart (a multiple of
- * 8), so that q, k and v may be read in place from one projection's rows. */
+ * 8, below 2^31), so that q, k and v may be read in place from one projection's rows. */
 typedef struct {
     int32_t num_tokens;
     int32_t num_q_heads;

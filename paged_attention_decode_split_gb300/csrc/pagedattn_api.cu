@@ -25,7 +25,11 @@ namespace {
 
 constexpr int kMaxChunksPerSplit = 256; // 4096 tokens: bounds the longest CTA for load balance
 constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tokens
-constexpr int64_t kMinShared = 6 << 20;   // elements of K that sharing must save
+// Bytes of K and V that sharing must save, or its two more launches cost more than the reads.  2 to 32 sequences of 512
+// to 8192 common tokens, us shared / read by each sequence: bf16, 28 MB saved 13.9 / 11.5, 48 MB 14.1 / 16.9; e4m3, 28 MB
+// 15.7 / 15.4, 48 MB 19.3 / 18.4 (head_dim 256) and 20.6 / 23.5 (128); fp4, 34 MB 19.2 / 16.3, 54 MB 23.9 / 23.2 (256)
+// and 26.0 / 38.4 (128).
+constexpr double kMinSharedBytes = 40 << 20;
 constexpr int kMaxDevices = 64;
 constexpr int kKernelSlots = 288;
 
@@ -148,12 +152,16 @@ struct SharedPlan {
     int prefix_splits, prefix_chunks, prefix_most;
     int suffix_splits, suffix_chunks, suffix_most;  // likewise of a sequence's own part
     int row_blocks;                    // of the largest group
-    int copies;                        // of its rows, over a bf16 cache: records of a prefix split
+    int copies;                        // of its rows: records of a prefix split
     size_t ws_bytes, off_part_ml;
 };
 
+enum CacheKind { kCacheBf16, kCacheFp8, kCacheFp4 };
+constexpr CacheKind kCacheKinds[] = {kCacheBf16, kCacheFp8, kCacheFp4};
+constexpr double kCacheBytes[] = {4.0, 2.0, 9.0 / 8};  // of K and V per element
+
 // The hints bound nothing: a longer prefix or own part has longer splits.
-pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, SharedPlan *pl) {
+pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, CacheKind kind, SharedPlan *pl) {
     pa_status st = check_desc(d, false);
     if (st != PA_OK) return st;
     if (!x || x->num_groups < 0 || x->max_group_seqs < 0 || x->max_prefix_len < 0 || x->max_suffix_len < 0 ||
@@ -176,9 +184,9 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
     const int np = chunks(x->max_prefix_len), ns = chunks(x->max_suffix_len);
     auto tiles = [](int n, int splits) { return (std::max(1, (n + splits - 1) / splits) + 3) & ~3; };
     // Where sharing saves little, its launch costs more: every sequence reads the prefix for itself then.
-    const int64_t saved = std::max<int64_t>(0, static_cast<int64_t>(d->num_seqs) - x->num_groups) * np * kChunk *
-                          d->num_kv_heads * d->head_dim;
-    const bool direct = x->prefix_splits == 0 && saved < kMinShared;
+    const double saved = kCacheBytes[kind] * std::max(0, d->num_seqs - x->num_groups) * np * kChunk * d->num_kv_heads *
+                         d->head_dim;
+    const bool direct = x->prefix_splits == 0 && saved < kMinSharedBytes;
     // the prefix: whole waves of CTAs, splits of whole 64-token tiles
     const int64_t units = std::max<int64_t>(1, x->num_groups * blocks * d->num_kv_heads);
     int sp = x->prefix_splits;
@@ -215,7 +223,7 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Share
     pl->suffix_splits = std::min(ss, std::max(1, all));
     pl->suffix_chunks = std::max(kMinChunksPerSplit, (own + pl->suffix_splits - 1) / pl->suffix_splits);
     pl->suffix_most = std::max(pl->suffix_chunks, (all + pl->suffix_splits - 1) / pl->suffix_splits);
-    pl->copies = prefix_copies(d->head_dim, static_cast<int>(rows), true);
+    pl->copies = kind == kCacheBf16 ? prefix_copies(d->head_dim, static_cast<int>(rows), true) : 1;
     size_t records =
         static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits * pl->copies + pl->suffix_splits);
     if (pl->prefix_splits + pl->suffix_splits == 1) records = 0;  // (the outputs themselves)
@@ -682,9 +690,13 @@ pa_status pa_paged_attention_verify_fp4(const void *q, const void *k_cache, cons
 }
 
 size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc *prefix) {
-    SharedPlan pl;
-    if (make_shared_plan(desc, prefix, &pl) != PA_OK) return static_cast<size_t>(-1);
-    return pl.ws_bytes;
+    size_t most = 0;
+    for (const CacheKind kind : kCacheKinds) {
+        SharedPlan pl;
+        if (make_shared_plan(desc, prefix, kind, &pl) != PA_OK) return static_cast<size_t>(-1);
+        most = std::max(most, pl.ws_bytes);
+    }
+    return most;
 }
 
 pa_status pa_paged_attention_decode_shared(const void *q, const void *k_cache, const void *v_cache,
@@ -880,7 +892,7 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
                       int32_t *device_status, void *stream, bool fp4) {
     const bool fp8 = k_scale != nullptr && !fp4;
     SharedPlan pl;
-    pa_status st = make_shared_plan(desc, prefix, &pl);
+    pa_status st = make_shared_plan(desc, prefix, fp4 ? kCacheFp4 : fp8 ? kCacheFp8 : kCacheBf16, &pl);
     if (st != PA_OK) return st;
     if (desc->num_seqs == 0) return PA_OK;
     st = check_common_ptrs(q, k_cache, v_cache, block_table, seq_lens, out);
@@ -916,7 +928,7 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     p.block_size = desc->block_size;
     p.chunks_per_split = pl.prefix_most;
     p.prefix_chunks = pl.prefix_chunks;
-    const int prefix_records = pl.prefix_splits * (fp8 || fp4 ? 1 : pl.copies);
+    const int prefix_records = pl.prefix_splits * pl.copies;
     p.num_splits = prefix_records + pl.suffix_splits;
     p.scale_log2 = desc->scale * 1.4426950408889634f;
     p.out_bf16 = desc->out_dtype == PA_OUT_BF16;

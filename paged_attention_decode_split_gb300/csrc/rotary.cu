@@ -244,6 +244,9 @@ pa_status check_rope(const RopeParams &p, int64_t n, int flags, bool cache) {
     const Rows q{p.q, p.q_stride, wq}, k{p.k, p.k_stride, wk}, v{p.v, p.v_stride, wk};
     const Rows qo{p.q_out, p.q_out_stride, wq}, ko{p.k_out, p.k_out_stride, wk};
     if (n > 1 && (p.q_stride < 0 || p.k_stride < 0 || p.v_stride < 0)) return PA_ERR_INVALID_ARG;
+    if (n > 1)  // (so that offsets of rows stay in 64 bits)
+        for (const int64_t stride : {p.q_stride, p.k_stride, p.v_stride, p.q_out_stride, p.k_out_stride})
+            if (stride > INT32_MAX) return PA_ERR_UNSUPPORTED;
     if (!in_place_or_apart(q, qo, n) || !disjoint(k, qo, n) || !disjoint(v, qo, n)) return PA_ERR_INVALID_ARG;
     if (!cache && (!in_place_or_apart(k, ko, n) || !disjoint(q, ko, n) || !disjoint(qo, ko, n)))
         return PA_ERR_INVALID_ARG;

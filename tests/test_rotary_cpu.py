@@ -94,7 +94,8 @@ Q, K, V, QO, KO = (FAKE + 0x100000 * i for i in range(5))
 BAD = [(dict(num_tokens=-1), "arg"), (dict(rotary_dim=144), "arg"), (dict(rotary_dim=0), "arg"), (dict(flags=4), "arg"),
        (dict(factor=float("nan")), "arg"), (dict(num_q_heads=0, num_kv_heads=0), "arg"), (dict(rotary_dim=24), "no"),
        (dict(head_dim=24, rotary_dim=16), "no"), (dict(head_dim=16, rotary_dim=16), "no"), (dict(head_dim=2048), "no"),
-       (dict(q_stride=1028), "arg"), (dict(q_out_stride=1016), "arg"), (dict(k_stride=-256), "arg")]
+       (dict(q_stride=1028), "arg"), (dict(q_out_stride=1016), "arg"), (dict(k_stride=-256), "arg"),
+       (dict(q_stride=1 << 31), "no"), (dict(v_stride=1 << 40, q_out_stride=1 << 61), "no")]
 CODE = {"arg": pa.PA_ERR_INVALID_ARG, "no": pa.PA_ERR_UNSUPPORTED}
 
 
