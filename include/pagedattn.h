@@ -701,8 +701,8 @@ typedef struct {
 } pa_rotary_desc;
 
 /* rotary -- q_out = rotated q, k_out = rotated k.  An output may be its own
- * input (the same pointer and stride); apart from that what is written shares
- * no byte with another argument (PA_ERR_INVALID_ARG).  num_kv_heads may be 0 (k
+ * input (the same pointer and stride); apart from that rows that are written
+ * share no byte with other rows (PA_ERR_INVALID_ARG).  num_kv_heads may be 0 (k
  * and k_out are not used then).
  *   q, q_out     device bf16 [num_tokens, num_q_heads, head_dim]
  *   k, k_out     device bf16 [num_tokens, num_kv_heads, head_dim]

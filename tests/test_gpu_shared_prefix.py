@@ -249,6 +249,67 @@ def test_nan_reaches_what_depends_on_it(kind, splits):
     check(got[good], ref[~bad], tol[~bad])
 
 
+def spoil_value(b, slot, head):
+    """A NaN value of dim 21 (over an fp4 cache of its block of 16 dims, 16 .. 31) of a slot; returns the dims."""
+    if b.kind == "bf16":
+        b.v.view(-1, b.hkv, b.d)[slot, head, 21] = float("nan")
+    elif b.kind == "fp8":
+        b.v.reshape(-1, b.hkv, b.d)[slot, head, 21] = 0x7F
+    else:
+        from tests import fp4_ref
+        _, scales = fp4_ref.byte_places("v", slot % 16, b.d)
+        b.v[slot // b.bs, head, slot % b.bs // 16, scales[1]] = 0x7F
+        return slice(16, 32)
+    return slice(21, 22)
+
+
+@BOTH
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape,out", [(HYBRID, "f32"), (HYBRID, "bf16"), (DENSE, "f32"), (DENSE, "bf16")])
+@pytest.mark.parametrize("n", [3, 12, 30])  # rows of the first group: copies of them share a tile, or a block, or blocks
+def test_nan_values_reach_who_sees_them(n, shape, out, kind, splits):
+    b = Batch(n, [(96, [3 + i for i in range(n)]), (64, [5, 9])], *shape, 16, kind, out)
+    ref, tol = b.reference()
+    g = b.hq // b.hkv
+    bad = np.zeros((b.n, b.hq, b.d), bool)
+    bad[:n, 2 * g:3 * g, spoil_value(b, int(b.slots(0)[70]), 2)] = True      # of the first group's prefix
+    bad[n + 1, :g, spoil_value(b, int(b.slots(n + 1)[66]), 0)] = True        # of the last sequence's own part
+    got = b.run(prefix_splits=splits).cpu()
+    assert torch.isnan(got[torch.from_numpy(bad)]).all()
+    check(got[torch.from_numpy(~bad)], ref[~bad], tol[~bad])
+
+
+@BOTH
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [3, 12])
+def test_slots_past_the_sequences_may_be_nan_at_128(n, out, kind, splits):
+    b = Batch(n, [(100, [1 + 5 * i for i in range(n)]), (48, [0, 5])], *DENSE, 48, kind, out)
+    ref, tol = b.reference()
+    dead = np.ones(b.pages * b.bs, bool)
+    for s in range(b.n):
+        dead[b.slots(s)] = False
+    if kind == "fp4":
+        whole = dead.reshape(b.pages, 1, -1, 16).all(-1)  # chunks without a token in use
+        for c in (b.k, b.v):
+            c[np.broadcast_to(whole, c.shape[:3])] = 0xFF
+    else:
+        for c in (b.k, b.v):
+            if kind == "bf16":
+                c.view(-1, b.hkv, b.d)[torch.from_numpy(dead)] = float("nan")
+            else:
+                c.reshape(-1, b.hkv, b.d)[dead] = 0x7F
+    check(b.run(prefix_splits=splits), ref, tol)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape,out", [((8, 2, 128), "f32"), ((6, 1, 256), "bf16")])
+def test_more_pages_than_a_cta_stages(kind, shape, out):
+    """Prefixes and own parts of more than 512 pages in one split."""
+    b = Batch(5, [(9000, [9001, 3, 1]), (8200, [20] * 7)], *shape, 16, kind, out)
+    check(b.run(desc=b.desc(num_splits=1), shared=b.shared(prefix_splits=1)), *b.reference())
+
+
 # -- calls side by side ----------------------------------------------------------------------------
 
 @BOTH
