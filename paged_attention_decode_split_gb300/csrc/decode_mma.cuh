@@ -296,6 +296,9 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
 
     const int stream = warp / DS, ds = warp % DS;
     const int r = lane >> 2, c = lane & 3;
+    // SH over an e4m3 cache: the reference max is kept 2^7 below the largest score it was raised for, so that P in f16,
+    // at most 2^15, holds weights down to 2^-32 of the largest
+    constexpr float kBelow = SH && F8 ? 7.f : 0.f, kRaise = kLazyLog2 + kBelow;
     float m_run[NT][2], l_run[NT][2];
     float oacc[MTW][NT][4];
     // the second sum: in registers where they hold it, else in local memory with the maxima that it stands for
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) up |= x[nt][q] > m_run[nt][q & 1] + kLazyLog2;
+            for (int q = 0; q < 4; ++q) up |= x[nt][q] > m_run[nt][q & 1] + kRaise;
         if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -581,7 +584,8 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
                     cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 4));
                     cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 8));
                     cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 16));
-                    if (cm > m_run[nt][j] + kLazyLog2) {
+                    if (cm > m_run[nt][j] + kRaise) {
+                        cm -= kBelow;
                         const float alpha = fast_exp2(m_run[nt][j] - cm);  // 0 on the first chunk
                         m_run[nt][j] = cm;
                         l_run[nt][j] *= alpha;

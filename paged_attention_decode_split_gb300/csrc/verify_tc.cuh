@@ -395,9 +395,10 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     constexpr int RB = C::M / COP, KPT = TT / COP;  // rows of a copy; keys of a tile per softmax thread
     static_assert(COP == 1 || (SH && VPK == 1 && !F4), "copies of rows: the common part of a shared prefix");
     constexpr float kLazy = 8.f;  // raise the reference max only when it grows by more than 2^8
-    // fp4: the reference is kept 2^7 below the max, so that P in f16, at most 2^15,
-    // holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
-    constexpr float kBelow = F4 || !RES ? 7.f : 0.f;
+    // fp4 and, behind shared prefixes, e4m3: the reference is kept 2^7 below the max,
+    // so that P in f16, at most 2^15, holds weights down to 2^-32 of the largest (f16
+    // ends at 2^-25).
+    constexpr float kBelow = F4 || (SH && F8) ? 7.f : 0.f;
     extern __shared__ uint8_t smem_dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
     // K and V tiles have their own rings: a K slot is free again as soon as

@@ -84,8 +84,8 @@ class Batch:
             return c.flatten(0, 1)[torch.from_numpy(slots)].double().numpy()
         return e4m3(c.reshape(-1, self.hkv, self.d)[slots]).astype(np.float64) * self.g[which].astype(np.float64)[:, None]
 
-    def reference(self):
-        """(outputs, tolerance): float64 [n, hq, d]."""
+    def reference(self, f16_end=2.0 ** -24):
+        """(outputs, tolerance): float64 [n, hq, d]; f16_end: of the largest weight, what f16 may lose of any."""
         ref, tol = np.zeros((self.n, self.hq, self.d)), np.zeros((self.n, self.hq, self.d))
         grp, q = self.hq // self.hkv, self.q.double().numpy()
         for b in range(self.n):
@@ -108,7 +108,7 @@ class Batch:
                 weight = 2.0 ** -17 if self.kind == "bf16" else 2.0 ** -11 if self.kind == "fp4" and self.out == "bf16" else 2.0 ** -21
                 rel = 2.02 * e + 2 * (weight + 2.0 ** -22) + (len(s) / 16 + 64) * 2.0 ** -23
                 # f16 ends at 2^-25: weights relative to a reference that gives the largest 1 or more
-                lost = np.minimum(w, 2.0 ** -24) / total @ np.abs(v[:, h]) if self.kind != "bf16" else 0.0
+                lost = np.minimum(w, f16_end) / total @ np.abs(v[:, h]) if self.kind != "bf16" else 0.0
                 ref[b, hs], tol[b, hs] = o, rel[:, None] * mag + lost + 1e-30
         return ref, tol + (np.abs(ref) * 2.0 ** -8 if self.out == "bf16" else 0.0)
 

@@ -139,6 +139,25 @@ def test_rising_scores(rows):
             check(b.run(prefix_splits=splits), *ref)
 
 
+@BOTH
+@pytest.mark.parametrize("shape,out", [(HYBRID, "f32"), (HYBRID, "bf16"), (DENSE, "f32"), (DENSE, "bf16"), (WIDE, "f32"), (WIDE, "bf16")])
+def test_small_weights_beside_small_values(shape, out, splits):
+    """e4m3: keys at 2^-20 of the first one's weight carry the output, as the first one's values are 2^-18 of theirs.
+    The reference is 2^7 or more below the largest score, and f16 ends half a step below 2^-24: 2^-32 of a weight."""
+    b = Batch(6, [(160, [3, 40, 100]), (320, [5] * 9)], *shape, 16, "fp8", out)
+    g = b.hq // b.hkv
+    b.k.reshape(-1, b.hkv, b.d)[..., 0] = 0
+    b.v[...] = np.random.default_rng(1).integers(0x70, 0x7F, b.v.shape)  # 128 to 448
+    b.q[...] = 0
+    for h in range(b.hkv):
+        b.q[:, h * g:(h + 1) * g, 0] = 20 * np.log(2) / (16 * float(b.g[0][h]) * b.scale)
+    for s, at in ((0, 0), (1, 170), (3, 0), (4, 322)):  # of both prefixes and of two own parts
+        b.k.reshape(-1, b.hkv, b.d)[b.slots(s)[at], :, 0] = 0x58  # 16
+        b.v.reshape(-1, b.hkv, b.d)[b.slots(s)[at]] = 0x01        # 2^-9
+    ref, tol = b.reference(f16_end=2.0 ** -32)
+    check(b.run(prefix_splits=splits), ref, tol)
+
+
 # -- lengths, groups and pages that make no sense --------------------------------------------------
 
 def zero_rows(b, bad):
