@@ -70,5 +70,8 @@ cudaError_t ensure_smem_limit(const void *fn, int bytes, int slot);
 // Whether `fn` is launched with at least `regs` registers per thread, asked
 // once per device (cudaErrorInvalidConfiguration if not).
 cudaError_t ensure_launch_regs(const void *fn, int regs, int slot);
+// Allows `fn` clusters of more than 8 CTAs, once per device
+// (cudaErrorInvalidConfiguration if the device has no room for one).
+cudaError_t ensure_wide_cluster(const void *fn, int ctas, int threads, int smem, int slot);
 
 }  // namespace pa

@@ -31,7 +31,7 @@ constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tok
 // and 26.0 / 38.4 (128).
 constexpr double kMinSharedBytes = 40 << 20;
 constexpr int kMaxDevices = 64;
-constexpr int kKernelSlots = 288;
+constexpr int kKernelSlots = 296;
 
 thread_local pa_plan_info g_last_plan;
 thread_local bool g_have_plan = false;
@@ -415,6 +415,34 @@ cudaError_t ensure_launch_regs(const void *fn, int regs, int slot) {
         cudaFuncAttributes attr;
         const cudaError_t err = cudaFuncGetAttributes(&attr, fn);
         return err != cudaSuccess ? err : attr.numRegs >= regs ? cudaSuccess : cudaErrorInvalidConfiguration;
+    });
+}
+
+cudaError_t ensure_wide_cluster(const void *fn, int ctas, int threads, int smem, int slot) {
+    static DeviceOnce<kMaxDevices, kKernelSlots> once;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return once.run(dev, slot, [&] {
+        cudaError_t err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();  // (the caller goes on without)
+            return err;
+        }
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        err = cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg);
+        if (err != cudaSuccess) (void)cudaGetLastError();
+        return err != cudaSuccess ? err : clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
     });
 }
 

@@ -13,17 +13,19 @@
 // a replayed call gives the same again.
 //
 // What bounds them is the chain of launches and of dependent loads.  A release
-// and a compaction are one cluster of 8 CTAs (and the rewriting of the tables): the
-// pages are spread over the CTAs' shared memories, which hold 409,600, an entry of a
-// block table adds to its page's counter there, and the sums pass through
-// distributed shared memory.  Where 8 SMs would take long to walk the pages and
+// and a compaction are one cluster of CTAs (and the rewriting of the tables): the
+// pages are spread over the CTAs' shared memories, those of 8 hold 409,600, an entry
+// of a block table adds to its page's counter there, and the sums pass through
+// distributed shared memory.  Where a cluster would take long to walk the pages and
 // the tables, a release goes through kernels that fill the GPU: one copies the
 // counts, the next adds to them, a cluster scans.  A fork has nothing to scan; it
-// takes two such kernels at any size.
+// takes two such kernels at any size.  Scans of many pages take 16 CTAs.
 // (us per call, requests x pages per request of a pool of so many pages, release
-// by one cluster / by three kernels: 64 x 40, 1.2K: 6.3 / 8.0; 256 x 100, 15K: 7.4 /
-// 9.0; 256 x 300, 60K: 12 / 11.  Fork 4.8 us for 8 requests, 10.4 for 1000 x 600;
-// as one cluster it took 6.9 and 12.)
+// by one cluster / by three kernels: 64 x 40, 1.2K: 4.9 / 8.0; 256 x 100, 15K: 6.4 /
+// 9.0; 256 x 300, 60K: 12 / 9.9.  Compaction by 8 / 16 CTAs: 15K: 11.0 / 10.9; 60K:
+// 18.9 / 14.2; 286K: 33.5 / 26.0.  Release by three kernels, 60K: 9.9 / 10.4; 90K: 13.7
+// / 10.5; 286K: 28.9 / 21.1.  Fork 4.6 us for 8 requests, 10.0 for 1000 x 600; as one
+// cluster it took 6.9 and 12.)
 #include <algorithm>
 
 #include "pa_internal.h"
@@ -35,6 +37,8 @@ namespace {
 constexpr int kShareThreads = 256;
 constexpr int kShareCtas = 304;       // two per SM
 constexpr int kScanCtas = 8;          // CTAs of the cluster that scans the pages
+constexpr int kScanWide = 16;         // the same, of many pages, where the device has room for it
+constexpr int64_t kWideCompact = 16 * 1024, kWideRelease = 64 * 1024;  // from more pages on
 constexpr int kScanThreads = 1024;
 constexpr int kScanItems = 8;         // pages per thread and step
 constexpr int kClusterPages = 50 * 1024;         // counters of a CTA of the cluster (200 KiB)
@@ -254,14 +258,20 @@ __global__ void __launch_bounds__(kShareThreads) pa_release_counts_kernel(const 
 
 // ---- a cluster's sums ---------------------------------------------------------
 
+// The kernels that scan are one cluster of CTAS CTAs.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Every CTA of the cluster gives v (the same in all of its threads) and gets
-// all of them in box[0 .. kScanCtas); a box is used once.
+// all of them in box[0 .. CTAS); a box is used once.  A CTA may leave after
+// its last one: what others write into its shared memory is there by then.
+template <int CTAS>
 __device__ __forceinline__ void cluster_share(int v, int *box) {
-    if (threadIdx.x < kScanCtas) {
+    if (threadIdx.x < CTAS) {
         uint32_t there;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_addr(box + blockIdx.x)), "r"(threadIdx.x));
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(v) : "memory");
@@ -273,9 +283,10 @@ __device__ __forceinline__ void cluster_share(int v, int *box) {
 struct Span {
     int64_t lo, hi;
 };
+template <int CTAS>
 __device__ __forceinline__ Span span_of(int64_t pages) {
     const int64_t step = kScanThreads * kScanItems;
-    const int64_t per = (pages + step * kScanCtas - 1) / (step * kScanCtas) * step;
+    const int64_t per = (pages + step * CTAS - 1) / (step * CTAS) * step;
     const int64_t lo = min(pages, per * blockIdx.x);
     return {lo, min(pages, lo + per)};
 }
@@ -286,8 +297,9 @@ struct Counters {
     uint32_t base;   // shared-memory address in this CTA
     int lo, n, per;  // the CTA's pages [lo, lo + n)
 };
+template <int CTAS>
 __device__ __forceinline__ Counters counters_of(const ShareParams &p, int32_t *smem) {
-    const int per = ((int)((p.num_pages + kScanCtas - 1) / kScanCtas) + 3) & ~3;
+    const int per = ((int)((p.num_pages + CTAS - 1) / CTAS) + 3) & ~3;
     const int lo = (int)min(p.num_pages, (int64_t)per * blockIdx.x);
     return {smem_addr(smem), lo, (int)min((int64_t)per, p.num_pages - lo), per};
 }
@@ -313,29 +325,31 @@ __device__ __forceinline__ Share share_of(int n) {
 
 // Sum of v over the CTAs before this one (and the threads before this one, which
 // block_before gave), and over all: `box` is used once.
+template <int CTAS>
 __device__ __forceinline__ int cluster_before(int total, int *box, int &all) {
-    cluster_share(total, box);
+    cluster_share<CTAS>(total, box);
     int before = 0;
     all = 0;
-    for (int c = 0; c < kScanCtas; ++c) {
+    for (int c = 0; c < CTAS; ++c) {
         if (c < (int)blockIdx.x) before += box[c];
         all += box[c];
     }
     return before;
 }
 
+template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const ShareParams p) {
     pdl_wait_primary();  // (no early launch of dependents, as above)
     extern __shared__ int32_t counts[];
     __shared__ int tmp[32];
-    __shared__ int box[kScanCtas];
-    const Counters c = counters_of(p, counts);
+    __shared__ int box[CTAS];
+    const Counters c = counters_of<CTAS>(p, counts);
     for_each((int)threadIdx.x, c.n, kScanThreads, [&](int i) { return p.shares[c.lo + i]; },
              [&](int i, int v) { counts[i] = v; });
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();
     // a warp per request
-    for (int b = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); b < p.B; b += kScanCtas * (kScanThreads / 32)) {
+    for (int b = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5); b < p.B; b += CTAS * (kScanThreads / 32)) {
         const int len = p.lens[b], done = p.count[b];
         const bool ok = len >= 0 && len <= room_of(p);
         if ((threadIdx.x & 31) == 0) {
@@ -358,7 +372,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const 
     int total;
     const int in_cta = block_before(mine, tmp, total);
     int all;
-    int64_t to = (int64_t)F + cluster_before(total, box, all) + in_cta;
+    int64_t to = (int64_t)F + cluster_before<CTAS>(total, box, all) + in_cta;
     if (mine > 0) {
         for (int i = s.lo; i < s.hi; ++i) {
             if (counts[i] >= 0) continue;
@@ -370,23 +384,23 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_cluster_kernel(const 
     }
     for (int i = threadIdx.x; i < c.n; i += kScanThreads) p.shares_out[c.lo + i] = max(counts[i], 0);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = (int)min((int64_t)F + all, p.num_pages);
-    cluster_sync();  // (no CTA leaves while another may still write into its shared memory)
 }
 
-// (grid = one cluster of kScanCtas CTAs)
+// (grid = one cluster)
+template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const ShareParams p) {
     pdl_wait_primary();  // (no early launch of dependents, as above)
     __shared__ int tmp[32];
-    __shared__ int box[kScanCtas];
-    const Span s = span_of(p.num_pages);
+    __shared__ int box[CTAS];
+    const Span s = span_of<CTAS>(p.num_pages);
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
     int mine = 0;
     for_each(s.lo + threadIdx.x, s.hi, (int64_t)kScanThreads, [&](int64_t i) { return __ldcg(p.shares_out + i); },
              [&](int64_t, int v) { mine += v < 0; });
-    cluster_share(block_sum(mine, tmp), box);
+    cluster_share<CTAS>(block_sum(mine, tmp), box);
     int64_t at = F, all = F;
-    for (int c = 0; c < kScanCtas; ++c) {
+    for (int c = 0; c < CTAS; ++c) {
         if (c < (int)blockIdx.x) at += box[c];
         all += box[c];
     }
@@ -412,7 +426,6 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const Sha
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) p.num_free_out[0] = (int)min(all, p.num_pages);
-    cluster_sync();  // (no CTA leaves while another may still write into its shared memory)
 }
 
 // ---- compaction ---------------------------------------------------------------
@@ -426,27 +439,24 @@ __global__ void __launch_bounds__(kScanThreads) pa_release_pool_kernel(const Sha
 // by the free pages filled below p and lost the moved ones, which places every
 // free page on the new list without a second scan.
 // The marks and the ranks stand in the cluster's shared memory; a thread scans a
-// stretch of pages of its own.  40,000 pages with 4096 moves: 18 us, half of it the
+// stretch of pages of its own.  40,000 pages with 4096 moves: 12 us, half of it the
 // barriers of the cluster and the waits for the counters of other CTAs; the copies
-// that the call lists take twice as long.
+// that the call lists take three times as long.
+template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const ShareParams p) {
     pdl_launch_dependents();  // (the kernel behind this one rewrites the tables and is the call's last)
     pdl_wait_primary();
     extern __shared__ int32_t used[];
     __shared__ int tmp[32];
-    __shared__ int box[3][kScanCtas];
+    __shared__ int box[3][CTAS];
     __shared__ int top;
     const int P = (int)p.num_pages;
-    const Counters c = counters_of(p, used);
+    const Counters c = counters_of<CTAS>(p, used);
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
     const int tid = blockIdx.x * kScanThreads + threadIdx.x;
-    constexpr int stride = kScanCtas * kScanThreads;
+    constexpr int stride = CTAS * kScanThreads;
     if (threadIdx.x == 0) top = 0;
-    for_each((int)threadIdx.x, c.n, kScanThreads, [&](int i) { return p.shares[c.lo + i]; }, [&](int i, int v) {
-        used[i] = 1;
-        __stcg(p.page_map + c.lo + i, c.lo + i);
-        __stcg(p.shares_out + c.lo + i, v);
-    });
+    for (int i = threadIdx.x; i < c.n; i += kScanThreads) used[i] = 1;
     cluster_sync();
     for_each(tid, F, stride, [&](int i) { return p.free_pages[i]; }, [&](int, int page) {
         if (valid_page(p, page))
@@ -454,18 +464,23 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
         else
             set_status(p.status, PA_DEV_BAD_PAGE);
     });
-    cluster_sync();
+    cluster_arrive();
+    for_each((int)threadIdx.x, c.n, kScanThreads, [&](int i) { return p.shares[c.lo + i]; }, [&](int i, int v) {
+        __stcg(p.page_map + c.lo + i, c.lo + i);
+        __stcg(p.shares_out + c.lo + i, v);
+    });
+    cluster_wait();
     const Share s = share_of(c.n);
     int mine = 0;
     for (int i = s.lo; i < s.hi; ++i) mine += used[i];
     int total;
     const int in_cta = block_before(mine, tmp, total);
     int n;  // (pages are fewer than 2^19 here)
-    int bef = cluster_before(total, box[0], n) + in_cta;
+    int bef = cluster_before<CTAS>(total, box[0], n) + in_cta;
     mine = 0;
     for (int i = max(s.lo, n - c.lo); i < s.hi; ++i) mine += used[i];
     int m;
-    cluster_before(block_sum(mine, tmp), box[1], m);
+    cluster_before<CTAS>(block_sum(mine, tmp), box[1], m);
     m = min(m, p.moves);
     const int n_free = P - n;
     int highest = 0;
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
     highest = __reduce_max_sync(0xffffffffu, highest);
     if ((threadIdx.x & 31) == 0) atomicMax(&top, highest);
     __syncthreads();
-    cluster_share(top, box[2]);  // (also: every move is listed)
+    cluster_share<CTAS>(top, box[2]);  // (also: every move is listed)
     for (int64_t i = tid; i < m; i += stride) {
         const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i), held = p.shares[from];
         __stcg(p.page_map + from, to);
@@ -496,24 +511,24 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_cluster_kernel(const 
     }
     if (tid == 0) {
         int e = 0;
-        for (int k = 0; k < kScanCtas; ++k) e = max(e, box[2][k]);
+        for (int k = 0; k < CTAS; ++k) e = max(e, box[2][k]);
         p.extent[0] = e;
         p.num_free_out[0] = (int)n_free;
     }
-    cluster_sync();
 }
 
 // The same for more pages than the cluster's shared memory holds.
+template <int CTAS>
 __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const ShareParams p) {
     pdl_launch_dependents();  // (the kernel behind this one rewrites the tables and is the call's last)
     pdl_wait_primary();
     __shared__ int tmp[32];
-    __shared__ int box[3][kScanCtas];
+    __shared__ int box[3][CTAS];
     __shared__ int top;
     const int64_t P = p.num_pages;
-    const Span s = span_of(P);
+    const Span s = span_of<CTAS>(P);
     const int F = pool_of(p, blockIdx.x == 0 && threadIdx.x == 0);
-    const int64_t tid = (int64_t)blockIdx.x * kScanThreads + threadIdx.x, stride = kScanCtas * kScanThreads;
+    const int64_t tid = (int64_t)blockIdx.x * kScanThreads + threadIdx.x, stride = CTAS * kScanThreads;
     if (threadIdx.x == 0) top = 0;
     // page_map holds the marks until the pages are placed: 1 = in use
     for (int64_t i = s.lo + threadIdx.x; i < s.hi; i += kScanThreads) __stcg(p.page_map + i, 1);
@@ -529,17 +544,17 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
     int mine = 0;
     auto mark = [&](int64_t i) { return __ldcg(p.page_map + i); };
     for_each(s.lo + threadIdx.x, s.hi, (int64_t)kScanThreads, mark, [&](int64_t, int v) { mine += v; });
-    cluster_share(block_sum(mine, tmp), box[0]);
+    cluster_share<CTAS>(block_sum(mine, tmp), box[0]);
     int64_t before = 0, n = 0;
-    for (int c = 0; c < kScanCtas; ++c) {
+    for (int c = 0; c < CTAS; ++c) {
         if (c < (int)blockIdx.x) before += box[0][c];
         n += box[0][c];
     }
     mine = 0;
     for_each(max(s.lo, n) + threadIdx.x, s.hi, (int64_t)kScanThreads, mark, [&](int64_t, int v) { mine += v; });
-    cluster_share(block_sum(mine, tmp), box[1]);
+    cluster_share<CTAS>(block_sum(mine, tmp), box[1]);
     int64_t m = 0;
-    for (int c = 0; c < kScanCtas; ++c) m += box[1][c];
+    for (int c = 0; c < CTAS; ++c) m += box[1][c];
     m = min(m, (int64_t)p.moves);
     const int64_t n_free = P - n;
     int highest = 0;
@@ -577,7 +592,7 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
     highest = __reduce_max_sync(0xffffffffu, highest);
     if ((threadIdx.x & 31) == 0) atomicMax(&top, highest);
     __syncthreads();
-    cluster_share(top, box[2]);  // (also: every move is listed)
+    cluster_share<CTAS>(top, box[2]);  // (also: every move is listed)
     for (int64_t i = tid; i < m; i += stride) {
         const int from = __ldcg(p.src + i), to = __ldcg(p.dst + i);
         __stcg(p.page_map + from, to);
@@ -586,11 +601,10 @@ __global__ void __launch_bounds__(kScanThreads) pa_compact_pool_kernel(const Sha
     }
     if (tid == 0) {
         int e = 0;
-        for (int c = 0; c < kScanCtas; ++c) e = max(e, box[2][c]);
+        for (int c = 0; c < CTAS; ++c) e = max(e, box[2][c]);
         p.extent[0] = e;
         p.num_free_out[0] = (int)n_free;
     }
-    cluster_sync();
 }
 
 __global__ void __launch_bounds__(kShareThreads) pa_compact_tables_kernel(const ShareParams p) {
@@ -731,15 +745,28 @@ int share_ctas(const ShareParams &p) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(kShareCtas, std::max<int64_t>(pages, p.B)));
 }
 
-// Whether a release's pages and tables suit one cluster; a cluster's launch, with
-// the counters of its share of the pages in every CTA.
+// Whether a release's pages and tables suit one cluster.
 bool suits_cluster(const ShareParams &p) {
     return p.num_pages <= kClusterMost && (int64_t)p.B * p.width <= kClusterMost;
 }
-pa_status launch_cluster(void (*kern)(ShareParams), const ShareParams &p, int slot, void *stream) {
-    const size_t smem = 4 * ((((size_t)p.num_pages + kScanCtas - 1) / kScanCtas + 3) & ~size_t(3));
-    if (ensure_smem_limit(reinterpret_cast<const void *>(kern), kClusterPages * 4, slot) != cudaSuccess) return PA_ERR_CUDA;
-    return launch_on(kern, kScanCtas, kScanThreads, true, smem, stream, p) ? PA_OK : PA_ERR_CUDA;
+
+// Launches a kernel that is one cluster, of kScanCtas CTAs or, for more than
+// wide_from pages, of kScanWide; `counters`: it keeps those of its share of the
+// pages in every CTA's shared memory.  Clusters of more than 8 CTAs are not
+// portable: such a one is taken where the device says that it has room for it.
+template <typename Kernel>
+pa_status launch_cluster(Kernel few, Kernel many, int64_t wide_from, const ShareParams &p, bool counters, int slot,
+                         void *stream) {
+    const void *fn = reinterpret_cast<const void *>(many);
+    const int most = counters ? kClusterPages * 4 : 0;
+    const bool wide = many != nullptr && p.num_pages > wide_from &&
+                      (!counters || ensure_smem_limit(fn, most, slot) == cudaSuccess) &&
+                      ensure_wide_cluster(fn, kScanWide, kScanThreads, most, slot) == cudaSuccess;
+    if (!wide && counters && ensure_smem_limit(reinterpret_cast<const void *>(few), most, slot + 1) != cudaSuccess)
+        return PA_ERR_CUDA;
+    const int ctas = wide ? kScanWide : kScanCtas;
+    const size_t smem = counters ? 4 * ((((size_t)p.num_pages + ctas - 1) / ctas + 3) & ~size_t(3)) : 0;
+    return launch_on(wide ? many : few, ctas, kScanThreads, true, smem, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -830,11 +857,11 @@ pa_status pa_release_shared_block_tables(const int32_t *seq_lens, const int32_t 
                            {share_counts_out, 4 * num_pages, true, true},
                            {num_free_out, 4, true, true}});
     if (st != PA_OK) return st;
-    if (suits_cluster(p)) return launch_cluster(pa_release_cluster_kernel, p, 281, stream);
+    if (suits_cluster(p)) return launch_cluster<void (*)(ShareParams)>(pa_release_cluster_kernel<kScanCtas>, nullptr, 0, p, true, 288, stream);
     if (!launch_on(pa_release_lens_kernel, share_ctas(p), kShareThreads, false, 0, stream, p)) return PA_ERR_CUDA;
     const int count_ctas = std::max(1, std::min(p.B, 4 * kShareCtas));
     if (!launch_on(pa_release_counts_kernel, count_ctas, kShareThreads, false, 0, stream, p)) return PA_ERR_CUDA;
-    return launch_on(pa_release_pool_kernel, kScanCtas, kScanThreads, true, 0, stream, p) ? PA_OK : PA_ERR_CUDA;
+    return launch_cluster(pa_release_pool_kernel<kScanCtas>, pa_release_pool_kernel<kScanWide>, kWideRelease, p, false, 290, stream);
 }
 
 pa_status pa_compact_block_tables(const int32_t *seq_lens, int32_t *block_table, const int32_t *free_pages,
@@ -878,12 +905,12 @@ pa_status pa_compact_block_tables(const int32_t *seq_lens, int32_t *block_table,
                             {copy_dst, moved, true, true},
                             {extent, 4, true, true}});
     if (st != PA_OK) return st;
-    if (p.num_pages <= (int64_t)kScanCtas * kClusterPages) {
-        st = launch_cluster(pa_compact_cluster_kernel, p, 282, stream);
-        if (st != PA_OK) return st;
-    } else if (!launch_on(pa_compact_pool_kernel, kScanCtas, kScanThreads, true, 0, stream, p)) {
-        return PA_ERR_CUDA;
-    }
+    st = p.num_pages <= (int64_t)kScanCtas * kClusterPages
+             ? launch_cluster(pa_compact_cluster_kernel<kScanCtas>, pa_compact_cluster_kernel<kScanWide>, kWideCompact, p, true,
+                              292, stream)
+             : launch_cluster(pa_compact_pool_kernel<kScanCtas>, pa_compact_pool_kernel<kScanWide>, kWideCompact, p, false, 294,
+                              stream);
+    if (st != PA_OK) return st;
     const int ctas = std::max(1, std::min(p.B, 4 * kShareCtas));
     return launch_on(pa_compact_tables_kernel, ctas, kShareThreads, false, 0, stream, p) ? PA_OK : PA_ERR_CUDA;
 }
