@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     // most 2^15, holds weights down to 2^-32 of the largest (f16 ends at 2^-25).
     constexpr float kBelow = 7.f, kRaise = kLazyLog2 + kBelow;
 
-    const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    const int split = blockIdx.x, kvh = blockIdx.y;
+    int b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = fp.group, hq0 = kvh * G, hkv = gridDim.y;
     [[maybe_unused]] const bool last_cta = split == (int)gridDim.x - 1 && kvh == hkv - 1 && b == (int)gridDim.z - 1;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     // early_kv lets the block table, seq_lens and the chunks wholly before the
     // new row go first.
     if (SH ? p.prefix_splits == 0 : !p.early_kv) pdl_wait_primary();
+    if constexpr (SH) b = sequence_of(p, b);
 
     // Q^T as B fragments, in f16: n-tile nt, k-step ks -> dims 16 ks + 4c (+1)
     // and 16 ks + 4c + 2 (+3) of head 8 nt + r; warp nt lays its tile out.  Its

@@ -217,7 +217,8 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
     float *merge_w = reinterpret_cast<float *>(smem + C::OFF_W);
     int32_t *page_tab = reinterpret_cast<int32_t *>(smem + C::OFF_PT);
 
-    const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    const int split = blockIdx.x, kvh = blockIdx.y;
+    int b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hq0 = kvh * G;
     [[maybe_unused]] const bool last_cta = split == (int)gridDim.x - 1 && kvh == (int)gridDim.y - 1 && b == (int)gridDim.z - 1;
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
         prefetch_tensormap(&tm_v);
     }
     if (SH ? p.prefix_splits == 0 : !p.early_kv) pdl_wait_primary();
+    if constexpr (SH) b = sequence_of(p, b);
 
     int L = p.seq_lens[b];
     const int record = SH ? p.prefix_splits + split : split;  // of the row's num_splits

@@ -191,17 +191,25 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Cache
     const int64_t units = std::max<int64_t>(1, x->num_groups * blocks * d->num_kv_heads);
     int sp = x->prefix_splits;
     if (sp == 0) {
-        // One group's CTAs are all as long as each other and would hold every SM to the end while the own parts wait:
-        // they get the SMs in proportion to the work, two thirds at least (64 sequences behind 32K: 95 us with 12
-        // splits, 88 with 8).  The work in 0.06 us of an SM: a chunk of a prefix 5, of an own part, half as long as
-        // the longest on average, 6, and 5 us for its CTA.
-        int64_t share = sms;
-        if (x->num_groups == 1) {
-            const int64_t common = 5 * units * np, rest = static_cast<int64_t>(d->num_seqs) * d->num_kv_heads * (3 * ns + 83);
-            share = std::max<int64_t>(sms * 2 / 3, common + rest > 0 ? sms * common / (common + rest) : sms);
-        }
-        sp = static_cast<int>(std::max<int64_t>(1, share / units));
-        sp = std::max(sp, (np + kMaxChunksPerSplit - 1) / kMaxChunksPerSplit);  // (the longest CTA, as in decode)
+        // A prefix's CTAs are as long as each other and hold their SMs to the end, the own parts take the others and
+        // then theirs: best when both end together.  With r = work of the prefixes / work of the own parts (each as
+        // long as the longest, and 8 chunks for its CTA), (r + 0.45) / (r + 1.05) of the SMs, more where two prefix
+        // CTAs share an SM: fitted to the best of ten numbers of splits in 86 batches (5 to 81 sequences, 1 to 3
+        // groups, 3K to 39K common tokens, the three caches), r = 0.1 .. 14, best shares 0.45 .. 1.2; the rule's
+        // splits cost 3 % more than the best ones on average.  (64 sequences behind 32K: 86 us with 8 splits, 79 with
+        // 9, 85 with 10, 99 with 12.)  The prefixes of several groups are taken for shorter than the longest, and their blocks of
+        // rows for no more than all the rows fill.
+        const double groups = std::max(1, x->num_groups), seqs = std::max(1.0, 1.0 * d->num_seqs * d->num_kv_heads);
+        const double held = d->num_kv_heads * std::min(groups * blocks, groups + d->num_seqs * group / 128.0);
+        const double two = kind == kCacheBf16 && d->head_dim == 128 &&
+                                   (d->out_dtype != PA_OUT_BF16 || !verify_wide_score_tiles(128, static_cast<int>(rows)))
+                               ? 1.6 : 1.0;
+        const double average = 0.6 + 0.4 / groups, r = average * held * np / (seqs * (ns + 8));
+        const double share = (r + 0.45) / (r / two + 1.05) * sms / (average * held);
+        const double most = (two > 1.0 ? 1.3 : 1.0) * sms / ((0.65 + 0.35 / groups) * held);  // (a second wave takes as long)
+        sp = std::max(1, static_cast<int>(std::min(share + 0.5, most)));
+        // more units than half of the SMs: waves, whose last one is as long as the longest CTA
+        if (2 * units > sms) sp = std::max(sp, (np + kMaxChunksPerSplit - 1) / kMaxChunksPerSplit);
         sp = std::min(sp, std::max(1, np / kMinPrefixChunks));
         const int per = tiles(np, sp);
         sp = std::max(1, (np + per - 1) / per);
@@ -999,6 +1007,9 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     d.max_members = p.max_members;
     d.prefix_splits = prefix_records;
     d.suffix_splits = pl.suffix_splits;
+    // (calls without a prefix kernel whose CTAs all start at once have no use for an order)
+    d.by_length = desc->num_seqs <= kOrderSeqs &&
+                  (pl.prefix_splits > 0 || pl.suffix_splits * desc->num_kv_heads * desc->num_seqs > pl.num_sms);
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 pgrid(pl.prefix_splits, desc->num_kv_heads * pl.row_blocks, prefix->num_groups);

@@ -13,19 +13,19 @@ int prefix_copies(int head_dim, int rows, bool bf16_cache) {
 }
 
 // rows: what the largest group may have, sequences x heads of the group.  The
-// layouts are the verify's (verify_launch.cu), but for one block of rows at
-// head_dim 128: one S/P buffer, 256 tensor-memory columns and half the rings, so
+// layouts are the verify's (verify_launch.cu) with 64-key score tiles at head_dim
+// 256, also for several blocks of rows (64 sequences behind 32K: 79 us for the call, 83
+// with 128-key tiles, whose one K slot waits for its copy), and but for one block of
+// rows at head_dim 128: one S/P buffer, 256 tensor-memory columns and half the rings, so
 // that two CTAs share an SM and one's set-up and epilogue pass behind the other's
 // tiles (the groups above: 17 us less for the whole call).
 cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const CUtensorMap &tv,
                           const CUtensorMap &tk64, const CUtensorMap &tv64, const CUtensorMap &tk128,
                           const VerifyParams &p, dim3 grid, cudaStream_t stream) {
     if (!p.out_bf16) return launch_prefix_f32(head_dim, rows, tk, tv, tk64, tv64, p, grid, stream);
-    const bool wide = verify_wide_score_tiles(head_dim, rows);
-    if (head_dim == 256)
-        return wide ? launch_verify_tc<256, 1, 3, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 224)
-                    : launch_verify_tc<256, 4, 3, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 225);
+    if (head_dim == 256) return launch_verify_tc<256, 4, 3, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 225);
     if (head_dim == 128) {
+        const bool wide = verify_wide_score_tiles(head_dim, rows);
         const int copies = prefix_copies(head_dim, rows, true);
         return wide          ? launch_verify_tc<128, 3, 6, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 226)
                : copies == 4 ? launch_verify_tc<128, 3, 3, 0, 1, 64, true, false, 2, 4>(tk, tv, tk64, tv64, p, grid, stream, 280)

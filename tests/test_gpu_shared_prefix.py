@@ -69,6 +69,21 @@ def test_heads_per_kv_head(g, d, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [31, 32, 33, 256, 257])
+@BOTH
+def test_many_sequences_of_all_lengths(n, kind, splits):
+    """Own parts of many lengths, equal ones and none, which are taken in an order of their own (up to 256)."""
+    own = [(i * 37) % 150 if i % 5 else (None if i % 3 else 0) for i in range(n - 8)]
+    b = Batch(n, [(48, own), (160, [1, 149, None, 149, 0, 149, 2, 149])], 4, 2, 128, 16, kind, "bf16")
+    t, status = b.tensors(), status0()
+    check(b.run(t, status=status, prefix_splits=splits), *b.reference())
+    assert int(status) == 0
+    t["lens"][3], t["lens"][n - 1] = -1, 2 ** 31 - 1
+    check(b.run(t, status=status, prefix_splits=splits), *zero_rows(b, {3, n - 1}))
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("prefix_splits,splits", [(1, 1), (2, 1), (1, 5), (7, 3), (40, 40), (300, 2)])
 def test_forced_splits(prefix_splits, splits, kind):
     b = Batch(7, [(700, [1, 90, None, 333]), (320, [5, 0])], *HYBRID, 64, kind)

@@ -39,13 +39,14 @@ def records(d, x):
 
 
 def test_plan(lib):
-    # 64 sequences of 6 heads: 3 row blocks of 4 KV heads, two thirds of the SMs; own parts of 1500 tokens in one split
-    assert records(desc(), prefix()) == 8 + 1
-    # prefixes next to which the own parts are short get more of them
-    assert records(desc(), prefix(max_suffix_len=64)) == 10 + 1
-    # 16 groups of 4 KV heads: two CTAs for each, and at most 4096 tokens for one
-    assert records(desc(), prefix(num_groups=16, max_group_seqs=4, max_prefix_len=8000)) == 2 + 1
-    assert records(desc(), prefix(num_groups=16, max_group_seqs=4)) == 8 + 1
+    # 64 sequences of 6 heads: 3 row blocks of 4 KV heads, 0.7 of the SMs; own parts of 1500 tokens in one split
+    assert records(desc(), prefix()) == 9 + 1
+    # prefixes next to which the own parts are short get nearly all, and no second wave
+    assert records(desc(), prefix(max_suffix_len=64)) == 12 + 1
+    # 16 groups of 4 KV heads, their prefixes taken for shorter than the longest on average
+    assert records(desc(), prefix(num_groups=16, max_group_seqs=4)) == 3 + 1
+    # 32: several waves, at most 4096 tokens for a CTA
+    assert records(desc(), prefix(num_groups=32, max_group_seqs=2)) == 8 + 1
     # short prefixes are not cut below 128 tokens; own parts are cut while SMs are left
     assert records(desc(), prefix(max_prefix_len=512, max_suffix_len=4000)) == 4 + 1
     # sharing that saves little is left: 4 sequences of 552 tokens, 35 chunks, split as a decode of that length
