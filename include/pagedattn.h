@@ -469,7 +469,8 @@ pa_status pa_release_block_tables(const int32_t *seq_lens, const int32_t *finish
  *   max_prefix_len,
  *   max_suffix_len  about the longest prefix and the most tokens that a sequence
  *                   has beyond it: they plan the splits and bound nothing; 0 =
- *                   max_seq_len of the description
+ *                   max_seq_len of the description.  Own parts are taken for half as
+ *                   long on average, the prefixes of several groups for shorter too
  *   prefix_splits   0 = automatic; > 0 forces the sharing, and the splits of the
  *                   prefixes (the description's num_splits those of the own parts) */
 typedef struct {

@@ -60,11 +60,11 @@ cudaError_t launch_decode_mma_t(const CUtensorMap &tk, const CUtensorMap &tv, co
 //    12 and 16 heads: 6 x 8, one warp per chunk (registers, as above).
 // The own parts of a decode over shared prefixes (SH) are short, so that a CTA's
 // table, first copies and merge weigh as much as its loop: half the stages each,
-// two CTAs per SM (64 own parts of up to 1500 tokens behind 32K, bf16, D = 256: 88
-// us for the call; with 1 x 3, 1 x 2, 2 x 2 and 4 x 1 streams x stages more).  12
-// and 16 heads need the registers of a whole SM: one CTA; over an e4m3 cache at
-// D = 256 six streams of four stages (33 sequences of 48 heads behind 16.6K: 70 us;
-// 78 with the layout of the plain decode).
+// two CTAs per SM (64 own parts of up to 1500 tokens behind 32K, bf16, D = 256: the
+// call takes longer with 1 x 3, 1 x 2, 2 x 2 and 4 x 1 streams x stages).  12 and 16
+// heads need the registers of a whole SM: one CTA; over an e4m3 cache at D = 256 six
+// streams of four stages (33 sequences of 48 heads behind 16.6K: 8 us less for the
+// call than with the layout of the plain decode).
 template <bool WIN, bool F8, bool SH = false, int PT = 2, bool FAR = false>
 cudaError_t launch_decode_cfg(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                               const DecodeParams &p, dim3 grid, cudaStream_t stream) {

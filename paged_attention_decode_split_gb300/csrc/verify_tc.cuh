@@ -288,13 +288,16 @@ __device__ __forceinline__ void st16(uint32_t taddr, const float (&v)[16]) {
 // V tiles per score tile.  At D = 256 two 128-column S/P buffers and O fill
 // tensor memory, so Q moves to shared memory as the product's A operand (QSM)
 // and the K ring holds one 128-key tile; at D = 128 Q stays in tensor memory.
-// PT = 3: a weight enters P V as three bf16 numbers, in 96 columns of its buffer;
+// PT = 3: a weight enters P V as three bf16 numbers, in 96 columns of its buffer,
+// and S is summed in two halves of the dims (8 sequences x 4 heads behind 38,000,
+// D = 256: error against float64 2.4e-6 with one sum, 1.4e-6 so, in the same time);
 // at D = 256 Q moves to shared memory for their sake too.
 template <int D, int NK, int NV, int NSG = 0, int NSB = 2, int TK = 64, bool F4 = false, int PT = 2>
 struct VerifyTcCfg {
     static constexpr bool F8 = NSG > 0;                // fp8 or fp4 cache: staging ring of NSG slots per tensor
     static constexpr bool QSM = (D == 256 && TK == 128) || (PT == 3 && (D == 256 || NSB == 1));  // Q in shared memory
-    static constexpr int SW = PT == 3 ? 96 : TK;       // columns of an S/P buffer
+    // columns of an S/P buffer (PT = 3: S is summed in two halves of the dims, which halves what the sums lose)
+    static constexpr int SPLIT_QK = PT == 3 ? 2 : 1, SW = SPLIT_QK * TK;
     static constexpr int M = 128;                      // MMA rows (query rows, zero padded)
     static constexpr int TT = 64;                      // tokens per V tile (4 TMA chunks)
     static constexpr int CPT = TT / kChunk;            // chunks per V tile
@@ -609,8 +612,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
     const int n_tiles = (n_my + CPK - 1) / CPK;   // score tiles (K tiles)
     const int n_vtiles = (n_my + CPT - 1) / CPT;  // V tiles (VPK per score tile)
     // tile i starts O anew: what the tiles before it summed goes to the second sum
-    // (three products a step at D = 256, beside Q K^T's own loss: fewer tiles; a copy adds to its sums in every COP-th step)
-    constexpr int kFarTiles = (PT == 3 && D == 256 ? 3 : kVerifyFarTiles) * COP;
+    // (beside Q K^T's own loss: fewer tiles at D = 256 and for three products a step; a copy adds to its sums in every
+    // COP-th step)
+    constexpr int kFarTiles = (PT == 3 || (SH && D == 256) ? 3 : kVerifyFarTiles) * COP;
     auto far_at = [&](int i) { return FAR && i > 0 && i % kFarTiles == 0; };
 
     // The split's block-table entries, staged in shared memory by all threads
@@ -945,7 +949,9 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                             const uint32_t koff = ((kk >> 2) * (TK * 128) + (kk & 3) * 32) >> 4;
                             if constexpr (QSM) {  // Q from shared memory, laid out like K with M rows
                                 const uint32_t qoff = ((kk >> 2) * (C::M * 128) + (kk & 3) * 32) >> 4;
-                                tc::mma_bf16(tm + C::SBUF(j), q_desc + qoff, k_desc + koff, kIdQK, kk > 0 ? 1u : 0u);
+                                constexpr int KH = D / 16 / C::SPLIT_QK;
+                                tc::mma_bf16(tm + C::SBUF(j) + kk / KH * TK, q_desc + qoff, k_desc + koff, kIdQK,
+                                             kk % KH > 0 ? 1u : 0u);
                             } else {
                                 tc::mma_bf16_ta(tm + C::SBUF(j), tm + C::Q_COL + kk * 8, k_desc + koff, kIdQK,
                                                 kk > 0 ? 1u : 0u);
@@ -1321,6 +1327,14 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
                     tc::wait_ld();
 #pragma unroll
                     for (int c = 0; c < KPT; ++c) sv[c] = __uint_as_float(r[c / 16][c % 16]);
+                    if constexpr (C::SPLIT_QK == 2) {
+#pragma unroll
+                        for (int c0 = 0; c0 < KPT / 16; ++c0)
+                            tc::ld16_nowait(lane_base + C::SBUF(j) + TK + copy * KPT + 16 * c0, r[c0]);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int c = 0; c < KPT; ++c) sv[c] += __uint_as_float(r[c / 16][c % 16]);
+                    }
                 }
                 const int t_tile = (c_begin + i * CPT) * kChunk, t0 = t_tile + copy * KPT;
                 float mx = -INFINITY;
