@@ -51,7 +51,7 @@ cudaError_t launch_prefix_f32(int head_dim, int rows, const CUtensorMap &tk, con
                               cudaStream_t stream);
 // Copies of its rows that the common part of groups of at most `rows` rows keeps (VerifyParams::prefix_splits * copies
 // records).
-int prefix_copies(int head_dim, int rows, bool bf16_cache);
+int prefix_copies(int head_dim, int rows);
 cudaError_t launch_prefix_fp8_f32(int head_dim, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &tk64,
                                   const CUtensorMap &tv64, const VerifyParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_prefix_fp4(int head_dim, const VerifyParams &p, dim3 grid, cudaStream_t stream);

@@ -231,7 +231,7 @@ pa_status make_shared_plan(const pa_attn_desc *d, const pa_prefix_desc *x, Cache
     pl->suffix_splits = std::min(ss, std::max(1, all));
     pl->suffix_chunks = std::max(kMinChunksPerSplit, (own + pl->suffix_splits - 1) / pl->suffix_splits);
     pl->suffix_most = std::max(pl->suffix_chunks, (all + pl->suffix_splits - 1) / pl->suffix_splits);
-    pl->copies = kind == kCacheBf16 ? prefix_copies(d->head_dim, static_cast<int>(rows), true) : 1;
+    pl->copies = kind == kCacheBf16 ? prefix_copies(d->head_dim, static_cast<int>(rows)) : 1;
     size_t records =
         static_cast<size_t>(d->num_seqs) * d->num_q_heads * (pl->prefix_splits * pl->copies + pl->suffix_splits);
     if (pl->prefix_splits + pl->suffix_splits == 1) records = 0;  // (the outputs themselves)

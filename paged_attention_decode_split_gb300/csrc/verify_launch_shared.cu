@@ -8,8 +8,8 @@ namespace pa {
 // Row copies pay where a CTA's products wait for its softmax: one S/P buffer (16
 // groups of 8 sequences x 4 heads behind 1K-8K: 143 -> 136 us, fp32 outputs 185 ->
 // 170; at head_dim 256 the products bound a tile, not the softmax).
-int prefix_copies(int head_dim, int rows, bool bf16_cache) {
-    return head_dim != 128 || !bf16_cache ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+int prefix_copies(int head_dim, int rows) {
+    return head_dim != 128 ? 1 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
 }
 
 // rows: what the largest group may have, sequences x heads of the group.  The
@@ -26,7 +26,7 @@ cudaError_t launch_prefix(int head_dim, int rows, const CUtensorMap &tk, const C
     if (head_dim == 256) return launch_verify_tc<256, 4, 3, 0, 2, 64, true>(tk, tv, tk64, tv64, p, grid, stream, 225);
     if (head_dim == 128) {
         const bool wide = verify_wide_score_tiles(head_dim, rows);
-        const int copies = prefix_copies(head_dim, rows, true);
+        const int copies = prefix_copies(head_dim, rows);
         return wide          ? launch_verify_tc<128, 3, 6, 0, 2, 128, true>(tk, tv, tk128, tv64, p, grid, stream, 226)
                : copies == 4 ? launch_verify_tc<128, 3, 3, 0, 1, 64, true, false, 2, 4>(tk, tv, tk64, tv64, p, grid, stream, 280)
                : copies == 2 ? launch_verify_tc<128, 3, 3, 0, 1, 64, true, false, 2, 2>(tk, tv, tk64, tv64, p, grid, stream, 283)

@@ -13,7 +13,7 @@ cudaError_t launch_prefix_f32(int head_dim, int rows, const CUtensorMap &tk, con
     if (head_dim == 256)
         return launch_verify_tc<256, 2, 3, 0, 2, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 236);
     if (head_dim == 128) {
-        const int copies = prefix_copies(head_dim, rows, true);
+        const int copies = prefix_copies(head_dim, rows);
         return copies == 4   ? launch_verify_tc<128, 2, 2, 0, 1, 64, true, true, 3, 4>(tk, tv, tk64, tv64, p, grid, stream, 284)
                : copies == 2 ? launch_verify_tc<128, 2, 2, 0, 1, 64, true, true, 3, 2>(tk, tv, tk64, tv64, p, grid, stream, 285)
                              : launch_verify_tc<128, 2, 2, 0, 1, 64, true, true, 3>(tk, tv, tk64, tv64, p, grid, stream, 237);
