@@ -396,6 +396,26 @@ def test_many_calls_behind_one_another(splits):
         assert torch.equal(o, want)
 
 
+@BOTH
+@pytest.mark.parametrize("kind", KINDS)
+def test_two_calls_at_once(kind, splits):
+    """Calls on two streams beside each other, each with a workspace of its own."""
+    batches = [Batch(3, [(256, [1, 33, 80]), (1024, [5] * 12)], *HYBRID, 16, kind), Batch(4, [(640, [7, 200, None])], *DENSE, 16, kind)]
+    jobs = []
+    for b in batches:
+        t, desc, shared = b.tensors(), b.desc(), b.shared(prefix_splits=splits)
+        want = b.run(t, desc, shared)
+        jobs.append((b, t, desc, shared, want, torch.empty(pa.shared_workspace_bytes(desc, shared), dtype=torch.uint8, device="cuda"),
+                     [torch.full_like(want, float("nan")) for _ in range(15)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(15):
+        for b, t, desc, shared, _, ws, outs, stream in jobs:
+            b.run(t, desc, shared, workspace=ws, out=outs[i], stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, _, want, _, outs, _ in jobs:
+        assert all(torch.equal(o, want) for o in outs)
+
+
 def test_cache_past_two_to_the_32_bytes():
     pages, bs, hkv, d = 2700, 832, 8, 128  # 4.6 GB each
     b = Batch(1, [(bs * 2, [30, 900]), (bs, [5])], 32, hkv, d, bs)
