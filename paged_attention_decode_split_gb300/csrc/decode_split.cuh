@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(128) pa_split_reduce_rows_kernel(const ReduceP
     for (int e = 0; e < E; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < S; i0 += 32) {
         const float2 v = i0 + lane < S ? ml[i0 + lane] : make_float2(-INFINITY, 0.f);
-        const float w = v.y > 0.f ? fast_exp2(v.x - M) * v.y : 0.f;  // (0: an empty split, its outputs may be anything)
+        const float w = v.y > 0.f ? fast_exp2(v.x - M) * v.y : 0.f;
+        const uint32_t full = __ballot_sync(0xffffffffu, v.y > 0.f);  // an empty split's outputs may be anything
         W += w;
         for (int i1 = 0; i1 < min(32, S - i0); i1 += U) {
             float4 o[U][E];
@@ -409,8 +410,8 @@ __global__ void __launch_bounds__(128) pa_split_reduce_rows_kernel(const ReduceP
                     o[u][e] = *reinterpret_cast<const float4 *>(po + (size_t)min(i0 + i1 + u, S - 1) * D + 128 * e);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float c = __shfl_sync(0xffffffffu, w, i1 + u);  // (0 past the last split)
-                if (c == 0.f) continue;
+                const float c = __shfl_sync(0xffffffffu, w, i1 + u);
+                if ((full >> (i1 + u) & 1) == 0) continue;  // (not by c: a weight of 0 keeps the NaN of what it weighs)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     a[e].x = fmaf(c, o[u][e].x, a[e].x); a[e].y = fmaf(c, o[u][e].y, a[e].y);

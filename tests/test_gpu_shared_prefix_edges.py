@@ -1,0 +1,88 @@
+"""paged_attention_decode_shared where the values, groups and lengths are at
+their edges: NaN beside large logits, starts past the sequences, leaders that
+make no sense.  Tolerances: shared_ref.Batch.reference."""
+import numpy as np
+import pytest
+import torch
+
+import paged_attention_decode_split_gb300 as pa
+from paged_attention_decode_split_gb300 import _build
+from tests import fp4_ref
+from tests.shared_ref import KINDS, Batch, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _build.build()
+    pa.load_library()
+
+
+def status0():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+HYBRID, DENSE = (24, 4, 256), (32, 8, 128)
+
+
+# -- NaN beside large logits -----------------------------------------------------------------------
+
+def only_key(b, slot, logit):
+    """K is zero but for dim 0 of one slot, q but for dim 0: that key's logit is `logit`, the others' are 0."""
+    b.k[...] = 0
+    if b.kind == "bf16":
+        b.k.view(-1, b.hkv, b.d)[slot, :, 0] = 8.0
+        at = np.full(b.hkv, 8.0)
+    elif b.kind == "fp8":
+        b.k.reshape(-1, b.hkv, b.d)[slot, :, 0] = 0x50  # 8
+        at = 8.0 * b.g[0]
+    else:
+        codes, scales = fp4_ref.byte_places("k", slot % 16, b.d)
+        rec = b.k[slot // b.bs, :, slot % b.bs // 16]
+        rec[:, codes[0]], rec[:, scales[0]] = 7, 0x38  # 6 * 1
+        at = 6.0 * b.g[0]
+    b.q[...] = 0
+    grp = b.hq // b.hkv
+    for h in range(b.hkv):
+        b.q[:, h * grp:(h + 1) * grp, 0] = logit / (b.scale * float(at[h]))
+
+
+def spoil(b, which, slot, head):
+    """A NaN in dim 21 of a slot's K or V row (fp4: in its block of 16 dims); returns the dims."""
+    c = (b.k, b.v)[which]
+    if b.kind == "bf16":
+        c.view(-1, b.hkv, b.d)[slot, head, 21] = float("nan")
+    elif b.kind == "fp8":
+        c.reshape(-1, b.hkv, b.d)[slot, head, 21] = 0x7F
+    else:
+        _, scales = fp4_ref.byte_places("kv"[which], slot % 16, b.d)
+        c[slot // b.bs, head, slot % b.bs // 16, scales[1]] = 0x7F
+        return slice(16, 32)
+    return slice(21, 22)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape,out", [(HYBRID, "f32"), (DENSE, "bf16")])
+@pytest.mark.parametrize("n", [3, 14])
+@pytest.mark.parametrize("own_splits,prefix_splits", [(1, 1), (2, 4), (2, 12), (12, 0)])
+def test_nan_far_below_the_largest_logit(kind, shape, out, own_splits, prefix_splits, n):
+    """A NaN whose split's largest logit is so far below the row's that its weight is 0 in binary32 (2^-289) is NaN
+    all the same: by each of the merges, which differ by the numbers of splits and rows (14 x 24: more than two per
+    SM), and for any place of the large logit."""
+    pre = 768
+    for large, low in ((700, 20), (20, 700), (pre + 150, 300), (300, pre + 150)):  # tokens; those past 768 of sequence 2 alone
+        b = Batch(n, [(pre, [180 + i for i in range(n)])], *shape, 16, kind, out)
+        only_key(b, int(b.slots(2)[large]), 200.0)
+        ref, tol = b.reference()
+        g = b.hq // b.hkv
+        who = slice(2, 3) if low >= pre else slice(0, n)
+        bad = np.zeros((b.n, b.hq, b.d), bool)
+        bad[who, g:2 * g] = True                                                 # a NaN key: the whole rows
+        spoil(b, 0, int(b.slots(2)[low]), 1)
+        bad[who, 2 * g:3 * g, spoil(b, 1, int(b.slots(2)[low + 16]), 2)] = True  # a NaN value: its dims
+        got = b.run(desc=b.desc(num_splits=own_splits), shared=b.shared(prefix_splits=prefix_splits)).cpu()
+        assert torch.isnan(got[torch.from_numpy(bad)]).all()
+        check(got[torch.from_numpy(~bad)], ref[~bad], tol[~bad])
