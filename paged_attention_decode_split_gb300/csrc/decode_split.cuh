@@ -285,10 +285,11 @@ __global__ void __launch_bounds__(128) pa_split_reduce_kernel(const ReduceParams
         const bool zero = any_bad || !(Wt > 0.f);
         const float inv = zero ? 0.f : 1.f / Wt;
         const size_t base = r * D + slice * 32 + qd * 4;
-        store_out(p.out, base + 0, at.x * inv, p.out_bf16);
-        store_out(p.out, base + 1, at.y * inv, p.out_bf16);
-        store_out(p.out, base + 2, at.z * inv, p.out_bf16);
-        store_out(p.out, base + 3, at.w * inv, p.out_bf16);
+        // (a poisoned row is zero whatever its other splits hold: not 0 times a NaN)
+        store_out(p.out, base + 0, zero ? 0.f : at.x * inv, p.out_bf16);
+        store_out(p.out, base + 1, zero ? 0.f : at.y * inv, p.out_bf16);
+        store_out(p.out, base + 2, zero ? 0.f : at.z * inv, p.out_bf16);
+        store_out(p.out, base + 3, zero ? 0.f : at.w * inv, p.out_bf16);
     }
 }
 
@@ -356,11 +357,14 @@ __global__ void __launch_bounds__(256, 1) pa_split_reduce_small_kernel(const Red
             }
             M = Mn;
         }
-        const float inv = (bad || !(W > 0.f)) ? 0.f : 1.f / W;
+        const bool zero = bad || !(W > 0.f);
+        const float inv = zero ? 0.f : 1.f / W;
         const size_t base = (size_t)(pair0 + j) * D + 4 * lane;
 #pragma unroll
         for (int e = 0; e < E / 4; ++e)
-            store_out4(p.out, base + 128 * e, make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv),
+            store_out4(p.out, base + 128 * e,
+                       zero ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(a[e].x * inv, a[e].y * inv, a[e].z * inv, a[e].w * inv),
                        p.out_bf16);
     }
 }

@@ -86,3 +86,32 @@ def test_nan_far_below_the_largest_logit(kind, shape, out, own_splits, prefix_sp
         got = b.run(desc=b.desc(num_splits=own_splits), shared=b.shared(prefix_splits=prefix_splits)).cpu()
         assert torch.isnan(got[torch.from_numpy(bad)]).all()
         check(got[torch.from_numpy(~bad)], ref[~bad], tol[~bad])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape,out", [(HYBRID, "f32"), (DENSE, "bf16")])
+@pytest.mark.parametrize("n", [3, 14])
+@pytest.mark.parametrize("own_splits,prefix_splits", [(1, 1), (2, 4), (2, 12), (3, 0), (12, 0)])
+def test_bad_pages_beside_nan(kind, shape, out, own_splits, prefix_splits, n):
+    """A sequence with a bad page is a zero row, also where another of its splits has a NaN."""
+    pre = 768
+    b = Batch(n, [(pre, [180 + i for i in range(n)])], *shape, 16, kind, out)
+    ref, tol = b.reference()
+    g = b.hq // b.hkv
+    bad = np.zeros((b.n, b.hq, b.d), bool)
+    bad[:, g:2 * g, spoil(b, 1, int(b.slots(0)[40]), 1)] = True  # a value of the prefix
+    own = bad.copy()
+    t = b.tensors()
+    t["table"][1, pre // 16 + 3] = 10 ** 6                       # a page of sequence 1's own part
+    ref[1], tol[1], bad[1] = 0, 0, False
+    run = lambda t: b.run(t, desc=b.desc(num_splits=own_splits), shared=b.shared(prefix_splits=prefix_splits), status=status).cpu()  # noqa: E731
+    status = status0()
+    got = run(t)
+    assert torch.isnan(got[torch.from_numpy(bad)]).all()
+    check(got[torch.from_numpy(~bad)], ref[~bad], tol[~bad])
+    assert int(status) == pa.PA_DEV_BAD_PAGE
+    if prefix_splits:  # the prefix itself
+        t = b.tensors()
+        t["table"][0, pre // 16 - 2] = -1
+        check(run(t), np.zeros_like(ref), np.zeros_like(tol))
+    assert own.any()
