@@ -505,7 +505,8 @@ size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc 
  * depend on it NaN, and no others.  fp32 outputs are summed so that they lose
  * about 1e-6 of themselves at any length.  PA_FLAG_EARLY_KV_READ is accepted and
  * changes nothing; a window is refused (PA_ERR_UNSUPPORTED).
- *   group_starts  device int32 [num_groups + 1], 0 .. num_seqs ascending
+ *   group_starts  device int32 [num_groups + 1], 0 .. num_seqs ascending (more than
+ *                 num_seqs counts as num_seqs)
  *   prefix_lens   device int32 [num_seqs]
  *   workspace     device, >= pa_shared_workspace_bytes(desc, prefix) bytes (may
  *                 be NULL if 0)

@@ -159,7 +159,7 @@ __device__ __forceinline__ bool group_ok(const DecodeParams &p, int b, int L, in
         order &= x >= 0 && x <= y;
     }
     lo = __reduce_max_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    hi = min(__reduce_max_sync(0xffffffffu, hi), (int)gridDim.z);  // (a start past the sequences: their number)
     bool ok = __all_sync(0xffffffffu, order) && lo >= 0 && b - lo < p.max_members;
     const bool written = ok;  // by the prefix kernel
     for (int i0 = lo; ok && L != 0 && i0 < hi; i0 += 32) {

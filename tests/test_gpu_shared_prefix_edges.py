@@ -115,3 +115,27 @@ def test_bad_pages_beside_nan(kind, shape, out, own_splits, prefix_splits, n):
         t["table"][0, pre // 16 - 2] = -1
         check(run(t), np.zeros_like(ref), np.zeros_like(tol))
     assert own.any()
+
+
+# -- groups that make no sense ---------------------------------------------------------------------
+
+BOTH = pytest.mark.parametrize("splits", [0, 2], ids=["plain", "shared"])
+
+
+@BOTH
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("end", [7, 37, 2 ** 31 - 1])
+def test_a_start_past_the_sequences(end, kind, splits):
+    """The last group ends with the sequences, whatever its end says; a group past them is empty."""
+    b = Batch(4, [(112, [3, 20, 1, 60]), (32, [5, 9])], *HYBRID, 16, kind)
+    t, status = b.tensors(), status0()
+    t["starts"] = torch.tensor([0, 4, end, end, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    got = b.run(t, shared=b.shared(num_groups=4, max_group_seqs=40, prefix_splits=splits), status=status)
+    check(got, *b.reference())
+    assert int(status) == 0
+    # ... and a sequence there that no one else of its group is in front of
+    t["starts"] = torch.tensor([0, 5, end], dtype=torch.int32, device="cuda")
+    ref, tol = b.reference()
+    ref[4], tol[4] = 0, 0  # (of the first group now, and not with its prefix)
+    check(b.run(t, shared=b.shared(num_groups=2, max_group_seqs=40, prefix_splits=splits), status=status), ref, tol)
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
