@@ -491,14 +491,15 @@ size_t pa_shared_workspace_bytes(const pa_attn_desc *desc, const pa_prefix_desc 
  * their first prefix_lens[b] tokens, rounded down to a multiple of 16: their
  * rows of the block table lead to the same pages for them, or to copies (as
  * pa_fork_block_tables leaves them).  Those tokens are read once per group,
- * through the row of its first sequence that is not idle; where that would save
+ * through the row of its leader, the first sequence that is not idle, has a
+ * length in range and is no shorter than its prefix_lens; where that would save
  * too little (less than 40 MiB of K and V by the description) every sequence
  * reads them through its own row.
  * prefix_lens[b] is the same throughout a group, and at most seq_lens[b]; a group
  * without a common part has 0, and any length serves, also one that ends inside a
  * page.  seq_lens[b] == 0 is an idle sequence: a zero row whatever its
  * prefix_lens says.  A sequence whose length is out of range, or whose prefix_lens
- * is negative, longer than it or not its group's, is PA_DEV_BAD_SEQLEN and a zero
+ * is negative, longer than it or not its leader's, is PA_DEV_BAD_SEQLEN and a zero
  * row, as is one that no group has; group_starts that do not ascend give zero
  * rows throughout (PA_DEV_BAD_SEQLEN).  A bad page of a prefix zeroes the rows of
  * those that read it.  A NaN in q or in a visible key makes the outputs that

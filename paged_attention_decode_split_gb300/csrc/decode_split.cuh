@@ -143,7 +143,7 @@ __device__ __forceinline__ void wait_prefix(bool last_cta) {
 
 // Whether sequence b has a place in a group that makes sense: group_starts
 // ascends, b is among the first max_members of its group, and its prefix is that
-// of the group's first sequence that is not idle.  By one whole warp, for the CTAs
+// of the group's leader.  By one whole warp, for the CTAs
 // of a sequence's first split; otherwise (status set) the records that the prefix
 // kernel may not write are poisoned, so that b's rows become zeros.
 __device__ __forceinline__ bool group_ok(const DecodeParams &p, int b, int L, int hq0, int heads, bool report) {
@@ -163,8 +163,8 @@ __device__ __forceinline__ bool group_ok(const DecodeParams &p, int b, int L, in
     bool ok = __all_sync(0xffffffffu, order) && lo >= 0 && b - lo < p.max_members;
     const bool written = ok;  // by the prefix kernel
     for (int i0 = lo; ok && L != 0 && i0 < hi; i0 += 32) {
-        const int i = i0 + lane, len = i < hi ? p.seq_lens[i] : 0;
-        const uint32_t live = __ballot_sync(0xffffffffu, len > 0 && len <= p.max_seq_len);
+        const int i = i0 + lane, len = i < hi ? p.seq_lens[i] : 0, pre = i < hi ? p.prefix_lens[i] : 0;
+        const uint32_t live = __ballot_sync(0xffffffffu, leads_group(len, pre, p.max_seq_len));
         if (live != 0) {
             ok = p.prefix_lens[i0 + __ffs(live) - 1] == p.prefix_lens[b];
             break;

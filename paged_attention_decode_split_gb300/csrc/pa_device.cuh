@@ -252,4 +252,12 @@ __device__ __forceinline__ void set_status(int32_t *status, int bits) {
     if (status) atomicOr(status, bits);
 }
 
+// Decode over shared prefixes: a group's leader, whose prefix is the group's and
+// whose block table is read for it, is its first sequence with tokens for which
+// this holds.  (One that is shorter than its prefix says is wrong by itself, and
+// does not make the others so.)
+__device__ __forceinline__ bool leads_group(int len, int prefix, int max_seq_len) {
+    return len > 0 && len <= max_seq_len && prefix <= len;
+}
+
 }  // namespace pa

@@ -110,7 +110,7 @@ struct VerifyParams {
     // The common part of a decode over shared prefixes (SH kernels): the rows of
     // a CTA are those of the sequences of group blockIdx.z, one per sequence and
     // head, and see the first prefix_lens tokens, rounded down to whole chunks,
-    // through the table of the group's first sequence that is not idle.
+    // through the table of the group's leader (leads_group).
     const int32_t *prefix_lens;   // [num_seqs]
     const int32_t *group_starts;  // [groups + 1]
     int num_seqs;
@@ -455,17 +455,16 @@ __global__ void __launch_bounds__(VerifyTcCfg<D, NK, NV, NSG, NSB, TK, F4, PT>::
         const int hi = min(max(p.group_starts[g + 1], lo), p.num_seqs);
         row_base = lo;
         members = min(hi - lo, p.max_members);
-        // the first sequence with tokens has the table and the length of the prefix
+        // the group's leader has the table and the length of the prefix
         int first = -1;
         for (int i0 = 0; i0 < members && first < 0; i0 += 32) {
             const int i = i0 + (threadIdx.x & 31);
-            const int len = i < members ? p.seq_lens[lo + i] : 0;
-            const uint32_t there = __ballot_sync(0xffffffffu, len > 0 && len <= p.max_seq_len);
+            const int len = i < members ? p.seq_lens[lo + i] : 0, pre = i < members ? p.prefix_lens[lo + i] : 0;
+            const uint32_t there = __ballot_sync(0xffffffffu, leads_group(len, pre, p.max_seq_len));
             if (there != 0) first = i0 + __ffs(there) - 1;
         }
         b = lo + max(first, 0);
-        if (first >= 0) prefix = p.prefix_lens[b];
-        if (prefix < 0 || (first >= 0 && prefix > p.seq_lens[b])) prefix = 0;  // (that sequence is flagged below)
+        if (first >= 0) prefix = max(0, p.prefix_lens[b]);  // (a sequence with a negative one is flagged below)
         if (row0 == 0 && members < hi - lo) {  // more than the host said: rows without a CTA
             if (threadIdx.x == 0 && split == 0 && kvh == 0) set_status(p.status, PA_DEV_BAD_SEQLEN);
             for (int rho = members * G + threadIdx.x; rho < (hi - lo) * G; rho += C::THREADS)

@@ -139,3 +139,26 @@ def test_a_start_past_the_sequences(end, kind, splits):
     ref[4], tol[4] = 0, 0  # (of the first group now, and not with its prefix)
     check(b.run(t, shared=b.shared(num_groups=2, max_group_seqs=40, prefix_splits=splits), status=status), ref, tol)
     assert int(status) == pa.PA_DEV_BAD_SEQLEN
+
+
+
+
+
+@BOTH
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("change,bad", [
+    (dict(lens={0: 100}), {0}), (dict(lens={0: 1}), {0}), (dict(lens={0: 100, 1: 111}), {0, 1}), (dict(prefix={0: 10 ** 9}), {0}),
+    (dict(lens={0: 0, 1: 50}), {0, 1}), (dict(lens={0: -1, 1: 50}), {0, 1}), (dict(lens={0: 5, 1: 5, 2: 5, 3: 5}), {0, 1, 2, 3}),
+    (dict(lens={4: 31}), {4})])
+def test_a_leader_shorter_than_its_prefix(change, bad, kind, splits):
+    """It is a zero row itself; the others of its group, whose lengths make sense, are computed."""
+    b = Batch(4, [(112, [3, 20, 1, 60]), (32, [5, 9])], *HYBRID, 16, kind)
+    ref, tol = b.reference()
+    ref[list(bad)], tol[list(bad)] = 0, 0
+    t = b.tensors()
+    for name, values in change.items():
+        for i, v in values.items():
+            t[name][i] = v
+    status = status0()
+    check(b.run(t, status=status, prefix_splits=splits), ref, tol)
+    assert int(status) == pa.PA_DEV_BAD_SEQLEN
