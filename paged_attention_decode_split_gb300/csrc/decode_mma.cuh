@@ -254,8 +254,9 @@ __global__ void __launch_bounds__((NST * DS + 1) * 32, SH && NT == 1 ? 2 : 1)
         const bool len_ok = L >= 0 && L <= p.max_seq_len;  // (flagged below)
         const Suffix x = suffix_of(p, b, len_ok ? L : 0);
         own_ok = len_ok && x.ok;
-        cps = x.per;
-        c_begin = x.first + split * cps;
+        // (no further than the sequence: the plan's splits may, for all of max_seq_len, reach past 2^31 tokens)
+        c_begin = min(x.first + split * x.per, x.end);
+        cps = min(x.per, x.end - c_begin);
     }
     if constexpr (WIN) {
         if (L > p.window && L <= p.max_seq_len) c_begin += (L - p.window) / kChunk;

@@ -72,15 +72,16 @@ struct DecodeParams {
 // whether its lengths make sense (an idle sequence, L = 0, has nothing).
 struct Suffix {
     int first;  // chunk
+    int end;    // chunks of the sequence
     int per;    // chunks per split
     bool ok;
 };
 __device__ __forceinline__ Suffix suffix_of(const DecodeParams &p, int b, int L) {
     const int P = p.prefix_lens[b];
-    Suffix s{0, 1, L == 0 || (P >= 0 && P <= L)};
+    Suffix s{0, (L + kChunk - 1) / kChunk, 1, L == 0 || (P >= 0 && P <= L)};
     if (L > 0 && s.ok) {
         s.first = p.prefix_splits > 0 ? P / kChunk : 0;
-        const int n = (L + kChunk - 1) / kChunk - s.first;
+        const int n = s.end - s.first;
         s.per = max(p.suffix_chunks, (n + p.suffix_splits - 1) / p.suffix_splits);
     }
     return s;

@@ -162,3 +162,42 @@ def test_a_leader_shorter_than_its_prefix(change, bad, kind, splits):
     status = status0()
     check(b.run(t, status=status, prefix_splits=splits), ref, tol)
     assert int(status) == pa.PA_DEV_BAD_SEQLEN
+
+
+# -- lengths ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("num_splits", [0, 1])
+def test_a_bound_of_two_to_the_31_tokens(kind, num_splits):
+    """A description for sequences of any length (max_seq_len nearly 2^31, no hints), a prefix of 1.2 million tokens:
+    prefix and planned splits end past token 2^31 together.  Two keys, one of the prefix and one of the own part, have
+    a logit of 30, the others 0: the output is the mean of their values, but for 1.2e6 e^-30 = 1.1e-7 of the others."""
+    bs, width, d, hq, prefix = 2 ** 20, 2047, 128, 4, 1200005
+    dtype = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    k = torch.zeros((2, bs, 1, d), dtype=torch.uint8 if kind == "fp8" else dtype, device="cuda")
+    v = torch.randn((2, bs, 1, d), generator=gen, device="cuda", dtype=torch.bfloat16).to(dtype)
+    a, b = 777777, prefix + 21
+    flat = k.view(dtype).view(2 * bs, d)
+    flat[a, 0] = flat[b, 0] = 8.0
+    q = torch.zeros((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 30 * d ** 0.5 / 8
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.ones((1, width), dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    desc = pa.make_desc(num_seqs=1, num_q_heads=hq, num_kv_heads=1, head_dim=d, block_size=bs, max_pages_per_seq=width,
+                        max_seq_len=width * bs, num_pages=2, scale=d ** -0.5, num_splits=num_splits)
+    shared = pa.make_prefix(num_groups=1, max_group_seqs=1, prefix_splits=8)
+    ws = torch.empty(pa.shared_workspace_bytes(desc, shared), dtype=torch.uint8, device="cuda")
+    out, status = torch.empty((1, hq, d), device="cuda"), status0()
+    args = (table, i32(prefix + 37), i32(0, 1), i32(prefix), desc, shared, out, ws, status)
+    if kind == "bf16":
+        pa.paged_attention_decode_shared(q, k, v, *args)
+    else:
+        one = torch.ones(1, device="cuda")
+        pa.paged_attention_decode_shared_fp8(q, k, v.view(torch.uint8), one, one, *args)
+    rows = v.view(2 * bs, d)
+    want = ((rows[a].double() + rows[b].double()) / 2).cpu()
+    # the two weights are the same number; sums and merges as in shared_ref for what has weight, 64 * 2^-23 of |v| < 6
+    assert (out[0].double().cpu() - want).abs().max() < 6 * (2 * 1.2e-7 + 64 * 2.0 ** -23)
+    assert int(status) == 0
