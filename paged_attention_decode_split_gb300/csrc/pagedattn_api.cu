@@ -1009,7 +1009,8 @@ pa_status shared_call(const void *q, const void *k_cache, const void *v_cache, c
     d.suffix_splits = pl.suffix_splits;
     // (calls without a prefix kernel whose CTAs all start at once have no use for an order)
     d.by_length = desc->num_seqs <= kOrderSeqs &&
-                  (pl.prefix_splits > 0 || pl.suffix_splits * desc->num_kv_heads * desc->num_seqs > pl.num_sms);
+                  (pl.prefix_splits > 0 ||
+                   static_cast<int64_t>(pl.suffix_splits) * desc->num_kv_heads * desc->num_seqs > pl.num_sms);
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 pgrid(pl.prefix_splits, desc->num_kv_heads * pl.row_blocks, prefix->num_groups);
