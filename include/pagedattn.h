@@ -521,7 +521,11 @@ pa_status pa_paged_attention_decode_shared(const void *q, const void *k_cache, c
                                            void *stream);
 
 /* The same over an e4m3 cache (K and V as for pa_paged_attention_decode_fp8) and
- * over an fp4 cache (as for pa_paged_attention_decode_fp4). */
+ * over an fp4 cache (as for pa_paged_attention_decode_fp4).  For bf16 outputs a
+ * softmax weight is rounded to one f16 as it enters the product with V (off by at
+ * most 2^-11 of itself, an eighth of the half step that an output is rounded by):
+ * over an fp4 cache as its decode has it, over an e4m3 cache, whose decode takes
+ * two, where prefixes are shared and only there. */
 pa_status pa_paged_attention_decode_shared_fp8(const void *q, const void *k_cache, const void *v_cache,
                                                const float *k_scale, const float *v_scale,
                                                const int32_t *block_table, const int32_t *seq_lens,

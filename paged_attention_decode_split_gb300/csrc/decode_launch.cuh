@@ -69,7 +69,9 @@ template <bool WIN, bool F8, bool SH = false, int PT = 2, bool FAR = false>
 cudaError_t launch_decode_cfg(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                               const DecodeParams &p, dim3 grid, cudaStream_t stream) {
     // shared-memory limit bookkeeping: one slot per kernel
-    constexpr int slot0 = SH ? 160 + (F8 ? 20 : 0) + (FAR ? 80 : 0) : (WIN ? 20 : 0) + (F8 ? 40 : 0);
+    constexpr int slot0 = !SH                         ? (WIN ? 20 : 0) + (F8 ? 40 : 0)
+                          : F8 && PT == 2 && !FAR ? 296
+                                                  : 160 + (F8 ? 20 : 0) + (FAR ? 80 : 0);
 #define PA_DECODE_CASES(D, NST, SPS, DS, LP, NST2, SPS2, DS2, S0)                                             \
     switch (group) {                                                                                          \
         case 1: return launch_decode_mma_t<D, 1, NST, SPS, DS, WIN, F8, LP, SH, PT, FAR>(tk, tv, p, grid, stream, S0 + 0);  \

@@ -192,9 +192,9 @@ __device__ __forceinline__ void append_new_row(const DecodeParams &p, int b, int
 // half a ring: own parts are short, and one CTA's table, first copies and merge
 // then pass behind the other's copies.
 // PT: the numbers a softmax weight enters the product as: 2 (head and residual),
-// over an e4m3 cache 1 for bf16 outputs (one f16: off by half a step, 2^-11 of
-// itself, an eighth of the half step that the output is rounded by), over a bf16
-// cache 3 for fp32 outputs (two residuals: 2^-26).  FAR: the accumulators, which
+// over an e4m3 cache 1 for bf16 outputs where prefixes are shared (one f16: off by
+// half a step, 2^-11 of itself, an eighth of the half step that the output is rounded
+// by), over a bf16 cache 3 for fp32 outputs (two residuals: 2^-26).  FAR: the accumulators, which
 // the tensor core cuts off towards zero at every addition, 2.4e-9 of the sum per
 // key, are moved to a second sum every kFarChunks chunks of a stream (fp32 outputs;
 // 128 keys: 3e-7).

@@ -61,6 +61,8 @@ cudaError_t launch_decode_fp8_shared(int head_dim, int group, const CUtensorMap 
                                      const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_shared_f32(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                                      const DecodeParams &p, dim3 grid, cudaStream_t stream);
+cudaError_t launch_decode_fp8_shared_alone(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
+                                           const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_fp8_shared_f32(int head_dim, int group, const CUtensorMap &tk, const CUtensorMap &tv,
                                          const DecodeParams &p, dim3 grid, cudaStream_t stream);
 cudaError_t launch_decode_fp4_shared(int head_dim, int group, const DecodeParams &p, dim3 grid, cudaStream_t stream);

@@ -31,7 +31,7 @@ constexpr int kMinPrefixChunks = 8;       // a split of a shared prefix: 128 tok
 // and 26.0 / 38.4 (128).
 constexpr double kMinSharedBytes = 40 << 20;
 constexpr int kMaxDevices = 64;
-constexpr int kKernelSlots = 296;
+constexpr int kKernelSlots = 316;
 
 thread_local pa_plan_info g_last_plan;
 thread_local bool g_have_plan = false;

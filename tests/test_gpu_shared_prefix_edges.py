@@ -201,3 +201,32 @@ def test_a_bound_of_two_to_the_31_tokens(kind, num_splits):
     # the two weights are the same number; sums and merges as in shared_ref for what has weight, 64 * 2^-23 of |v| < 6
     assert (out[0].double().cpu() - want).abs().max() < 6 * (2 * 1.2e-7 + 64 * 2.0 ** -23)
     assert int(status) == 0
+
+
+# -- what the weights lose -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [HYBRID, DENSE, (48, 4, 256), (32, 2, 128)])
+@pytest.mark.parametrize("n,own_splits", [(3, 0), (3, 1), (40, 1)])
+def test_plain_reads_keep_the_decodes_weights(shape, n, own_splits):
+    """bf16 outputs over an e4m3 cache, read without sharing: as exact as the decode that such a call stands for.  All
+    keys but one, whose value is 0, have the same logit and the same value, so what a weight loses as it enters the
+    product does not average out."""
+    b = Batch(n, [(64, [150 + i % 7 for i in range(n)])], *shape, 16, "fp8", "bf16")
+    slot = int(b.slots(0)[20])
+    only_key(b, slot, 4.0)
+    grp = b.hq // b.hkv
+    b.q[:, :, 0] *= torch.linspace(0.7, 1.4, b.n * b.hq).reshape(b.n, b.hq).to(torch.bfloat16)
+    b.v[...] = np.random.default_rng(n).integers(0x20, 0x7F, (b.hkv, b.d))
+    b.v.reshape(-1, b.hkv, b.d)[slot] = 0
+    ref, _ = b.reference()
+    # A logit is one product: exact, then scaled in three roundings of 2^-24 of at most 1.45 * 5.6 log2 units, 1.5e-6
+    # of a weight; exp2 2^-22 and two f16 numbers 2^-22 of it, and of the sum; 250 keys' sums and merges as in
+    # shared_ref, (250 / 16 + 64) * 2^-23.  One f16 would be off by up to 2^-11, 4.9e-4.
+    rel = 2 * (1.5e-6 + 2.0 ** -22 + 2.0 ** -22) + (250 / 16 + 64) * 2.0 ** -23
+    half_step = np.exp2(np.floor(np.log2(np.abs(ref))) - 8)
+    t, desc = b.tensors(), b.desc(num_splits=own_splits)
+    check(b.run(t, desc=desc), ref, half_step + rel * np.abs(ref))
+    assert grp <= 16
+    out, ws = torch.empty_like(t["q"]), torch.empty(max(1, pa.workspace_bytes(desc)), dtype=torch.uint8, device="cuda")
+    pa.paged_attention_decode_fp8(t["q"], *t["caches"], *t["scales"], t["table"], t["lens"], desc, out, ws)
+    check(out, ref, half_step + rel * np.abs(ref))
