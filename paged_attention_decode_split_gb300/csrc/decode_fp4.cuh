@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(NW * 32, 1) pa_decode_fp4_kernel(const DecodeP
     const int32_t *bt = p.block_table + (size_t)b * p.max_pages_per_seq;
     int unused;
     const int lp_first = page_of_chunk(c_begin, unused);
-    const int lp_last = min(page_of_chunk(c_begin + cps - 1, unused), p.max_pages_per_seq - 1);
+    const int c_last = SH ? max(c_begin + cps, 1) - 1 : c_begin + cps - 1;  // (SH: an idle sequence has no chunk)
+    const int lp_last = min(page_of_chunk(c_last, unused), p.max_pages_per_seq - 1);
     const int n_pt = lp_last - lp_first + 1;
     const bool staged = n_pt <= kPageTab;
     if (staged)
